@@ -42,6 +42,11 @@ class ModelWeights(C.Structure):
                 ("fc", C.c_void_p), ("fc_norm", C.c_void_p)]
 
 
+class Kv4CacheStruct(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("k_codes", "k_scales", "v_codes", "v_scales")] + \
+               [(n, C.c_int32) for n in ("n_layers", "b", "Hkv", "hd", "cap", "k_exp", "v_exp")]
+
+
 _lib = None
 
 _SIGS = {
@@ -89,6 +94,19 @@ _SIGS = {
     "dflash_draft_block_workspace_size": (C.c_size_t, [C.c_void_p, C.c_int, C.c_int]),
     "dflash_draft_block": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_void_p, C.c_int] + [C.c_void_p] * 4 +
                            [C.c_int] + [C.c_void_p] * 3 + [C.c_size_t, C.c_void_p]),
+    "dflash_kv4_append_workspace_size": (C.c_size_t, []),
+    "dflash_kv4_append": (C.c_int, [C.c_void_p, C.c_int, C.c_void_p, C.c_void_p, C.c_int] + [C.c_void_p] * 5 +
+                          [C.c_size_t, C.c_void_p]),
+    "dflash_kv4_attention_workspace_size": (C.c_size_t, [C.c_void_p, C.c_int, C.c_int]),
+    "dflash_kv4_attention": (C.c_int, [C.c_void_p, C.c_int, C.c_int, C.c_int] + [C.c_void_p] * 3 + [C.c_float] +
+                             [C.c_void_p] * 3 + [C.c_size_t, C.c_void_p]),
+    "dflash_kv4_attention_weights_workspace_size": (C.c_size_t, [C.c_void_p, C.c_int, C.c_int]),
+    "dflash_kv4_attention_weights": (C.c_int, [C.c_void_p, C.c_int, C.c_int, C.c_int] + [C.c_void_p] * 5 +
+                                     [C.c_int, C.c_float, C.c_float] + [C.c_void_p] * 3 + [C.c_size_t, C.c_void_p]),
+    "dflash_kv4_compact_workspace_size": (C.c_size_t, []),
+    "dflash_kv4_compact": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int] + [C.c_void_p] * 3 + [C.c_size_t, C.c_void_p]),
+    "dflash_kv4_evict_workspace_size": (C.c_size_t, [C.c_void_p, C.c_int]),
+    "dflash_kv4_evict": (C.c_int, [C.c_void_p] * 3 + [C.c_int] * 3 + [C.c_void_p] * 5 + [C.c_size_t, C.c_void_p]),
 }
 
 
@@ -233,11 +251,13 @@ def accept_and_compact_workspace_size(b, n_tree):
     return load().accept_and_compact_workspace_size(b, n_tree)
 
 
-def accept_and_compact(choice, tok, parent, k_cache, v_cache, cache_len, tree_feat, new_feat, out, ws: Workspace):
-    """k_cache [L][b][Hkv][cap][hd], v_cache [L][b][Hkv][hd][cap]; out: n_new, acc_tok, n_acc, new_bonus, src_slot."""
+def accept_and_compact(choice, tok, parent, k_cache, v_cache, cache_len, tree_feat, new_feat, out, ws: Workspace,
+                       cap=None):
+    """k_cache [L][b][Hkv][cap][hd], v_cache [L][b][Hkv][hd][cap]; out: n_new, acc_tok, n_acc, new_bonus, src_slot.
+    k_cache, v_cache None: the walk alone; cap is then the slots of the cache that kv4_compact moves."""
     b, T = choice.shape
     nl, Hkv, cap, hd = (k_cache.shape[0], k_cache.shape[2], k_cache.shape[3], k_cache.shape[4]) \
-        if k_cache is not None else (0, 1, 1, 128)
+        if k_cache is not None else (0, 1, 1 if cap is None else cap, 128)
     max_new = out["acc_tok"].shape[1]
     feat_dim = tree_feat.shape[-1] if tree_feat is not None else 0
     _check("accept_and_compact", load().accept_and_compact(
@@ -341,6 +361,137 @@ def linear_logsoftmax(X, W, out, ws: Workspace = None):
     _check("dflash_linear_logsoftmax", load().dflash_linear_logsoftmax(_p(X), _p(W), M, N, K, _p(out), ws.ptr,
                                                                        ws.nbytes, _stream()))
     return ws
+
+
+# ------------------------------------------------------------------- KV cache held in 4 bits
+class Kv4Cache:
+    """A KV cache held in 4 bits (df_kv4_cache): four uint8 tensors and two exponents.
+
+    k_codes, v_codes [n_layers][b][Hkv][cap][64]; k_scales, v_scales [n_layers][b][Hkv][cap][8];
+    a value is 2^exp * scale (e4m3) * code (e2m1), one scale for 16 values."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, k_exp=0, v_exp=0):
+        if k_codes.dim() != 5 or k_codes.shape[4] != 64:
+            raise ValueError("k_codes must be [n_layers][b][Hkv][cap][64]")
+        rows = k_codes.shape[:4]
+        for t, last, name in ((k_codes, 64, "k_codes"), (k_scales, 8, "k_scales"), (v_codes, 64, "v_codes"),
+                              (v_scales, 8, "v_scales")):
+            _dev(t, torch.uint8, name)
+            if t.device != k_codes.device or tuple(t.shape) != (*rows, last):
+                raise ValueError(f"{name} must be [n_layers][b][Hkv][cap][{last}] on {k_codes.device}")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.n_layers, self.b, self.n_kv_heads, self.cap = rows
+        self.k_exp, self.v_exp = int(k_exp), int(v_exp)
+        self.device = k_codes.device
+        self.rows = tuple(rows)
+        self.struct = Kv4CacheStruct(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+                                     *rows[:3], 128, rows[3], self.k_exp, self.v_exp)
+        self.ref = C.addressof(self.struct)
+
+    @classmethod
+    def empty(cls, n_layers, b, n_kv_heads, cap, k_exp=0, v_exp=0, device="cuda"):
+        z = lambda last: torch.zeros(n_layers, b, n_kv_heads, cap, last, dtype=torch.uint8, device=device)
+        return cls(z(64), z(8), z(64), z(8), k_exp, v_exp)
+
+    def _arg(self, t, dtype, shape, name):
+        """Address of an argument that lies on the cache's device (None: 0)."""
+        if t is None:
+            return 0
+        if t.dtype != dtype or t.device != self.device or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on {self.device}")
+        return t.data_ptr()
+
+    def _ws(self, ws):
+        """A call's workspace and stream: the current stream of the current device, which has to be the cache's."""
+        dev = self.device.index
+        if torch.cuda.current_device() != dev or ws.buf.device != self.device:
+            raise ValueError(f"the current device and the workspace's have to be the cache's ({self.device})")
+        return ws.buf.data_ptr(), ws.nbytes, torch.cuda.current_stream(dev).cuda_stream
+
+
+def kv4_append_workspace_size():
+    return load().dflash_kv4_append_workspace_size()
+
+
+def kv4_append(cache: Kv4Cache, layer, k, v, cache_len, ws: Workspace, n_new=None, k_held=None, v_held=None):
+    """Rounds k, v [b][n][Hkv][128] bf16 into slots cache_len[s] .. of one layer (n_new [b]: rows per sequence);
+    k_held, v_held (optional, like k) take the values that the cache then stands for."""
+    b, n = cache.b, k.shape[1]
+    shape = (b, n, cache.n_kv_heads, 128)
+    arg, bf, i32 = cache._arg, torch.bfloat16, torch.int32
+    _check("dflash_kv4_append", load().dflash_kv4_append(
+        cache.ref, layer, arg(k, bf, shape, "k"), arg(v, bf, shape, "v"), n, arg(n_new, i32, (b,), "n_new"),
+        arg(cache_len, i32, (b,), "cache_len"), arg(k_held, bf, shape, "k_held"), arg(v_held, bf, shape, "v_held"),
+        *cache._ws(ws)))
+
+
+def kv4_attention_workspace_size(cache: Kv4Cache, n_tree, Hq):
+    return load().dflash_kv4_attention_workspace_size(cache.ref, n_tree, Hq)
+
+
+def kv4_attention(cache: Kv4Cache, layer, q, cache_len, anc, scale, out, ws: Workspace, lse=None):
+    """Tree attention over one layer of the cache; q, out [b][T][Hq][128] bf16, anc [b][T][ceil(T/32)] int32 or
+    None (a chain), lse (optional) [b][T][Hq] fp32."""
+    b, T, Hq, _ = shape = tuple(q.shape)
+    arg, bf, i32 = cache._arg, torch.bfloat16, torch.int32
+    if b != cache.b or shape[3] != 128:
+        raise ValueError(f"q must be [{cache.b}][T][Hq][128]")
+    _check("dflash_kv4_attention", load().dflash_kv4_attention(
+        cache.ref, layer, T, Hq, arg(q, bf, shape, "q"), arg(cache_len, i32, (b,), "cache_len"),
+        arg(anc, i32, (b, T, (T + 31) // 32), "anc"), scale, arg(out, bf, shape, "out"),
+        arg(lse, torch.float32, shape[:3], "lse"), *cache._ws(ws)))
+
+
+def kv4_attention_weights_workspace_size(cache: Kv4Cache, n_tree, Hq):
+    return load().dflash_kv4_attention_weights_workspace_size(cache.ref, n_tree, Hq)
+
+
+def kv4_attention_weights(cache: Kv4Cache, layer, q, lse, cache_len, scale, score, ws: Workspace, n_rows=None,
+                          src_slot=None, decay=1.0, score_out=None):
+    """score_out = decay * score + the attention weight of the rows that stayed (see dflash.h); score and score_out
+    [n_layers][b][Hkv][cap] fp32, score_out None: in place.  n_rows and src_slot are accept_and_compact's n_new and
+    src_slot, cache_len its new length."""
+    b, T, Hq, _ = shape = tuple(q.shape)
+    arg, i32, f32 = cache._arg, torch.int32, torch.float32
+    if b != cache.b or shape[3] != 128:
+        raise ValueError(f"q must be [{cache.b}][T][Hq][128]")
+    max_src = 0 if src_slot is None else src_slot.shape[1]
+    sc = arg(score, f32, cache.rows, "score")
+    _check("dflash_kv4_attention_weights", load().dflash_kv4_attention_weights(
+        cache.ref, layer, T, Hq, arg(q, torch.bfloat16, shape, "q"), arg(lse, f32, shape[:3], "lse"),
+        arg(cache_len, i32, (b,), "cache_len"), arg(n_rows, i32, (b,), "n_rows"),
+        arg(src_slot, i32, (b, max_src), "src_slot"), max_src, scale, decay, sc,
+        sc if score_out is None else arg(score_out, f32, cache.rows, "score_out"), *cache._ws(ws)))
+
+
+def kv4_compact_workspace_size():
+    return load().dflash_kv4_compact_workspace_size()
+
+
+def kv4_compact(cache: Kv4Cache, src_slot, n_acc, cache_len, ws: Workspace):
+    """Moves the accepted path's rows in every layer; src_slot [b][max], n_acc, cache_len as accept_and_compact
+    left them."""
+    b, i32, max_src = cache.b, torch.int32, src_slot.shape[1]
+    _check("dflash_kv4_compact", load().dflash_kv4_compact(
+        cache.ref, cache._arg(src_slot, i32, (b, max_src), "src_slot"), max_src, cache._arg(n_acc, i32, (b,), "n_acc"),
+        cache._arg(cache_len, i32, (b,), "cache_len"), *cache._ws(ws)))
+
+
+def kv4_evict_workspace_size(cache: Kv4Cache, budget):
+    return load().dflash_kv4_evict_workspace_size(cache.ref, budget)
+
+
+def kv4_evict(cache: Kv4Cache, score, cache_len, budget, n_sink, n_recent, to: Kv4Cache, score_out, new_len, kept,
+              ws: Workspace):
+    """Copies the slots that stay (n_sink first, n_recent last, then the largest scores) to another cache; kept
+    [n_layers][b][Hkv][budget] int32 lists them, new_len [b] may be cache_len; score_out may be None."""
+    arg, i32, f32 = cache._arg, torch.int32, torch.float32
+    if to.device != cache.device:
+        raise ValueError("both caches have to lie on one device")
+    _check("dflash_kv4_evict", load().dflash_kv4_evict(
+        cache.ref, arg(score, f32, cache.rows, "score"), arg(cache_len, i32, (cache.b,), "cache_len"), budget, n_sink,
+        n_recent, to.ref, arg(score_out, f32, to.rows, "score_out"), arg(new_len, i32, (cache.b,), "new_len"),
+        arg(kept, i32, (*cache.rows[:3], budget), "kept"), *cache._ws(ws)))
 
 
 def plant_logprobs(logprobs, ref, pos, rate, bias, seed, miss_bias=0.0):

@@ -12,6 +12,7 @@
 #include "layers.h"
 #include "moe.h"
 #include "nvtx.h"
+#include "workspace.h"
 
 namespace df {
 int launch_ddtree(const float* lp, int b, int D, int V, int B, const int32_t* root_tok, int32_t* tok,
@@ -29,31 +30,6 @@ int launch_accept(int b, int n_tree, const int32_t* choice, const int32_t* tok, 
                   int* status, cudaStream_t st);
 
 namespace {
-
-constexpr size_t kAlign = 256;
-inline size_t up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
-
-// Bump allocator over a caller-provided workspace (or a size counter when base is null).
-struct Carver {
-  unsigned char* base;
-  size_t off = kAlign;  // the first 256 bytes hold the status header
-  explicit Carver(void* b) : base(static_cast<unsigned char*>(b)) {}
-  template <class T>
-  T* take(size_t count) {
-    T* p = base ? reinterpret_cast<T*>(base + off) : nullptr;
-    off = up(off + count * sizeof(T));
-    return p;
-  }
-};
-
-inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-inline int* status_of(void* ws) { return reinterpret_cast<int*>(ws); }
-
-#define DF_TRY(x)            \
-  do {                       \
-    int _rc = (x);           \
-    if (_rc != DF_OK) return _rc; \
-  } while (0)
 
 // Router GEMM (E <= 256 weight rows): each CTA takes at least this many k-steps.
 constexpr int kRouterMinK = 4;

@@ -1,0 +1,627 @@
+// Attention over a KV cache held in 4 bits, for few query rows per kv head, and the attention
+// weight that given rows lay on every slot.
+//
+// Row (s, i, h) sees slots [0, N) and the tree slots N + j of its ancestors, N = cache_len[s]:
+//   out = softmax(scale q K^T) V,  lse = log of the softmax's sum
+// with K, V the values that the cache's codes and scales stand for (kv4.cuh: fp16 numbers, so
+// the fp16 tensor-core products are exact; sums, softmax statistics and outputs are fp32).
+//
+// What bounds it with few rows is the cache, 144 bytes a slot and kv head.  A work item is a
+// stage of 32 slots of one (sequence, kv head); all stages of a call are laid out in one line,
+// which the CTAs cut into equal shares whatever the sequences' lengths.  In a CTA every warp
+// streams stages of its own (bulk copies into a ring of its own, no CTA barrier), decodes codes
+// straight into tensor-core fragments and keeps its own running maximum, sum and output; the
+// warps are merged when the share, or the (sequence, kv head), ends.
+#include <math.h>
+
+#include "kv4.cuh"
+#include "kv4.h"
+#include "runtime.h"
+#include "trace.h"
+
+namespace df {
+
+constexpr int kWarps = 8;
+constexpr int kStageKeys = 32;
+constexpr int kStages = 2;
+constexpr int kStageBytes = kStageKeys * 2 * (kKv4Codes + kKv4Scales);   // K codes, V codes, K scales, V scales
+constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+// Probabilities are scaled by 2^12 before they are rounded to fp16: what lies 2^26 below the
+// row's largest still has all its bits.
+constexpr float kPShift = 12.f;
+
+struct Kv4AttnParams {
+  Kv4Planes p;
+  int b, T, Hq, Hkv, G, cap, W;
+  const df_bf16* q;
+  const int32_t* cache_len;
+  const uint32_t* anc;
+  float scale2;          // scale * log2(e) * 2^k_exp
+  float v_mul;           // 2^v_exp
+  df_bf16* out;
+  float* lse;
+  float* o_part;         // [slots][16 MT][128]
+  float2* ml_part;       // [slots][16 MT]
+  int n_cta, nrt;        // CTAs of the grid, row tiles of a (sequence, kv head)
+  int* status;
+};
+
+// Shares: stage t of all `total` stages belongs to the CTA c with first(c) <= t < first(c + 1).
+struct Shares {
+  long long total;
+  int n;   // CTAs that get a share: none gets fewer than kWarps stages, while there are several
+  DF_DEV long long first(int c) const { return total * c / n; }
+  DF_DEV int owner(long long t) const { return (int)(((t + 1) * n - 1) / total); }
+};
+
+DF_DEV int seq_stages(const Kv4AttnParams& p, int s) {   // per unit; a sequence that shows nothing has one
+  const int n = p.cache_len[s];
+  const int len = n >= 0 && n <= p.cap - p.T ? n + p.T : 0;
+  return max(1, (len + kStageKeys - 1) / kStageKeys);
+}
+DF_DEV long long warp_sum_ll(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// Stages of sequences [0, s1), a whole warp.
+DF_DEV long long stages_before(const Kv4AttnParams& p, int s1, int lane) {
+  long long v = 0;
+  for (int s = lane; s < s1; s += 32) v += seq_stages(p, s);
+  return warp_sum_ll(v) * p.Hkv * p.nrt;
+}
+DF_DEV Shares make_shares(const Kv4AttnParams& p, int lane) {
+  Shares sh;
+  sh.total = stages_before(p, p.b, lane);
+  const long long most = (sh.total + kWarps - 1) / kWarps;
+  sh.n = most < p.n_cta ? (int)most : p.n_cta;
+  return sh;
+}
+
+// Ancestor (or causal) visibility of tree slot t for node i.
+DF_DEV bool tree_sees(const uint32_t* anc_row, int node, int t) {
+  return anc_row ? (anc_row[t >> 5] >> (t & 31)) & 1u : t <= node;
+}
+
+template <int MT>   // row tiles of 16 per warp
+__global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 2 : 1) kv4_attn_kernel(const Kv4AttnParams p) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  constexpr int R = 16 * MT;
+  __shared__ __align__(8) uint64_t bars[kWarps][kStages];
+  __shared__ float2 ml[kWarps][R];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) mbar_init(&bars[warp][i], 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  unsigned char* ring = smem + warp * kStages * kStageBytes;
+  pdl_wait();
+  pdl_trigger();
+  const Shares sh = make_shares(p, lane);
+  if ((int)blockIdx.x >= sh.n) return;
+  const long long t1 = sh.first(blockIdx.x + 1);
+  long long t = sh.first(blockIdx.x);
+  // the sequence that stage t lies in
+  int s = 0;
+  long long seq0 = 0;   // its first stage
+  const int per_seq = p.Hkv * p.nrt;
+  for (int base = 0; base < p.b; base += 32) {
+    const long long mine = base + lane < p.b ? (long long)seq_stages(p, base + lane) * per_seq : 0;
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, seq0 + inc <= t && base + lane < p.b);
+    const int k = __popc(past);   // whole sequences before t
+    s += k;
+    if (k > 0) seq0 += __shfl_sync(0xffffffffu, inc, k - 1);
+    if (k < 32) break;
+  }
+  uint32_t uses = 0;   // stages this warp has loaded so far, modulo 2^32: slot uses % kStages
+  bool ok = true;
+  while (t < t1) {
+    const int per_unit = seq_stages(p, s);
+    const int unit = (int)((t - seq0) / per_unit), tile0 = (int)((t - seq0) % per_unit);
+    const int count = (int)min(t1 - t, (long long)(per_unit - tile0));
+    const int kvh = unit / p.nrt, rt = unit % p.nrt;
+    const int N = p.cache_len[s];
+    const bool fits = N >= 0 && N <= p.cap - p.T;
+    if (!fits && tid == 0) set_status(p.status, DF_ERR_CAPACITY, s);
+    const int len = fits ? N + p.T : 0;
+    const size_t plane = ((size_t)s * p.Hkv + kvh) * p.cap;
+    const int rows = min(R, p.T * p.G - rt * R);   // live rows of the tile
+    const uint8_t *kc = p.p.kc + plane * kKv4Codes, *vc = p.p.vc + plane * kKv4Codes;
+    const uint8_t *ks = p.p.ks + plane * kKv4Scales, *vs = p.p.vs + plane * kKv4Scales;
+    auto issue = [&](int i, uint32_t slot) {   // this warp's i-th stage of the segment
+      if (lane == 0) {
+        unsigned char* st = ring + slot * kStageBytes;
+        uint64_t* bar = &bars[warp][slot];
+        const int key0 = (tile0 + warp + i * kWarps) * kStageKeys;
+        const uint32_t n = min(kStageKeys, p.cap - key0);   // a multiple of 8
+        mbar_arrive_expect_tx(bar, n * 2 * (kKv4Codes + kKv4Scales));
+        bulk_load(st, kc + (size_t)key0 * kKv4Codes, n * kKv4Codes, bar);
+        bulk_load(st + 2 * kStageKeys * kKv4Codes, ks + (size_t)key0 * kKv4Scales, n * kKv4Scales, bar);
+        bulk_load(st + kStageKeys * kKv4Codes, vc + (size_t)key0 * kKv4Codes, n * kKv4Codes, bar);
+        bulk_load(st + kStageKeys * (2 * kKv4Codes + kKv4Scales), vs + (size_t)key0 * kKv4Scales, n * kKv4Scales, bar);
+      }
+    };
+    const int mine = count > warp ? (count - warp + kWarps - 1) / kWarps : 0;
+    for (int i = 0; i < kStages && i < mine; ++i) issue(i, (uses + i) % kStages);
+    // Q fragments.  The products run over dimensions in the order in which a lane finds its
+    // codes: lane t4 of a quad takes dimensions 32 t4 .. 32 t4 + 31, four at a step.
+    uint32_t qf[MT][8][4];
+    float qs[MT][2];   // raw score -> log2 units
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int r = rt * R + m * 16 + half * 8 + g;
+        uint4 raw[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) raw[c] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < p.T * p.G) {
+          const df_bf16* src = p.q + (((size_t)s * p.T + r / p.G) * p.Hq + kvh * p.G + r % p.G) * 128 + t4 * 32;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) raw[c] = reinterpret_cast<const uint4*>(src)[c];
+        }
+        float amax = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        float back;
+        const float f = f16_row_factor(amax, back);
+        qs[m][half] = p.scale2 * back;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            qf[m][2 * c + (e >> 1)][(e & 1) * 2 + half] =
+                pack_f16x2(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xFFFF0000u) * f);
+        }
+      }
+    }
+    float o[MT][16][4], mx[MT][2], l[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) o[m][j][0] = o[m][j][1] = o[m][j][2] = o[m][j][3] = 0.f;
+      mx[m][0] = mx[m][1] = -INFINITY;
+      l[m][0] = l[m][1] = 0.f;
+    }
+    for (int i = 0; i < mine; ++i) {
+      const uint32_t slot = uses % kStages;
+      ok = ok && mbar_wait(&bars[warp][slot], (uses / kStages) & 1, p.status, 50);
+      ok = __all_sync(0xffffffffu, ok);
+      const unsigned char* st = ring + slot * kStageBytes;
+      const unsigned char *skc = st, *svc = st + kStageKeys * kKv4Codes;
+      const unsigned char *sks = st + 2 * kStageKeys * kKv4Codes, *svs = sks + kStageKeys * kKv4Scales;
+      const int key0 = (tile0 + warp + i * kWarps) * kStageKeys;
+      // S: four tiles of 8 keys.  Key of tile q, column n: 16 (q/2) + 8 (q%2) + 4 (n%2) + n/2, so
+      // that lane t4's probabilities belong to keys t4 + 4i, whose value rows it decodes below.
+      float sc[MT][4][4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) sc[m][q][0] = sc[m][q][1] = sc[m][q][2] = sc[m][q][3] = 0.f;
+        const int key = q * 8 + (g & 1) * 4 + (g >> 1);
+        const uint4 c = *reinterpret_cast<const uint4*>(skc + key * kKv4Codes + t4 * 16);
+        const uint32_t two = *reinterpret_cast<const uint16_t*>(sks + key * kKv4Scales + t4 * 2);
+        const uint32_t s0 = e4m3x2_to_f16((two & 0xFFu) * 0x00010001u), s1 = e4m3x2_to_f16((two >> 8) * 0x00010001u);
+        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t f[4];
+          e2m1x8_to_f16(w[e], f);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) f[x] = hmul2(f[x], e < 2 ? s0 : s1);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            mma_f16_16816(sc[m][q], qf[m][2 * e], f[0], f[1]);
+            mma_f16_16816(sc[m][q], qf[m][2 * e + 1], f[2], f[3]);
+          }
+        }
+      }
+      // log2 units, mask, running maximum
+      const bool edge = key0 + kStageKeys > N || !fits;
+      uint32_t pf[MT][2][4];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        float mt[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float x = sc[m][q][e] * qs[m][e >> 1];
+            if (edge) {
+              const int r = rt * R + m * 16 + (e >> 1) * 8 + g;
+              const int node = r / p.G;
+              const int key = key0 + q * 8 + (e & 1) * 4 + t4;
+              bool see = key < len && r < p.T * p.G;
+              if (see && key >= N)
+                see = tree_sees(p.anc ? p.anc + ((size_t)s * p.T + node) * p.W : nullptr, node, key - N);
+              if (!see) x = -INFINITY;
+            }
+            sc[m][q][e] = x;
+            mt[e >> 1] = fmaxf(mt[e >> 1], x);
+          }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          mt[half] = fmaxf(mt[half], __shfl_xor_sync(0xffffffffu, mt[half], 1));
+          mt[half] = fmaxf(mt[half], __shfl_xor_sync(0xffffffffu, mt[half], 2));
+          mt[half] = fmaxf(mt[half], mx[m][half]);
+        }
+        if (__any_sync(0xffffffffu, mt[0] > mx[m][0] || mt[1] > mx[m][1])) {
+          const float a0 = mx[m][0] == -INFINITY ? 0.f : ex2_approx(mx[m][0] - mt[0]);
+          const float a1 = mx[m][1] == -INFINITY ? 0.f : ex2_approx(mx[m][1] - mt[1]);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) { o[m][j][0] *= a0; o[m][j][1] *= a0; o[m][j][2] *= a1; o[m][j][3] *= a1; }
+          l[m][0] *= a0;
+          l[m][1] *= a1;
+          mx[m][0] = mt[0];
+          mx[m][1] = mt[1];
+        }
+        // a row that has seen nothing yet: every x is -inf, and 2^(-inf - 0) = 0
+        const float b0 = kPShift - (mt[0] == -INFINITY ? 0.f : mt[0]), b1 = kPShift - (mt[1] == -INFINITY ? 0.f : mt[1]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float p0 = ex2_approx(sc[m][q][0] + b0), p1 = ex2_approx(sc[m][q][1] + b0);
+          const float p2 = ex2_approx(sc[m][q][2] + b1), p3 = ex2_approx(sc[m][q][3] + b1);
+          l[m][0] += p0 + p1;
+          l[m][1] += p2 + p3;
+          pf[m][q >> 1][(q & 1) * 2] = pack_f16x2(p0, p1);
+          pf[m][q >> 1][(q & 1) * 2 + 1] = pack_f16x2(p2, p3);
+        }
+      }
+      // O: lane g of the column takes dimensions 16 g .. 16 g + 15 (one scale a key), tile j of
+      // 8 columns the j-th of them.  Two keys' codes are merged nibble by nibble, so that one
+      // conversion gives the pair of keys that a fragment register holds.
+#pragma unroll
+      for (int k2 = 0; k2 < 2; ++k2) {
+        uint2 c[4];
+        uint32_t sb[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = k2 * 16 + e * 4 + t4;
+          c[e] = *reinterpret_cast<const uint2*>(svc + key * kKv4Codes + g * 8);
+          sb[e] = svs[key * kKv4Scales + g];
+        }
+        const uint32_t s01 = e4m3x2_to_f16(sb[0] | (sb[1] << 16)), s23 = e4m3x2_to_f16(sb[2] | (sb[3] << 16));
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const uint32_t c0 = w ? c[0].y : c[0].x, c1 = w ? c[1].y : c[1].x, c2 = w ? c[2].y : c[2].x, c3 = w ? c[3].y : c[3].x;
+          uint32_t e01[4], o01[4], e23[4], o23[4];
+          e2m1x8_to_f16((c0 & 0x0F0F0F0Fu) | ((c1 & 0x0F0F0F0Fu) << 4), e01);
+          e2m1x8_to_f16(((c0 >> 4) & 0x0F0F0F0Fu) | (c1 & 0xF0F0F0F0u), o01);
+          e2m1x8_to_f16((c2 & 0x0F0F0F0Fu) | ((c3 & 0x0F0F0F0Fu) << 4), e23);
+          e2m1x8_to_f16(((c2 >> 4) & 0x0F0F0F0Fu) | (c3 & 0xF0F0F0F0u), o23);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t be0 = hmul2(e01[x], s01), be1 = hmul2(e23[x], s23);
+            const uint32_t bo0 = hmul2(o01[x], s01), bo1 = hmul2(o23[x], s23);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              mma_f16_16816(o[m][8 * w + 2 * x], pf[m][k2], be0, be1);
+              mma_f16_16816(o[m][8 * w + 2 * x + 1], pf[m][k2], bo0, bo1);
+            }
+          }
+        }
+      }
+      __syncwarp();   // every lane has read the stage
+      if (ok && i + kStages < mine) issue(i + kStages, slot);
+      ++uses;
+    }
+    // ---------------------------------------------------------------- merge the warps
+    __syncthreads();   // every ring is read, every copy of the segment has landed
+    float* so = reinterpret_cast<float*>(smem) + warp * R * 128;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        l[m][half] += __shfl_xor_sync(0xffffffffu, l[m][half], 1);
+        l[m][half] += __shfl_xor_sync(0xffffffffu, l[m][half], 2);
+        const int r = m * 16 + half * 8 + g;
+        if (t4 == 0) ml[warp][r] = make_float2(mx[m][half], l[m][half]);
+        float* dst = so + r * 128 + t4 * 32;
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          *reinterpret_cast<float4*>(dst + j) = make_float4(o[m][j][half * 2], o[m][j + 1][half * 2], o[m][j + 2][half * 2], o[m][j + 3][half * 2]);
+          *reinterpret_cast<float4*>(dst + 16 + j) = make_float4(o[m][j][half * 2 + 1], o[m][j + 1][half * 2 + 1], o[m][j + 2][half * 2 + 1], o[m][j + 3][half * 2 + 1]);
+        }
+      }
+    }
+    __syncthreads();
+    const int u_glob = s * per_seq + unit;
+    const bool whole = count == per_unit;
+    for (int x = tid; x < rows * 32; x += kWarps * 32) {   // four dimensions of one row
+      const int r = x >> 5, d = (x & 31) * 4;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w][r].x);
+      float L = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 v = ml[w][r];
+        const float f = v.x == -INFINITY ? 0.f : ex2_approx(v.x - M);
+        const float4 ov = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem) + (w * R + r) * 128 + d);
+        L += f * v.y;
+        acc.x += f * ov.x; acc.y += f * ov.y; acc.z += f * ov.z; acc.w += f * ov.w;
+      }
+      if (whole) {
+        const int row = rt * R + r;
+        const size_t grow = ((size_t)s * p.T + row / p.G) * p.Hq + kvh * p.G + row % p.G;
+        const float inv = L > 0.f ? p.v_mul / L : 0.f;
+        uint2 w2;
+        w2.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+        w2.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2*>(p.out + grow * 128 + d) = w2;
+        if (p.lse && d == 0) p.lse[grow] = L > 0.f ? (M - kPShift + log2f(L)) * 0.6931471805599453f : -INFINITY;
+      } else {
+        const size_t at = (size_t)(blockIdx.x + u_glob) * R + r;
+        *reinterpret_cast<float4*>(p.o_part + at * 128 + d) = acc;
+        if (d == 0) p.ml_part[at] = make_float2(M, L);
+      }
+    }
+    fence_proxy_async();   // the rings were written by ordinary stores: order them before the next copies
+    __syncthreads();
+    t += count;
+    if (tile0 + count == per_unit && unit + 1 == per_seq) {
+      seq0 += (long long)per_unit * per_seq;
+      ++s;
+    }
+  }
+}
+
+// One warp per query row whose (sequence, kv head) was cut: the shares' partial results in
+// the order of the shares.
+__global__ void __launch_bounds__(256) kv4_combine_kernel(const Kv4AttnParams p, int R) {
+  pdl_wait();
+  pdl_trigger();
+  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= (long long)p.b * p.T * p.Hq) return;
+  const int head = (int)(row % p.Hq), node = (int)(row / p.Hq % p.T), s = (int)(row / p.Hq / p.T);
+  const int kvh = head / p.G, r = node * p.G + head % p.G;
+  const Shares sh = make_shares(p, lane);
+  const int per_unit = seq_stages(p, s), per_seq = p.Hkv * p.nrt;
+  const int unit = kvh * p.nrt + r / R;
+  const long long a0 = stages_before(p, s, lane) + (long long)unit * per_unit;
+  const int c0 = sh.owner(a0), c1 = sh.owner(a0 + per_unit - 1);
+  if (c0 == c1) return;
+  const size_t slot0 = (size_t)s * per_seq + unit, rr = r % R;
+  float M = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.ml_part[(slot0 + c) * R + rr].x);
+  M = warp_max(M);
+  float L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const size_t at = (slot0 + c) * R + rr;
+    const float2 v = p.ml_part[at];
+    const float4 o = reinterpret_cast<const float4*>(p.o_part + at * 128)[lane];
+    const float f = v.x == -INFINITY ? 0.f : ex2_approx(v.x - M);
+    L += f * v.y;
+    acc.x += f * o.x; acc.y += f * o.y; acc.z += f * o.z; acc.w += f * o.w;
+  }
+  const float inv = L > 0.f ? p.v_mul / L : 0.f;
+  uint2 w2;
+  w2.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+  w2.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+  reinterpret_cast<uint2*>(p.out + row * 128)[lane] = w2;
+  if (p.lse && lane == 0) p.lse[row] = L > 0.f ? (M - kPShift + log2f(L)) * 0.6931471805599453f : -INFINITY;
+}
+
+// ------------------------------------------------------------------------------- host
+static int rows_per_tile(int T, int G) { return T * G <= 16 ? 16 : 32; }
+static int few_rows_ctas(int R) { return num_sms() * (R == 16 ? 2 : 1); }
+
+size_t kv4_attn_scratch_bytes(int b, int T, int Hq, int Hkv, int cap) {
+  (void)cap;
+  const int G = Hq / Hkv, R = rows_per_tile(T, G);
+  const size_t slots = (size_t)few_rows_ctas(R) + (size_t)b * Hkv * ((T * G + R - 1) / R);
+  return slots * R * (128 * 4 + 8) + 256;
+}
+
+int launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t st) {
+  Kv4AttnParams p{};
+  p.p = a.p;
+  p.b = a.b; p.T = a.T; p.Hq = a.Hq; p.Hkv = a.Hkv; p.G = a.Hq / a.Hkv; p.cap = a.cap; p.W = (a.T + 31) / 32;
+  p.q = a.q; p.cache_len = a.cache_len; p.anc = a.anc;
+  p.scale2 = ldexpf(a.scale * 1.4426950408889634f, a.k_exp);
+  p.v_mul = ldexpf(1.f, a.v_exp);
+  p.out = a.out; p.lse = a.lse; p.status = a.status;
+  const int R = rows_per_tile(a.T, p.G);
+  p.nrt = (a.T * p.G + R - 1) / R;
+  p.n_cta = few_rows_ctas(R);
+  const size_t slots = (size_t)p.n_cta + (size_t)a.b * a.Hkv * p.nrt;
+  p.o_part = static_cast<float*>(a.scratch);
+  p.ml_part = reinterpret_cast<float2*>(p.o_part + slots * R * 128);
+  const size_t merge = (size_t)kWarps * R * 128 * 4;
+  const size_t smem = merge > kRingBytes ? merge : kRingBytes;
+  {
+    DF_TRACE("kv4_attention", st);
+    if (R == 16) {
+      if (ensure_dynamic_smem(kv4_attn_kernel<1>, smem) != cudaSuccess) return DF_ERR_CUDA;
+      launch_k(kv4_attn_kernel<1>, dim3(p.n_cta), dim3(kWarps * 32), smem, st, p);
+    } else {
+      if (ensure_dynamic_smem(kv4_attn_kernel<2>, smem) != cudaSuccess) return DF_ERR_CUDA;
+      launch_k(kv4_attn_kernel<2>, dim3(p.n_cta), dim3(kWarps * 32), smem, st, p);
+    }
+  }
+  {
+    DF_TRACE("kv4_combine", st);
+    const long long nrows = (long long)a.b * a.T * a.Hq;
+    launch_k(kv4_combine_kernel, dim3((unsigned)((nrows + 7) / 8)), dim3(256), 0, st, p, R);
+  }
+  return cudaGetLastError() == cudaSuccess ? DF_OK : DF_ERR_CUDA;
+}
+
+// --------------------------------------------------------------------- attention weights
+constexpr int kWtRows = 64;    // query rows per round
+constexpr int kWtKeys = 16;    // keys per warp and step
+
+struct Kv4WeightsParams {
+  Kv4WeightsArgs a;
+  int G;
+  float scale2;   // scale * log2(e) * 2^k_exp
+};
+
+// S^T = K Q^T: the keys are the rows of the product, so a slot's weight is a sum along a
+// lane's own accumulators and one exchange inside the quad.  A warp owns its slots: no
+// atomics, and the order of every sum is fixed.
+__global__ void __launch_bounds__(kWarps * 32) kv4_weights_kernel(const Kv4WeightsParams p) {
+  __shared__ __align__(16) uint4 qf[kWtRows / 8][4][32];   // [row tile][two steps][lane]
+  __shared__ float2 row_sl[kWtRows];                       // raw score -> log2 units, lse in log2 units
+  pdl_wait();
+  pdl_trigger();
+  const Kv4WeightsArgs& a = p.a;
+  const int s = blockIdx.z, kvh = blockIdx.y;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+  const int len = kv4_len(a.cache_len, s, 0, a.cap, a.status);
+  const int n = a.n_rows ? a.n_rows[s] : a.T;
+  if (len < 0) return;
+  if (n < 0 || n > a.T || n > len || (a.src_slot && n > a.max_src + 1)) {
+    if (tid == 0) set_status(a.status, DF_ERR_ARG, s);
+    return;
+  }
+  const int base = len - n;   // slots before the first row's own
+  const int key_cta = blockIdx.x * kWarps * kWtKeys;
+  if (key_cta >= len) return;
+  const int key0 = key_cta + warp * kWtKeys;
+  const size_t plane = ((size_t)s * a.Hkv + kvh) * a.cap;
+  // K fragments of keys key0 + g and key0 + g + 8, kept over all rows
+  uint32_t kf[8][4];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int key = key0 + half * 8 + g;
+    uint4 c = make_uint4(0u, 0u, 0u, 0u);
+    uint32_t two = 0;
+    if (key < len) {
+      c = *reinterpret_cast<const uint4*>(a.p.kc + (plane + key) * kKv4Codes + t4 * 16);
+      two = *reinterpret_cast<const uint16_t*>(a.p.ks + (plane + key) * kKv4Scales + t4 * 2);
+    }
+    const uint32_t s0 = e4m3x2_to_f16((two & 0xFFu) * 0x00010001u), s1 = e4m3x2_to_f16((two >> 8) * 0x00010001u);
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint32_t f[4];
+      e2m1x8_to_f16(w[e], f);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) kf[2 * e + (x >> 1)][(x & 1) * 2 + half] = hmul2(f[x], e < 2 ? s0 : s1);
+    }
+  }
+  float mass[2] = {0.f, 0.f};
+  const int total = n * p.G;
+  for (int r0 = 0; r0 < total; r0 += kWtRows) {
+    __syncthreads();
+    // four lanes a row: convert to fp16 fragments
+    {
+      const int r = tid >> 2, q4 = tid & 3;   // row of the round, lane of its quad
+      const int rr = r0 + r;
+      const int j = rr / p.G;
+      int node = -1;
+      if (rr < total) {
+        node = j;
+        if (a.src_slot && j > 0) node = a.src_slot[(size_t)s * a.max_src + j - 1] - base;
+        if (a.src_slot && j == 0) node = 0;
+        if (node < 0 || node >= a.T) {
+          set_status(a.status, DF_ERR_ARG, s);
+          node = -1;
+        }
+      }
+      uint4 raw[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) raw[c] = make_uint4(0u, 0u, 0u, 0u);
+      const size_t grow = ((size_t)s * a.T + (node < 0 ? 0 : node)) * a.Hq + kvh * p.G + rr % p.G;
+      if (node >= 0) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) raw[c] = reinterpret_cast<const uint4*>(a.q + grow * 128 + q4 * 32)[c];
+      }
+      float amax = 0.f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      float back;
+      const float f = f16_row_factor(amax, back);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = pack_f16x2(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xFFFF0000u) * f);
+        qf[r >> 3][c][(r & 7) * 4 + q4] = make_uint4(h[0], h[1], h[2], h[3]);
+      }
+      if (q4 == 0) {
+        float lse2 = INFINITY;   // such a row adds 2^(-inf) = 0 everywhere
+        if (node >= 0) {
+          const float v = a.lse[grow];
+          if (v != -INFINITY) lse2 = v * 1.4426950408889634f;
+        }
+        row_sl[r] = make_float2(p.scale2 * back, lse2);
+      }
+    }
+    __syncthreads();
+    const int tiles = (min(kWtRows, total - r0) + 7) / 8;
+    const bool edge = key0 + kWtKeys > base + 1;
+    for (int q = 0; q < tiles; ++q) {
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint4 b = qf[q][c][lane];
+        mma_f16_16816(d, kf[2 * c], b.x, b.y);
+        mma_f16_16816(d, kf[2 * c + 1], b.z, b.w);
+      }
+      const float4 sl = *reinterpret_cast<const float4*>(&row_sl[q * 8 + t4 * 2]);
+      float x[4] = {fmaf(d[0], sl.x, -sl.y), fmaf(d[1], sl.z, -sl.w), fmaf(d[2], sl.x, -sl.y), fmaf(d[3], sl.z, -sl.w)};
+      if (edge) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = (r0 + q * 8 + t4 * 2 + (e & 1)) / p.G;
+          if (key0 + (e >> 1) * 8 + g > base + j) x[e] = -INFINITY;
+        }
+      }
+      mass[0] += ex2_approx(x[0]) + ex2_approx(x[1]);
+      mass[1] += ex2_approx(x[2]) + ex2_approx(x[3]);
+    }
+  }
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    mass[half] += __shfl_xor_sync(0xffffffffu, mass[half], 1);
+    mass[half] += __shfl_xor_sync(0xffffffffu, mass[half], 2);
+    const int key = key0 + half * 8 + g;
+    if (t4 == 0 && key < len) {
+      const float old = key < base ? a.decay * a.score[plane + key] : 0.f;
+      a.score_out[plane + key] = old + mass[half];
+    }
+  }
+}
+
+int launch_kv4_weights(const Kv4WeightsArgs& a, cudaStream_t st) {
+  DF_TRACE("kv4_attention_weights", st);
+  Kv4WeightsParams p;
+  p.a = a;
+  p.G = a.Hq / a.Hkv;
+  p.scale2 = ldexpf(a.scale * 1.4426950408889634f, a.k_exp);
+  const int per = kWarps * kWtKeys;
+  launch_k(kv4_weights_kernel, dim3((a.cap + per - 1) / per, a.Hkv, a.b), dim3(kWarps * 32), 0, st, p);
+  return cudaGetLastError() == cudaSuccess ? DF_OK : DF_ERR_CUDA;
+}
+
+}  // namespace df

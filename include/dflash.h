@@ -342,6 +342,119 @@ int accept_and_compact(int b, int n_tree, const int32_t* choice, const int32_t* 
                        int32_t* src_slot, void* ws, size_t ws_bytes, df_stream stream);
 
 /* ------------------------------------------------------------------------------------
+ * A KV cache held in 4 bits (the pages have no counterpart: they verify over the target's own
+ * bf16 cache; at long contexts and batches that cache is what a step reads and holds).
+ *
+ * A row (one slot of one kv head) is 128 values of 4 bits with one 8-bit scale for each 16:
+ *     value = 2^exp * s * c
+ * c is an e2m1 number (0, 1/2, 1, 3/2, 2, 3, 4, 6 and a sign; dimension 2i in the low half of
+ * byte i), s an e4m3 number without sign, exp a whole number for all keys (k_exp) and one for
+ * all values (v_exp).  A cache row takes 72 bytes instead of 256.  Keys are stored rotated.
+ *
+ * The calls below use one workspace each, as every call does.  Lengths and lists are read on
+ * the device; one that does not fit the cache is recorded in the workspace's status word
+ * (DF_ERR_CAPACITY for a length, DF_ERR_ARG for a list or a count) and its sequence is left
+ * out: caches and scores as they were, attention outputs 0 with lse -inf.
+ * Codes and scales may hold any bytes in slots that no row sees: every byte decodes to a
+ * finite value.
+ * ------------------------------------------------------------------------------------ */
+typedef struct {
+  uint8_t* k_codes;   /* [n_layers][b][Hkv][cap][64]                                  */
+  uint8_t* k_scales;  /* [n_layers][b][Hkv][cap][8]                                   */
+  uint8_t* v_codes;   /* [n_layers][b][Hkv][cap][64]                                  */
+  uint8_t* v_scales;  /* [n_layers][b][Hkv][cap][8]                                   */
+  int32_t n_layers, b, Hkv, hd;   /* hd = 128                                         */
+  int32_t cap;                    /* slots of a sequence, a multiple of 8             */
+  int32_t k_exp, v_exp;           /* -32 .. 32: centre the scales' range 2^-9 .. 448  */
+} df_kv4_cache;
+
+/* dflash_kv4_append -- rounds rows of keys and values into one layer of the cache.
+ *
+ * Row j < n_new[s] of sequence s goes to slot cache_len[s] + j (a flattened tree's node j, a
+ * prompt's token j); cache_len is not modified.  Per block of 16 values x with largest
+ * magnitude a: s = e4m3(a / (6 * 2^exp)), c = e2m1(x / (s * 2^exp)), to nearest even and
+ * saturated; s = 0 gives c = 0.  A NaN is stored as 0 and recorded (DF_ERR_NAN).
+ *   k, v            [b][n][Hkv][hd] bf16, keys rotated
+ *   n_new           [b] int32, 0 <= n_new <= n, or NULL: n rows for every sequence
+ *   cache_len       [b] int32, cache_len + n_new <= cap
+ *   k_held, v_held  [b][n][Hkv][hd] bf16 out, the values that the cache now stands for
+ *                   (exact in bf16); both may be NULL; rows >= n_new are left as they were */
+size_t dflash_kv4_append_workspace_size(void);
+int dflash_kv4_append(const df_kv4_cache* cache, int layer, const df_bf16* k, const df_bf16* v, int n,
+                      const int32_t* n_new, const int32_t* cache_len, df_bf16* k_held, df_bf16* v_held,
+                      void* ws, size_t ws_bytes, df_stream stream);
+
+/* dflash_kv4_attention -- tree_verify_attention over one layer of a 4-bit cache.
+ *
+ * Row (s, i, h) attends slots [0, N) (N = cache_len[s]) and tree slots N + j for every j with
+ * bit j of anc[s][i] set: out = softmax(scale q.k) v, fp32 inside, fp16 probabilities (scaled
+ * by a power of two).  The tree's rows must already be in slots N .. N + n_tree - 1.
+ * n_tree = 1 with anc NULL is a plain decode step.
+ *   q          [b][n_tree][Hq][hd] bf16 (rotated);  Hq a multiple of Hkv
+ *   cache_len  [b] int32, N + n_tree <= cap
+ *   anc        [b][n_tree][ceil(n_tree/32)] uint32, or NULL: a chain, row i sees tree slots 0 .. i
+ *   scale      > 0 and finite
+ *   out        [b][n_tree][Hq][hd] bf16; 0 for a row that sees nothing
+ *   lse        [b][n_tree][Hq] fp32 out, log of the sum of exp(scale q.k); -inf for a row that
+ *              sees nothing; may be NULL */
+size_t dflash_kv4_attention_workspace_size(const df_kv4_cache* cache, int n_tree, int Hq);
+int dflash_kv4_attention(const df_kv4_cache* cache, int layer, int n_tree, int Hq, const df_bf16* q,
+                         const int32_t* cache_len, const uint32_t* anc, float scale, df_bf16* out, float* lse,
+                         void* ws, size_t ws_bytes, df_stream stream);
+
+/* dflash_kv4_attention_weights -- the attention weight that rows laid on every slot.
+ *
+ * The rows that vote are those that stayed: a sequence's last n_rows slots belong to them.  Row
+ * j (0 <= j < n_rows[s]) sees slots 0 .. N + j with N = cache_len[s] - n_rows[s], and
+ *     score_out[slot] = decay * score[slot] + sum_j sum_h exp(scale q_jh . k_slot - lse_jh)
+ * over the query heads h of the slot's kv head; a slot >= N starts from 0, whatever score
+ * holds there.  Slots >= cache_len are left as they were.  Sums run in a fixed order.
+ * After accept_and_compact pass its n_new as n_rows, its src_slot, and the new cache_len: the
+ * root and the accepted path vote, rejected nodes do not.
+ *   q, lse     [b][n_tree][Hq][hd] bf16, [b][n_tree][Hq] fp32: of dflash_kv4_attention
+ *   n_rows     [b] int32, 0 <= n_rows <= min(n_tree, cache_len), or NULL: n_tree
+ *   src_slot   [b][max_src] int32: row 0 is node 0, row j node src_slot[s][j-1] - N
+ *              (n_rows <= max_src + 1); or NULL: row j is node j
+ *   decay      0 .. 1
+ *   score, score_out  [n_layers][b][Hkv][cap] fp32 (the call's layer is used); may be the same */
+size_t dflash_kv4_attention_weights_workspace_size(const df_kv4_cache* cache, int n_tree, int Hq);
+int dflash_kv4_attention_weights(const df_kv4_cache* cache, int layer, int n_tree, int Hq, const df_bf16* q,
+                                 const float* lse, const int32_t* cache_len, const int32_t* n_rows,
+                                 const int32_t* src_slot, int max_src, float scale, float decay, const float* score,
+                                 float* score_out, void* ws, size_t ws_bytes, df_stream stream);
+
+/* dflash_kv4_compact -- the accepted path's rows move, in every layer (the cache's part of
+ * accept_and_compact, to be called behind it with n_layers = 0 and this cache's cap there).
+ *
+ * Row src_slot[s][j] moves to slot cache_len[s] - n_acc[s] + j, for j < n_acc[s].
+ *   src_slot   [b][max_src] int32, ascending, each at or behind its destination
+ *   n_acc      [b] int32, 0 <= n_acc <= max_src
+ *   cache_len  [b] int32: the length with the path (accept_and_compact's) */
+size_t dflash_kv4_compact_workspace_size(void);
+int dflash_kv4_compact(const df_kv4_cache* cache, const int32_t* src_slot, int max_src, const int32_t* n_acc,
+                       const int32_t* cache_len, void* ws, size_t ws_bytes, df_stream stream);
+
+/* dflash_kv4_evict -- drops the slots with the least score, in every layer.
+ *
+ * For each (layer, sequence, kv head) with more than `budget` slots, the budget slots that
+ * stay are the first n_sink, the last n_recent, and of the others those with the largest score
+ * (the lower slot first among equal scores; a NaN below everything).  Rows and scores that
+ * stay go to another cache in the order of their slots, so slots stay in order of age; a
+ * sequence with at most `budget` slots is copied whole.
+ *   score      [n_layers][b][Hkv][cap] fp32
+ *   cache_len  [b] int32
+ *   budget     >= 1, <= to->cap;  n_sink, n_recent >= 0, n_sink + n_recent <= budget
+ *   to         a cache of the same layers, sequences, kv heads and exponents, apart from
+ *              `cache`; its slots >= new_len are left as they were
+ *   score_out  [n_layers][b][Hkv][to->cap] fp32, may be NULL
+ *   new_len    [b] int32 out = min(cache_len, budget) (0 for a sequence left out); may be cache_len
+ *   kept       [n_layers][b][Hkv][budget] int32 out: the slots that stay, ascending; -1 behind */
+size_t dflash_kv4_evict_workspace_size(const df_kv4_cache* cache, int budget);
+int dflash_kv4_evict(const df_kv4_cache* cache, const float* score, const int32_t* cache_len, int budget, int n_sink,
+                     int n_recent, const df_kv4_cache* to, float* score_out, int32_t* new_len, int32_t* kept,
+                     void* ws, size_t ws_bytes, df_stream stream);
+
+/* ------------------------------------------------------------------------------------
  * dflash_linear -- building block: out (+)= X . W^T on the tensor cores.
  *
  * Every projection of the step (q/k/v, o, gate/up, down, context fusion, LM head) is

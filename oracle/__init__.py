@@ -39,6 +39,9 @@ Parity pins (see tests/test_oracle_*.py):
                           frequencies = softmax(logits / T), small-T limit = argmax;
                           step.spec_generate with drawn choices token-identical to plain
                           sampling (losslessness at temperature 1).    PINNED
+  kv4 (KV cache held in 4 bits; no counterpart in the pages) rounding against every
+                          candidate and torch's e4m3, attention against torch's, weights
+                          sum to the rows, eviction by brute force over subsets.  PINNED
   model.layer_forward     pinned only through the invariants above: the pages
                           print no layer equations or values (a Qwen3-style
                           pre-norm layer is the stated reading).
