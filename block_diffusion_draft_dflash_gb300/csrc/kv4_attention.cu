@@ -14,8 +14,7 @@
 // warps are merged when the share, or the (sequence, kv head), ends.
 #include <math.h>
 
-#include "kv4.cuh"
-#include "kv4.h"
+#include "kv4_attn.cuh"
 #include "runtime.h"
 #include "trace.h"
 
@@ -29,54 +28,6 @@ constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 // Probabilities are scaled by 2^12 before they are rounded to fp16: what lies 2^26 below the
 // row's largest still has all its bits.
 constexpr float kPShift = 12.f;
-
-struct Kv4AttnParams {
-  Kv4Planes p;
-  int b, T, Hq, Hkv, G, cap, W;
-  const df_bf16* q;
-  const int32_t* cache_len;
-  const uint32_t* anc;
-  float scale2;          // scale * log2(e) * 2^k_exp
-  float v_mul;           // 2^v_exp
-  df_bf16* out;
-  float* lse;
-  float* o_part;         // [slots][16 MT][128]
-  float2* ml_part;       // [slots][16 MT]
-  int n_cta, nrt;        // CTAs of the grid, row tiles of a (sequence, kv head)
-  int* status;
-};
-
-// Shares: stage t of all `total` stages belongs to the CTA c with first(c) <= t < first(c + 1).
-struct Shares {
-  long long total;
-  int n;   // CTAs that get a share: none gets fewer than kWarps stages, while there are several
-  DF_DEV long long first(int c) const { return total * c / n; }
-  DF_DEV int owner(long long t) const { return (int)(((t + 1) * n - 1) / total); }
-};
-
-DF_DEV int seq_stages(const Kv4AttnParams& p, int s) {   // per unit; a sequence that shows nothing has one
-  const int n = p.cache_len[s];
-  const int len = n >= 0 && n <= p.cap - p.T ? n + p.T : 0;
-  return max(1, (len + kStageKeys - 1) / kStageKeys);
-}
-DF_DEV long long warp_sum_ll(long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-// Stages of sequences [0, s1), a whole warp.
-DF_DEV long long stages_before(const Kv4AttnParams& p, int s1, int lane) {
-  long long v = 0;
-  for (int s = lane; s < s1; s += 32) v += seq_stages(p, s);
-  return warp_sum_ll(v) * p.Hkv * p.nrt;
-}
-DF_DEV Shares make_shares(const Kv4AttnParams& p, int lane) {
-  Shares sh;
-  sh.total = stages_before(p, p.b, lane);
-  const long long most = (sh.total + kWarps - 1) / kWarps;
-  sh.n = most < p.n_cta ? (int)most : p.n_cta;
-  return sh;
-}
 
 // Ancestor (or causal) visibility of tree slot t for node i.
 DF_DEV bool tree_sees(const uint32_t* anc_row, int node, int t) {
@@ -99,39 +50,14 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 2 : 1) kv4_attn_kernel(
   unsigned char* ring = smem + warp * kStages * kStageBytes;
   pdl_wait();
   pdl_trigger();
-  const Shares sh = make_shares(p, lane);
-  if ((int)blockIdx.x >= sh.n) return;
-  const long long t1 = sh.first(blockIdx.x + 1);
-  long long t = sh.first(blockIdx.x);
-  // the sequence that stage t lies in
-  int s = 0;
-  long long seq0 = 0;   // its first stage
-  const int per_seq = p.Hkv * p.nrt;
-  for (int base = 0; base < p.b; base += 32) {
-    const long long mine = base + lane < p.b ? (long long)seq_stages(p, base + lane) * per_seq : 0;
-    long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += x;
-    }
-    const uint32_t past = __ballot_sync(0xffffffffu, seq0 + inc <= t && base + lane < p.b);
-    const int k = __popc(past);   // whole sequences before t
-    s += k;
-    if (k > 0) seq0 += __shfl_sync(0xffffffffu, inc, k - 1);
-    if (k < 32) break;
-  }
+  Kv4Walk walk;
+  if (!walk.init(p, blockIdx.x, lane)) return;
+  Kv4Seg seg;
   uint32_t uses = 0;   // stages this warp has loaded so far, modulo 2^32: slot uses % kStages
   bool ok = true;
-  while (t < t1) {
-    const int per_unit = seq_stages(p, s);
-    const int unit = (int)((t - seq0) / per_unit), tile0 = (int)((t - seq0) % per_unit);
-    const int count = (int)min(t1 - t, (long long)(per_unit - tile0));
-    const int kvh = unit / p.nrt, rt = unit % p.nrt;
-    const int N = p.cache_len[s];
-    const bool fits = N >= 0 && N <= p.cap - p.T;
-    if (!fits && tid == 0) set_status(p.status, DF_ERR_CAPACITY, s);
-    const int len = fits ? N + p.T : 0;
+  while (walk.next(p, seg)) {
+    const int s = seg.s, kvh = seg.kvh, rt = seg.rt, tile0 = seg.tile0, count = seg.count, N = seg.N, len = seg.len;
+    if (len == 0 && tid == 0) set_status(p.status, DF_ERR_CAPACITY, s);
     const size_t plane = ((size_t)s * p.Hkv + kvh) * p.cap;
     const int rows = min(R, p.T * p.G - rt * R);   // live rows of the tile
     const uint8_t *kc = p.p.kc + plane * kKv4Codes, *vc = p.p.vc + plane * kKv4Codes;
@@ -233,7 +159,7 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 2 : 1) kv4_attn_kernel(
         }
       }
       // log2 units, mask, running maximum
-      const bool edge = key0 + kStageKeys > N || !fits;
+      const bool edge = key0 + kStageKeys > N;
       uint32_t pf[MT][2][4];
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
@@ -341,8 +267,12 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 2 : 1) kv4_attn_kernel(
       }
     }
     __syncthreads();
-    const int u_glob = s * per_seq + unit;
-    const bool whole = count == per_unit;
+    const bool whole = seg.first && seg.last;
+    if (tid == 0 && !whole) {
+      if (seg.first) p.range[seg.unit].x = blockIdx.x;
+      if (seg.last) p.range[seg.unit].y = blockIdx.x;
+    }
+    if (tid == 0 && whole) p.range[seg.unit] = make_int2(0, 0);
     for (int x = tid; x < rows * 32; x += kWarps * 32) {   // four dimensions of one row
       const int r = x >> 5, d = (x & 31) * 4;
       float M = -INFINITY;
@@ -366,26 +296,20 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 2 : 1) kv4_attn_kernel(
         w2.x = pack_bf16x2(acc.x * inv, acc.y * inv);
         w2.y = pack_bf16x2(acc.z * inv, acc.w * inv);
         *reinterpret_cast<uint2*>(p.out + grow * 128 + d) = w2;
-        if (p.lse && d == 0) p.lse[grow] = L > 0.f ? (M - kPShift + log2f(L)) * 0.6931471805599453f : -INFINITY;
+        if (p.lse && d == 0) p.lse[grow] = kv4_lse(M, L, kPShift);
       } else {
-        const size_t at = (size_t)(blockIdx.x + u_glob) * R + r;
+        const size_t at = (size_t)(blockIdx.x + seg.unit) * R + r;
         *reinterpret_cast<float4*>(p.o_part + at * 128 + d) = acc;
         if (d == 0) p.ml_part[at] = make_float2(M, L);
       }
     }
     fence_proxy_async();   // the rings were written by ordinary stores: order them before the next copies
     __syncthreads();
-    t += count;
-    if (tile0 + count == per_unit && unit + 1 == per_seq) {
-      seq0 += (long long)per_unit * per_seq;
-      ++s;
-    }
   }
 }
 
-// One warp per query row whose (sequence, kv head) was cut: the shares' partial results in
-// the order of the shares.
-__global__ void __launch_bounds__(256) kv4_combine_kernel(const Kv4AttnParams p, int R) {
+// One warp per query row of a cut unit: the parts in the order of the CTAs.
+__global__ void __launch_bounds__(256) kv4_combine_kernel(const Kv4AttnParams p) {
   pdl_wait();
   pdl_trigger();
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -393,21 +317,19 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const Kv4AttnParams p,
   if (row >= (long long)p.b * p.T * p.Hq) return;
   const int head = (int)(row % p.Hq), node = (int)(row / p.Hq % p.T), s = (int)(row / p.Hq / p.T);
   const int kvh = head / p.G, r = node * p.G + head % p.G;
-  const Shares sh = make_shares(p, lane);
-  const int per_unit = seq_stages(p, s), per_seq = p.Hkv * p.nrt;
-  const int unit = kvh * p.nrt + r / R;
-  const long long a0 = stages_before(p, s, lane) + (long long)unit * per_unit;
-  const int c0 = sh.owner(a0), c1 = sh.owner(a0 + per_unit - 1);
-  if (c0 == c1) return;
-  const size_t slot0 = (size_t)s * per_seq + unit, rr = r % R;
+  const int unit = (s * p.Hkv + kvh) * p.nrt + r / p.R;
+  const int2 range = p.range[unit];
+  const int c0 = max(range.x, 0), c1 = min(range.y, p.n_cta - 1);
+  if (c0 >= c1) return;
+  const size_t rr = r % p.R;
   float M = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.ml_part[(slot0 + c) * R + rr].x);
+  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.ml_part[((size_t)unit + c) * p.R + rr].x);
   M = warp_max(M);
   float L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int c = c0; c <= c1; ++c) {
-    const size_t at = (slot0 + c) * R + rr;
+    const size_t at = ((size_t)unit + c) * p.R + rr;
     const float2 v = p.ml_part[at];
     const float4 o = reinterpret_cast<const float4*>(p.o_part + at * 128)[lane];
     const float f = v.x == -INFINITY ? 0.f : ex2_approx(v.x - M);
@@ -419,18 +341,43 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const Kv4AttnParams p,
   w2.x = pack_bf16x2(acc.x * inv, acc.y * inv);
   w2.y = pack_bf16x2(acc.z * inv, acc.w * inv);
   reinterpret_cast<uint2*>(p.out + row * 128)[lane] = w2;
-  if (p.lse && lane == 0) p.lse[row] = L > 0.f ? (M - kPShift + log2f(L)) * 0.6931471805599453f : -INFINITY;
+  if (p.lse && lane == 0) p.lse[row] = kv4_lse(M, L, p.shift);
 }
 
 // ------------------------------------------------------------------------------- host
-static int rows_per_tile(int T, int G) { return T * G <= 16 ? 16 : 32; }
-static int few_rows_ctas(int R) { return num_sms() * (R == 16 ? 2 : 1); }
+int launch_kv4_attn_few(Kv4AttnParams p, cudaStream_t st) {
+  p.shift = kPShift;
+  const size_t merge = (size_t)kWarps * p.R * 128 * 4;
+  const size_t smem = merge > kRingBytes ? merge : kRingBytes;
+  if (p.R == 16) {
+    if (ensure_dynamic_smem(kv4_attn_kernel<1>, smem) != cudaSuccess) return DF_ERR_CUDA;
+    launch_k(kv4_attn_kernel<1>, dim3(p.n_cta), dim3(kWarps * 32), smem, st, p);
+  } else {
+    if (ensure_dynamic_smem(kv4_attn_kernel<2>, smem) != cudaSuccess) return DF_ERR_CUDA;
+    launch_k(kv4_attn_kernel<2>, dim3(p.n_cta), dim3(kWarps * 32), smem, st, p);
+  }
+  return cudaGetLastError() == cudaSuccess ? DF_OK : DF_ERR_CUDA;
+}
+
+namespace {
+// Rows, stage and grid of a call, by its rows per kv head.
+void kv4_attn_plan(int T, int G, Kv4AttnParams& p) {
+  const long long rows = (long long)T * G;
+  p.R = rows <= 16 ? 16 : 128;
+  p.nrt = (int)((rows + p.R - 1) / p.R);
+  p.stage = p.R == 128 ? 128 : kStageKeys;
+  p.min_stages = p.R == 128 ? 4 : kWarps;
+  p.n_cta = num_sms() * (p.R == 16 ? 2 : 1);
+}
+size_t up16(size_t x) { return (x + 15) & ~(size_t)15; }
+}  // namespace
 
 size_t kv4_attn_scratch_bytes(int b, int T, int Hq, int Hkv, int cap) {
   (void)cap;
-  const int G = Hq / Hkv, R = rows_per_tile(T, G);
-  const size_t slots = (size_t)few_rows_ctas(R) + (size_t)b * Hkv * ((T * G + R - 1) / R);
-  return slots * R * (128 * 4 + 8) + 256;
+  Kv4AttnParams p{};
+  kv4_attn_plan(T, Hq / Hkv, p);
+  const size_t units = (size_t)b * Hkv * p.nrt, slots = p.n_cta + units;
+  return up16(slots * p.R * (128 * 4 + 8)) + up16(units * sizeof(int2));
 }
 
 int launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t st) {
@@ -441,29 +388,20 @@ int launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t st) {
   p.scale2 = ldexpf(a.scale * 1.4426950408889634f, a.k_exp);
   p.v_mul = ldexpf(1.f, a.v_exp);
   p.out = a.out; p.lse = a.lse; p.status = a.status;
-  const int R = rows_per_tile(a.T, p.G);
-  p.nrt = (a.T * p.G + R - 1) / R;
-  p.n_cta = few_rows_ctas(R);
-  const size_t slots = (size_t)p.n_cta + (size_t)a.b * a.Hkv * p.nrt;
+  kv4_attn_plan(a.T, p.G, p);
+  const size_t units = (size_t)a.b * a.Hkv * p.nrt, slots = p.n_cta + units;
   p.o_part = static_cast<float*>(a.scratch);
-  p.ml_part = reinterpret_cast<float2*>(p.o_part + slots * R * 128);
-  const size_t merge = (size_t)kWarps * R * 128 * 4;
-  const size_t smem = merge > kRingBytes ? merge : kRingBytes;
+  p.ml_part = reinterpret_cast<float2*>(p.o_part + slots * p.R * 128);
+  p.range = reinterpret_cast<int2*>(static_cast<unsigned char*>(a.scratch) + up16(slots * p.R * (128 * 4 + 8)));
   {
     DF_TRACE("kv4_attention", st);
-    if (R == 16) {
-      if (ensure_dynamic_smem(kv4_attn_kernel<1>, smem) != cudaSuccess) return DF_ERR_CUDA;
-      launch_k(kv4_attn_kernel<1>, dim3(p.n_cta), dim3(kWarps * 32), smem, st, p);
-    } else {
-      if (ensure_dynamic_smem(kv4_attn_kernel<2>, smem) != cudaSuccess) return DF_ERR_CUDA;
-      launch_k(kv4_attn_kernel<2>, dim3(p.n_cta), dim3(kWarps * 32), smem, st, p);
-    }
+    const int rc = p.R == 128 ? launch_kv4_attn_tc(p, st) : launch_kv4_attn_few(p, st);
+    if (rc != DF_OK) return rc;
   }
-  {
-    DF_TRACE("kv4_combine", st);
-    const long long nrows = (long long)a.b * a.T * a.Hq;
-    launch_k(kv4_combine_kernel, dim3((unsigned)((nrows + 7) / 8)), dim3(256), 0, st, p, R);
-  }
+  p.shift = p.R == 128 ? kTcShift : kPShift;
+  DF_TRACE("kv4_combine", st);
+  const long long nrows = (long long)a.b * a.T * a.Hq;
+  launch_k(kv4_combine_kernel, dim3((unsigned)((nrows + 7) / 8)), dim3(256), 0, st, p);
   return cudaGetLastError() == cudaSuccess ? DF_OK : DF_ERR_CUDA;
 }
 
