@@ -21,7 +21,7 @@
 namespace df {
 
 constexpr int kWarps = 8;
-constexpr int kStageKeys = 32;
+constexpr int kStageKeys = 32;   // launch: stage_log2
 constexpr int kStages = 2;
 constexpr int kStageBytes = kStageKeys * 2 * (kKv4Codes + kKv4Scales);   // K codes, V codes, K scales, V scales
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
@@ -29,13 +29,8 @@ constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 // row's largest still has all its bits.
 constexpr float kPShift = 12.f;
 
-// Ancestor (or causal) visibility of tree slot t for node i.
-DF_DEV bool tree_sees(const uint32_t* anc_row, int node, int t) {
-  return anc_row ? (anc_row[t >> 5] >> (t & 31)) & 1u : t <= node;
-}
-
 template <int MT>   // row tiles of 16 per warp
-__global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 2 : 1) kv4_attn_kernel(const Kv4AttnParams p) {
+__global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 2 : 1) kv4_attn_kernel(const __grid_constant__ Kv4AttnParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int R = 16 * MT;
   __shared__ __align__(8) uint64_t bars[kWarps][kStages];
@@ -127,7 +122,7 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 2 : 1) kv4_attn_kernel(
     }
     for (int i = 0; i < mine; ++i) {
       const uint32_t slot = uses % kStages;
-      ok = ok && mbar_wait(&bars[warp][slot], (uses / kStages) & 1, p.status, 50);
+      ok = ok && kv4_wait(&bars[warp][slot], (uses / kStages) & 1, p.status, 50);
       ok = __all_sync(0xffffffffu, ok);
       const unsigned char* st = ring + slot * kStageBytes;
       const unsigned char *skc = st, *svc = st + kStageKeys * kKv4Codes;
@@ -167,20 +162,27 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 2 : 1) kv4_attn_kernel(
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float x = sc[m][q][e] * qs[m][e >> 1];
-            if (edge) {
-              const int r = rt * R + m * 16 + (e >> 1) * 8 + g;
-              const int node = r / p.G;
-              const int key = key0 + q * 8 + (e & 1) * 4 + t4;
-              bool see = key < len && r < p.T * p.G;
-              if (see && key >= N)
-                see = tree_sees(p.anc ? p.anc + ((size_t)s * p.T + node) * p.W : nullptr, node, key - N);
-              if (!see) x = -INFINITY;
-            }
-            sc[m][q][e] = x;
-            mt[e >> 1] = fmaxf(mt[e >> 1], x);
+          for (int e = 0; e < 4; ++e) sc[m][q][e] *= qs[m][e >> 1];
+        if (edge) {
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            const int r = rt * R + m * 16 + half * 8 + g, node = r / p.G;
+            const uint32_t* anc = p.anc && node < p.T ? p.anc + ((size_t)s * p.T + node) * p.W : nullptr;
+            uint32_t bits = node < p.T ? kv4_see_bits(anc, p.W, N, key0, node, len) : 0u;
+            bits >>= t4;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (!((bits >> (q * 8 + e * 4)) & 1u)) {
+                  if (half) sc[m][q][2 + e] = -INFINITY; else sc[m][q][e] = -INFINITY;
+                }
           }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mt[e >> 1] = fmaxf(mt[e >> 1], sc[m][q][e]);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           mt[half] = fmaxf(mt[half], __shfl_xor_sync(0xffffffffu, mt[half], 1));
@@ -268,11 +270,10 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 2 : 1) kv4_attn_kernel(
     }
     __syncthreads();
     const bool whole = seg.first && seg.last;
-    if (tid == 0 && !whole) {
+    if (tid == 0) {
       if (seg.first) p.range[seg.unit].x = blockIdx.x;
       if (seg.last) p.range[seg.unit].y = blockIdx.x;
     }
-    if (tid == 0 && whole) p.range[seg.unit] = make_int2(0, 0);
     for (int x = tid; x < rows * 32; x += kWarps * 32) {   // four dimensions of one row
       const int r = x >> 5, d = (x & 31) * 4;
       float M = -INFINITY;
@@ -320,21 +321,27 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const Kv4AttnParams p)
   const int unit = (s * p.Hkv + kvh) * p.nrt + r / p.R;
   const int2 range = p.range[unit];
   const int c0 = max(range.x, 0), c1 = min(range.y, p.n_cta - 1);
-  if (c0 >= c1) return;
-  const size_t rr = r % p.R;
+  // parts: one a CTA, or two of a tile whose halves share their rows
+  const int per = kv4_single(p, r / p.R) ? 2 : 1, parts = (c1 - c0 + 1) * per;
+  if (parts <= 1) return;
+  auto slot = [&](int i) { return ((size_t)unit + c0 + i / per) * p.R + (i % per) * (p.R / 2) + r % p.R; };
+  // lane i holds part i's maximum and sum (parts behind the 32nd in turn)
   float M = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.ml_part[((size_t)unit + c) * p.R + rr].x);
+  for (int i = lane; i < parts; i += 32) M = fmaxf(M, p.ml_part[slot(i)].x);
   M = warp_max(M);
   float L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const size_t at = ((size_t)unit + c) * p.R + rr;
-    const float2 v = p.ml_part[at];
-    const float4 o = reinterpret_cast<const float4*>(p.o_part + at * 128)[lane];
+  for (int i0 = 0; i0 < parts; i0 += 32) {
+    const float2 v = i0 + lane < parts ? p.ml_part[slot(i0 + lane)] : make_float2(-INFINITY, 0.f);
     const float f = v.x == -INFINITY ? 0.f : ex2_approx(v.x - M);
-    L += f * v.y;
-    acc.x += f * o.x; acc.y += f * o.y; acc.z += f * o.z; acc.w += f * o.w;
+    L += warp_sum(f * v.y);
+    const int n = min(32, parts - i0);
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const float4 o = reinterpret_cast<const float4*>(p.o_part + slot(i0 + i) * 128)[lane];
+      const float fi = __shfl_sync(0xffffffffu, f, i);
+      acc.x += fi * o.x; acc.y += fi * o.y; acc.z += fi * o.z; acc.w += fi * o.w;
+    }
   }
   const float inv = L > 0.f ? p.v_mul / L : 0.f;
   uint2 w2;
@@ -363,10 +370,11 @@ namespace {
 // Rows, stage and grid of a call, by its rows per kv head.
 void kv4_attn_plan(int T, int G, Kv4AttnParams& p) {
   const long long rows = (long long)T * G;
-  p.R = rows <= 16 ? 16 : 128;
+  p.R = rows <= 16 ? 16 : 256;
   p.nrt = (int)((rows + p.R - 1) / p.R);
-  p.stage = p.R == 128 ? 128 : kStageKeys;
-  p.min_stages = p.R == 128 ? 4 : kWarps;
+  p.last_single = p.R == 256 && rows - (long long)(p.nrt - 1) * p.R <= 128;
+  p.stage_log2 = p.R == 256 ? 7 : 5;
+  p.min_stages = p.R == 256 ? 2 : kWarps;
   p.n_cta = num_sms() * (p.R == 16 ? 2 : 1);
 }
 size_t up16(size_t x) { return (x + 15) & ~(size_t)15; }
@@ -384,6 +392,7 @@ int launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t st) {
   Kv4AttnParams p{};
   p.p = a.p;
   p.b = a.b; p.T = a.T; p.Hq = a.Hq; p.Hkv = a.Hkv; p.G = a.Hq / a.Hkv; p.cap = a.cap; p.W = (a.T + 31) / 32;
+  p.g_magic = p.G > 1 ? (uint32_t)(((1ull << 32) + p.G - 1) / p.G) : 0u;
   p.q = a.q; p.cache_len = a.cache_len; p.anc = a.anc;
   p.scale2 = ldexpf(a.scale * 1.4426950408889634f, a.k_exp);
   p.v_mul = ldexpf(1.f, a.v_exp);
@@ -395,10 +404,10 @@ int launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t st) {
   p.range = reinterpret_cast<int2*>(static_cast<unsigned char*>(a.scratch) + up16(slots * p.R * (128 * 4 + 8)));
   {
     DF_TRACE("kv4_attention", st);
-    const int rc = p.R == 128 ? launch_kv4_attn_tc(p, st) : launch_kv4_attn_few(p, st);
+    const int rc = p.R == 256 ? launch_kv4_attn_tc(p, st) : launch_kv4_attn_few(p, st);
     if (rc != DF_OK) return rc;
   }
-  p.shift = p.R == 128 ? kTcShift : kPShift;
+  p.shift = p.R == 256 ? kTcShift : kPShift;
   DF_TRACE("kv4_combine", st);
   const long long nrows = (long long)a.b * a.T * a.Hq;
   launch_k(kv4_combine_kernel, dim3((unsigned)((nrows + 7) / 8)), dim3(256), 0, st, p);

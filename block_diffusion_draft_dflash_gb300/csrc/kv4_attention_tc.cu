@@ -1,97 +1,176 @@
-// Tree attention over a KV cache held in 4 bits on the tcgen05 tensor cores: tiles of 128 query
-// rows (a node's heads of one kv head lie next to one another, so one decoded K/V tile feeds
-// all of them).
+// Tree attention over a KV cache held in 4 bits on the tcgen05 tensor cores.
 //
-// Per 128-key block:  S = Q K^T (fp16 operands, fp32 in TMEM, three buffers), softmax with a
-// running maximum that moves only when a block raises it by more than 2^8, P as fp16 over its
-// own S in TMEM, O += P V.  The cache's values are fp16 numbers (kv4.cuh), so decoding loses
-// nothing and the products are exact.
+// Query rows of one (sequence, kv head) lie node-major (a node's heads next to one another)
+// in tiles of 128.  A CTA runs two streams side by side, each with its own S, P and O in TMEM
+// and its own softmax warpgroup, so that one stream's exponentials run under the other's
+// products:
+//   pair    the unit has more than 128 rows: the streams are two row tiles, and a stage is one
+//           block of 128 keys, decoded once for both;
+//   single  it has at most 128: both streams hold the same rows, and a stage is two blocks of
+//           128 keys, one for each.  Their results are merged like those of two CTAs.
+// Either way a stage is two S = Q K^T, two softmax blocks and two O += P V, which makes equal
+// shares of stages (kv4_attn.cuh) equal shares of work.
 //
-// Warp roles: 8 softmax / epilogue warps (two per 32 rows, one per 64 columns), 4 decoding
-// warps, one MMA issuer (owns TMEM) and one warp that brings the codes.  Codes arrive by
-// untiled bulk copies (a block's rows are contiguous) in kNS stages; the decoding warps write K
-// as [key][dim] and V as [dim][key] in 128-byte-swizzled rows, which is what the MMA reads as
-// K-major operands.  V's codes lie [key][dim]: a decoding thread takes 8 keys x 16 dimensions
-// and merges two keys' codes nibble by nibble, so that one conversion yields a pair of keys.
-// A CTA walks through its share of all blocks (kv4_attn.cuh), unit by unit.
+// Per block:  S in fp32 (fp16 operands: the cache's values are fp16 numbers, kv4.cuh, so the
+// products are exact), softmax with a running maximum that moves only when a block raises it
+// by more than 2^8, P as fp16 over its own S, O += P V.  One thread owns one row of a stream and
+// holds its 128 scores in registers (given to it by the decoding warps): S is read once, and
+// no exchange between threads is needed.
+//
+// Warp roles: 4 softmax / epilogue warps and an MMA issuer for each stream, 8 decoding warps and
+// one warp that brings the codes.  Codes arrive by untiled bulk copies (a block's rows are
+// contiguous); the decoding warps write K and V alike as [key][dim] in 128-byte-swizzled rows,
+// which S = Q K^T reads as a K-major operand and O += P V as an MN-major one.
+//
+// A stream's issue order is fixed: S(0), then PV(i), S(i+1).  One thread's MMAs run in order, so
+// S(i+1) may take the place of P(i), and its completion implies that of PV(i): O may be
+// rescaled then.
+// setmaxnreg and calls do not go together: ptxas cannot allocate registers for both
+#define KV4_COLD DF_DEV
 #include "kv4_attn.cuh"
 #include "runtime.h"
 #include "trace.h"
 
 namespace df {
 
-constexpr int kCG = 2;                         // column groups (softmax warps per 32 rows)
-constexpr int kCols = 128 / kCG;
-constexpr int kSoft = 128 * kCG;               // softmax threads
-constexpr int kDecWarps = 4;
-constexpr int kDec0 = kSoft / 32;              // first decoding warp
-constexpr int kMmaWarp = kDec0 + kDecWarps, kLoadWarp = kMmaWarp + 1;
-constexpr int kThreads = (kLoadWarp + 1) * 32;
+constexpr int kDecWarps = 8;
+constexpr int kDec0 = 8;                       // first decoding warp, behind 4 softmax warps of each stream
+constexpr int kMmaWarp = kDec0 + kDecWarps, kLoadWarp = kMmaWarp + 2;   // an MMA warp for each stream
+constexpr int kThreads = (kLoadWarp + 2) * 32;   // the last warp only fills its warpgroup
 constexpr int kKB = 128;                       // keys of a block
-constexpr int kSBufs = 3;                      // S/P buffers in TMEM
-constexpr uint32_t kOCol = kSBufs * 128;
-constexpr int kNS = 3;                         // stages of codes
+constexpr uint32_t kSCol = 0, kOCol = 256;     // S (then P) of stream w at 128 w, O at 256 + 128 w
 constexpr uint32_t kTile = 128 * 128 * 2;      // one fp16 tile: two slabs of 64 columns
-constexpr int kOctet = 8 * kKv4Codes + 16;     // V codes of 8 keys, padded: 8 octets start in 8 bank groups
-constexpr int kStKc = 0, kStVc = kKB * kKv4Codes, kStKs = kStVc + 16 * kOctet, kStVs = kStKs + kKB * kKv4Scales;
-constexpr int kStage = kStVs + kKB * kKv4Scales;
-static_assert(kStage % 16 == 0, "bulk copies");
+constexpr int kTiles = 3;                      // ring of decoded tiles
+constexpr int kRaw = 6;                        // ring of codes, one tile each
+constexpr int kSegs = 4;                       // ring of units
+constexpr int kRawScales = kKB * kKv4Codes;    // codes [key][64], then scales [key][8]
+constexpr int kRawBytes = kRawScales + kKB * kKv4Scales;
 
-// Instruction descriptor, kind::f16: fp16 A and B, fp32 accumulator, both K-major.
-__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
-  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// Instruction descriptor, kind::f16: fp16 A and B, fp32 accumulator, A K-major, B K- or MN-major.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn) {
+  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// Shared-memory matrix descriptor, MN-major operand, 128-byte swizzle: rows of 64 fp16 along
+// MN; the next 64 follow a slab (half a tile) later, the next 8 rows (along K) 1024 bytes later.
+DF_DEV uint64_t sdesc_mnmajor_sw128(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFF) >> 4) | (uint64_t)((kTile / 2) >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
-// 32 bits of a row's visibility for keys j0 .. j0+31.
-DF_DEV uint32_t see_bits(const uint32_t* anc, int W, int N, int j0, int node, int len) {
-  const int n = N - j0;
-  uint32_t bits = n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;   // the cache
-  const int t0 = -n;                                                     // tree slot of bit 0
-  if (anc) {
-    const int w = t0 >= 0 ? t0 >> 5 : -((31 - t0) >> 5), sh = t0 - 32 * w;
-    const uint32_t lo = w >= 0 && w < W ? anc[w] : 0u;
-    const uint32_t hi = sh && w + 1 >= 0 && w + 1 < W ? anc[w + 1] : 0u;
-    bits |= sh ? (lo >> sh) | (hi << (32 - sh)) : lo;
-  } else {
-    const int m = N + node + 1 - j0;                                      // chain: keys below N + node + 1
-    bits = m >= 32 ? 0xFFFFFFFFu : m <= 0 ? 0u : (1u << m) - 1u;
-  }
-  const int l = len - j0;
-  return l >= 32 ? bits : l <= 0 ? 0u : bits & ((1u << l) - 1u);
-}
-
-DF_DEV bool soft_and(bool v) {   // over the softmax threads (barrier 1)
-  uint32_t r;
+// 32 lanes x 32 bits, 32 consecutive columns per thread.
+DF_DEV void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.and.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
-      : "=r"(r) : "r"((uint32_t)v), "r"(kSoft) : "memory");
-  return r != 0;
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
-DF_DEV void soft_sync() { asm volatile("bar.sync 1, %0;" ::"r"(kSoft) : "memory"); }
+DF_DEV float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Pairs of fp32 numbers in one instruction: (a.x * b.x + c.x, ..) and (a.x + b.x, ..).
+DF_DEV uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+DF_DEV void unpack2(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+DF_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+DF_DEV uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
-__global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnParams p) {
+// The 32 query rows from `first` on of a (sequence, kv head): node-major, a node's heads next
+// to one another.  One division for the first, a multiplication for each other.
+struct Rows {
+  int node0, rem0;
+  long long base;   // index in q, out and lse of the sequence's first row of the kv head
+  DF_DEV Rows(const Kv4AttnParams& p, int s, int kvh, int first) {
+    node0 = first / p.G;
+    rem0 = first - node0 * p.G;
+    base = (long long)s * p.T * p.Hq + kvh * p.G;
+  }
+  DF_DEV int step(const Kv4AttnParams& p, int x) const { return p.g_magic ? __umulhi(x, p.g_magic) : x; }
+  DF_DEV int node(const Kv4AttnParams& p, int k) const { return node0 + step(p, rem0 + k); }
+  DF_DEV long long index(const Kv4AttnParams& p, int k) const {   // -1: behind the last row
+    const int q = step(p, rem0 + k), n = node0 + q;
+    return n < p.T ? base + (long long)n * p.Hq + (rem0 + k - q * p.G) : -1;
+  }
+};
+
+// 32 bits of visibility (keys j0 .. j0+31) of the lane's row, `first` being the warp's first row.
+// Out of line, like what it calls: a block at the mask's edge is rare.
+DF_DEV uint32_t row_bits(const Kv4AttnParams& p, const Kv4Seg& sg, int first, int lane, int j0) {
+  const int node = Rows(p, sg.s, sg.kvh, first).node(p, lane);
+  if (node >= p.T) return 0u;
+  return kv4_see_bits(p.anc ? p.anc + ((size_t)sg.s * p.T + node) * p.W : nullptr, p.W, sg.N, j0, node, sg.len);
+}
+
+// Registers move to the softmax warps.  What a block has is what it was launched with (checked
+// at the launch): kWarps x 32 x kLaunchRegs.  A warpgroup changes its share as a whole.
+constexpr int kWarps = kThreads / 32, kLaunchRegs = 96, kSoftRegs = 168, kDecRegs = 40, kRestRegs = 64;
+static_assert(kWarps == 20 && 8 * kSoftRegs + 8 * kDecRegs + 4 * kRestRegs <= kWarps * kLaunchRegs, "registers");
+template <int N> DF_DEV void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> DF_DEV void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// O of the warp's rows times alpha, 8 columns at a time: few registers are free then.
+DF_DEV void scale_rows(uint32_t oaddr, float alpha) {
+#pragma unroll 1
+  for (int c = 0; c < 128; c += 8) {
+    float o[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7])
+                 : "r"(oaddr + c));
+    tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] *= alpha;
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 ::"r"(oaddr + c), "f"(o[0]), "f"(o[1]), "f"(o[2]), "f"(o[3]), "f"(o[4]), "f"(o[5]), "f"(o[6]), "f"(o[7])
+                 : "memory");
+  }
+}
+
+// Cycles that stream 1 waits before its first product.
+constexpr int kStagger = 1500;
+DF_DEV void pause(int cycles) {
+  const long long t0 = clock64();
+  while (clock64() - t0 < cycles) {}
+}
+
+__global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const __grid_constant__ Kv4AttnParams p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  unsigned char* q_smem = smem;
-  unsigned char* k_smem = q_smem + kTile;        // two tiles
-  unsigned char* v_smem = k_smem + 2 * kTile;    // two tiles
-  unsigned char* codes = v_smem + 2 * kTile;     // kNS stages
-  __shared__ __align__(8) uint64_t c_full[kNS], c_empty[kNS], k_full[2], k_empty[2], v_full[2], v_empty[2];
-  __shared__ __align__(8) uint64_t s_full[kSBufs], p_full[kSBufs], o_done[kSBufs], q_full, o_free, drain;
+  unsigned char* q_smem = smem;                       // one tile per stream
+  unsigned char* t_smem = q_smem + 2 * kTile;         // kTiles decoded tiles
+  unsigned char* raw_smem = t_smem + kTiles * kTile;  // kRaw tiles of codes
+  __shared__ __align__(8) uint64_t r_full[kRaw], r_empty[kRaw], t_full[kTiles], t_empty[kTiles];
+  __shared__ __align__(8) uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drain[2];
+  __shared__ __align__(8) uint64_t seg_full[kSegs], seg_empty[kSegs];
+  __shared__ Kv4Seg segs[kSegs];
   __shared__ uint32_t tmem_slot;
-  __shared__ float red_max[2][kCG][128], red_sum[kCG][128];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kNS; ++i) { mbar_init(&c_full[i], 1); mbar_init(&c_empty[i], kDecWarps); }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&k_full[i], kDecWarps); mbar_init(&k_empty[i], 1);
-      mbar_init(&v_full[i], kDecWarps); mbar_init(&v_empty[i], 1);
-    }
-    for (int i = 0; i < kSBufs; ++i) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], kSoft); mbar_init(&o_done[i], 1); }
-    mbar_init(&q_full, kSoft);
-    mbar_init(&o_free, kSoft);
-    mbar_init(&drain, 1);
+    for (int i = 0; i < kRaw; ++i) { mbar_init(&r_full[i], 1); mbar_init(&r_empty[i], kDecWarps); }
+    for (int i = 0; i < kTiles; ++i) { mbar_init(&t_full[i], kDecWarps); mbar_init(&t_empty[i], 2); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&q_full[i], 4); mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4); mbar_init(&o_full[i], 1); }
+    for (int i = 0; i < kSegs; ++i) { mbar_init(&seg_full[i], 1); mbar_init(&seg_empty[i], kLoadWarp); }
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     fence_barrier_init();
   }
   if (warp == kMmaWarp) { tmem_alloc(&tmem_slot, 512); tmem_relinquish(); }
@@ -101,369 +180,405 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnP
   pdl_wait();
   pdl_trigger();
   const uint32_t tmem = tmem_slot;
-  Kv4Walk walk;
-  const bool any = walk.init(p, blockIdx.x, lane);
-  Kv4Seg sg;
+  // Units of this CTA's share, from the loading warp to the others; a unit of 0 stages ends them.
+  bool ok = true;
+  int n_seg = 0;   // units taken so far
+  auto take = [&]() -> const Kv4Seg& {
+    ok = __all_sync(0xffffffffu, kv4_wait(&seg_full[n_seg % kSegs], (n_seg / kSegs) & 1, p.status, 59));
+    return segs[n_seg++ % kSegs];
+  };
+  auto give_back = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&seg_empty[(n_seg - 1) % kSegs]);
+  };
 
-  if (warp == kLoadWarp) {
+  if (warp >= kMmaWarp) regs_down<kRestRegs>();
+  if (warp > kLoadWarp) {
+    // nothing to do
+  } else if (warp == kLoadWarp) {
     // ---------------------------------------------------------------- bring codes
-    int j = 0;          // block of this CTA
-    bool ok = any;
-    while (ok && walk.next(p, sg)) {
+    int j = 0;          // tiles so far
+    int st = 0, phase = 0;
+    Kv4Walk walk;
+    Kv4Seg sg;
+    bool more = walk.init(p, blockIdx.x, lane);
+    while (ok) {
+      sg.count = 0;
+      if (more) more = walk.next(p, sg);
+      ok = __all_sync(0xffffffffu, kv4_wait(&seg_empty[n_seg % kSegs], ((n_seg / kSegs) & 1) ^ 1, p.status, 58));
+      if (!ok) break;
+      if (lane == 0) {
+        segs[n_seg % kSegs] = sg;
+        mbar_arrive(&seg_full[n_seg % kSegs]);
+      }
+      __syncwarp();
+      ++n_seg;
+      if (sg.count == 0) break;
       const size_t plane = ((size_t)sg.s * p.Hkv + sg.kvh) * p.cap;
-      for (int i = 0; i < sg.count && ok; ++i, ++j) {
-        const int st = j % kNS;
-        ok = __all_sync(0xffffffffu, mbar_wait(&c_empty[st], ((j / kNS) & 1) ^ 1, p.status, 60));
+      const bool single = sg.single;
+      const int tiles = sg.count * (single ? 4 : 2), block0 = sg.tile0 * (single ? 2 : 1);
+      for (int x = 0; x < tiles; ++x) {
+        ok = __all_sync(0xffffffffu, kv4_wait(&r_empty[st], phase ^ 1, p.status, 60));
         if (!ok) break;
-        const int key0 = (sg.tile0 + i) * kKB;
-        const int n = min(kKB, p.cap - key0);   // a multiple of 8
-        unsigned char* to = codes + st * kStage;
-        const size_t row = plane + key0;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&c_full[st], n * 2 * (kKv4Codes + kKv4Scales));
-          bulk_load(to + kStKc, p.p.kc + row * kKv4Codes, n * kKv4Codes, &c_full[st]);
-          bulk_load(to + kStKs, p.p.ks + row * kKv4Scales, n * kKv4Scales, &c_full[st]);
-          bulk_load(to + kStVs, p.p.vs + row * kKv4Scales, n * kKv4Scales, &c_full[st]);
+        if (lane == 0) {   // two copies a tile: what a bulk copy costs hardly depends on its size
+          // tiles of a pair's block: K, V; of a single's two blocks: Ka, Kb, Va, Vb
+          const bool is_v = single ? (x >> 1) & 1 : x & 1;
+          const int key0 = (block0 + (single ? (x >> 2) * 2 + (x & 1) : x >> 1)) * kKB;
+          const int n = max(0, min(kKB, p.cap - key0));   // a multiple of 8; 0: a single's block behind the cache
+          unsigned char* to = raw_smem + st * kRawBytes;
+          const size_t row = plane + key0;
+          mbar_arrive_expect_tx(&r_full[st], n * (kKv4Codes + kKv4Scales));
+          if (n > 0) {
+            bulk_load(to, (is_v ? p.p.vc : p.p.kc) + row * kKv4Codes, n * kKv4Codes, &r_full[st]);
+            bulk_load(to + kRawScales, (is_v ? p.p.vs : p.p.ks) + row * kKv4Scales, n * kKv4Scales, &r_full[st]);
+          }
         }
         __syncwarp();
-        if (lane < n / 8) bulk_load(to + kStVc + lane * kOctet, p.p.vc + (row + lane * 8) * kKv4Codes, 8 * kKv4Codes, &c_full[st]);
+        ++j;
+        if (++st == kRaw) { st = 0; phase ^= 1; }
       }
     }
     // every copy must have landed before the CTA may exit
-    for (int i = j - kNS > 0 ? j - kNS : 0; i < j; ++i) mbar_wait(&c_full[i % kNS], (i / kNS) & 1, nullptr, 0);
+    for (int i = max(0, j - kRaw); i < j; ++i) kv4_wait(&r_full[i % kRaw], (i / kRaw) & 1, nullptr, 0);
   } else if (warp >= kDec0 && warp < kMmaWarp) {
     // ---------------------------------------------------------------- decode
-    const int w = warp - kDec0;
-    int j = 0;
-    bool ok = any;
-    while (ok && walk.next(p, sg)) {
-      for (int i = 0; i < sg.count; ++i, ++j) {
-        const int st = j % kNS, buf = j & 1;
-        const uint32_t free_parity = ((j >> 1) & 1) ^ 1;
-        ok = mbar_wait(&c_full[st], (j / kNS) & 1, p.status, 61) && mbar_wait(&k_empty[buf], free_parity, p.status, 62);
+    regs_down<kDecRegs>();
+    // Half a key per lane: two 16-byte pieces (32 dimensions each), in an order that spreads the
+    // lanes of a phase over all banks, both when reading and when writing.
+    const int key = (warp - kDec0) * 16 + (lane & 15);
+    const int c0 = ((lane >> 4) + (lane >> 1)) & 3, c1 = c0 ^ 2;   // the two pieces
+    // swizzled place of a piece's first 8 dimensions; the e-th 8 lie at the place XOR 16 e
+    auto place = [&](int c) { return key * 128 + (c >> 1) * (kTile / 2) + ((((c & 1) * 4) ^ (key & 7)) * 16); };
+    const int src0 = key * kKv4Codes + c0 * 16, src1 = key * kKv4Codes + c1 * 16;
+    const int sc0 = kRawScales + key * kKv4Scales + c0 * 2, sc1 = kRawScales + key * kKv4Scales + c1 * 2;
+    const uint32_t dst0 = smem_u32(t_smem) + place(c0), dst1 = smem_u32(t_smem) + place(c1);
+    int st = 0, st_phase = 0, buf = 0, buf_phase = 0;
+    while (true) {
+      const Kv4Seg& sg = take();
+      const int tiles = sg.count * (sg.single ? 4 : 2);
+      give_back();
+      if (!ok || tiles == 0) break;
+      for (int x = 0; x < tiles; ++x) {
+        ok = kv4_wait(&r_full[st], st_phase, p.status, 61) && kv4_wait(&t_empty[buf], buf_phase ^ 1, p.status, 62);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        const unsigned char* from = codes + st * kStage;
-        {
-          // K: one key per lane; its four 16-byte pieces in an order that spreads the lanes
-          // of a phase over all banks, both when reading and when writing
-          const int key = w * 32 + lane;
-          unsigned char* dst = k_smem + buf * kTile + key * 128;
+        const unsigned char* from = raw_smem + st * kRawBytes;
+        const uint4 v0 = *reinterpret_cast<const uint4*>(from + src0), v1 = *reinterpret_cast<const uint4*>(from + src1);
+        const uint32_t two0 = *reinterpret_cast<const uint16_t*>(from + sc0), two1 = *reinterpret_cast<const uint16_t*>(from + sc1);
+        auto piece = [&](const uint4& v, uint32_t two, uint32_t dst) {
+          const uint32_t s0 = e4m3x2_to_f16((two & 0xFFu) * 0x00010001u), s1 = e4m3x2_to_f16((two >> 8) * 0x00010001u);
+          const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int cc = (c + (lane >> 1)) & 3;
-            const uint4 x = *reinterpret_cast<const uint4*>(from + kStKc + key * kKv4Codes + cc * 16);
-            const uint32_t two = *reinterpret_cast<const uint16_t*>(from + kStKs + key * kKv4Scales + cc * 2);
-            const uint32_t s0 = e4m3x2_to_f16((two & 0xFFu) * 0x00010001u), s1 = e4m3x2_to_f16((two >> 8) * 0x00010001u);
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t f[4];
-              e2m1x8_to_f16(xs[e], f);
-              const uint32_t sc = e < 2 ? s0 : s1;
-              const int pos = ((cc & 1) * 4 + e) ^ (key & 7);
-              *reinterpret_cast<uint4*>(dst + (cc >> 1) * (kTile / 2) + pos * 16) =
-                  make_uint4(hmul2(f[0], sc), hmul2(f[1], sc), hmul2(f[2], sc), hmul2(f[3], sc));
-            }
+          for (int e = 0; e < 4; ++e) {
+            uint32_t f[4];
+            e2m1x8_to_f16(vs[e], f);
+            const uint32_t sc = e < 2 ? s0 : s1;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst ^ (16 * e)), "r"(hmul2(f[0], sc)),
+                         "r"(hmul2(f[1], sc)), "r"(hmul2(f[2], sc)), "r"(hmul2(f[3], sc)) : "memory");
           }
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&k_full[buf]);
-        ok = mbar_wait(&v_empty[buf], free_parity, p.status, 63);
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        {
-          // V: 8 keys (octet 8 (w / 2) + lane % 8) x 16 dimensions (block 4 (w % 2) + lane / 8)
-          const int o8 = lane & 7, blk = (w & 1) * 4 + (lane >> 3), oct = (w >> 1) * 8 + o8;
-          uint2 x[8];
-          uint32_t sc[4];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] = *reinterpret_cast<const uint2*>(from + kStVc + oct * kOctet + k * kKv4Codes + blk * 8);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const unsigned char* sp = from + kStVs + (oct * 8 + 2 * k) * kKv4Scales + blk;
-            sc[k] = e4m3x2_to_f16((uint32_t)sp[0] | ((uint32_t)sp[kKv4Scales] << 16));
-          }
-          unsigned char* dst = v_smem + buf * kTile + (w >> 1) * (kTile / 2) + blk * 16 * 128;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t ev[4][4], od[4][4];   // [pair of keys][even or odd dimension]
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t a = h ? x[2 * k].y : x[2 * k].x, b = h ? x[2 * k + 1].y : x[2 * k + 1].x;
-              e2m1x8_to_f16((a & 0x0F0F0F0Fu) | ((b & 0x0F0F0F0Fu) << 4), ev[k]);
-              e2m1x8_to_f16(((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u), od[k]);
-            }
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              const int d0 = h * 8 + 2 * m;   // row of the tile, modulo 16
-              *reinterpret_cast<uint4*>(dst + d0 * 128 + (o8 ^ (d0 & 7)) * 16) =
-                  make_uint4(hmul2(ev[0][m], sc[0]), hmul2(ev[1][m], sc[1]), hmul2(ev[2][m], sc[2]), hmul2(ev[3][m], sc[3]));
-              *reinterpret_cast<uint4*>(dst + (d0 + 1) * 128 + (o8 ^ ((d0 + 1) & 7)) * 16) =
-                  make_uint4(hmul2(od[0][m], sc[0]), hmul2(od[1][m], sc[1]), hmul2(od[2][m], sc[2]), hmul2(od[3][m], sc[3]));
-            }
-          }
-        }
+        };
+        piece(v0, two0, dst0 + buf * kTile);
+        piece(v1, two1, dst1 + buf * kTile);
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&v_full[buf]);
-          mbar_arrive(&c_empty[st]);
+          mbar_arrive(&t_full[buf]);
+          mbar_arrive(&r_empty[st]);
         }
+        if (++st == kRaw) { st = 0; st_phase ^= 1; }
+        if (++buf == kTiles) { buf = 0; buf_phase ^= 1; }
       }
+      if (!ok) break;
     }
-  } else if (warp == kMmaWarp) {
-    // ---------------------------------------------------------------- MMA issuer
-    // The warp runs in lockstep (every decision is a vote); one elected lane issues.
-    constexpr uint32_t idesc = idesc_f16_f32(128, 128);
-    const uint32_t qa = smem_u32(q_smem);
+  } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+    // ---------------------------------------------------------------- MMA issuers
+    // Warp w issues the products of stream w: while one waits on a barrier the other's MMAs run.
+    // A warp runs in lockstep and one elected lane issues.  Whatever an MMA's operands depend on
+    // is made warp-uniform (a reduction's result is): operands in ordinary registers cost some
+    // 100 cycles an MMA.
+    constexpr uint32_t idesc_s = idesc_f16_f32(128, 128, false), idesc_pv = idesc_f16_f32(128, 128, true);
+    const int w = __reduce_max_sync(0xffffffffu, warp - kMmaWarp);
     const bool leader = elect_one();
-    bool ok = any;
-    int s_next = 0, pv_next = 0, n_seg = 0;
-    while (ok && walk.next(p, sg)) {
-      const int end = s_next + sg.count, first = s_next;
-      ok = mbar_wait(&q_full, n_seg & 1, p.status, 64);
-      // the epilogue has read the previous unit's O
-      if (n_seg > 0) ok = mbar_wait(&o_free, (n_seg - 1) & 1, p.status, 65) && ok;
-      ok = __all_sync(0xffffffffu, ok);
+    bool issued = false;
+    const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
+    const uint32_t tm_s = tm + kSCol + w * 128, tm_o = tm + kOCol + w * 128;
+    const uint64_t q_desc = sdesc_kmajor_sw128(smem_u32(q_smem + w * kTile)), k_desc = sdesc_kmajor_sw128(smem_u32(t_smem)),
+                   v_desc = sdesc_mnmajor_sw128(smem_u32(t_smem));
+    int slot = 0, phase = 0;   // ring place and phase of the segment's next stage's first tile
+    int n_p = 0;               // P blocks seen so far
+    // K-major: 16-byte units between the operands of two 16-wide steps
+    constexpr uint32_t kStep = 32 >> 4, kSlab = (kTile / 2) >> 4;
+    // the d-th tile from the stage's first: ring place, phase
+    auto at = [&](int d, int& sl, int& ph) {
+      sl = slot + d;
+      ph = phase;
+      while (sl >= kTiles) { sl -= kTiles; ph ^= 1; }
+    };
+    // waits for two barriers, whose first tests overlap
+    auto wait2 = [&](uint64_t* b0, int p0, uint64_t* b1, int p1, int id) {
+      const bool r0 = mbar_try_wait(b0, p0 & 1), r1 = mbar_try_wait(b1, p1 & 1);
+      bool r = r0 || kv4_wait_slow(b0, p0 & 1, p.status, id);
+      r = (r1 || kv4_wait_slow(b1, p1 & 1, p.status, id)) && r;
+      ok = __all_sync(0xffffffffu, ok && r);
       tc_fence_after();
-      ++n_seg;
-      int idle = 0;
-      uint64_t t_idle = 0;
-      const uint64_t limit = wait_limit(p.status);
-      while (ok && pv_next < end) {
-        if (s_next < end && s_next - pv_next < kSBufs &&
-            __any_sync(0xffffffffu, mbar_test_wait(&k_full[s_next & 1], (s_next >> 1) & 1))) {
-          tc_fence_after();
-          const uint32_t kb = smem_u32(k_smem + (s_next & 1) * kTile);
-          if (leader) {
+      return ok;
+    };
+    // a tile is free again when both streams have read it; one that a single stream reads is
+    // released twice by it
+    auto release = [&](int sl, int single) {
+      mma_commit(&t_empty[sl]);
+      if (single) mma_commit(&t_empty[sl]);
+    };
+    auto issue_s = [&](int sl, int single) {
+      if (leader) {
+        const uint64_t kd = k_desc + sl * (kTile >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              const uint32_t off = (kk >> 2) * (kTile / 2) + (kk & 3) * 32;
-              mma_bf16(tmem + (s_next % kSBufs) * 128, sdesc_kmajor_sw128(qa + off), sdesc_kmajor_sw128(kb + off), idesc,
-                       kk > 0 ? 1u : 0u);
-            }
-            mma_commit(&s_full[s_next % kSBufs]);
-            mma_commit(&k_empty[s_next & 1]);
-          }
-          __syncwarp();
-          ++s_next;
-        } else if (pv_next < s_next &&
-                   __any_sync(0xffffffffu, mbar_test_wait(&p_full[pv_next % kSBufs], (pv_next / kSBufs) & 1) &&
-                                               mbar_test_wait(&v_full[pv_next & 1], (pv_next >> 1) & 1))) {
-          tc_fence_after();
-          const uint32_t vb = smem_u32(v_smem + (pv_next & 1) * kTile);
-          const uint32_t pt = tmem + (pv_next % kSBufs) * 128;
-          if (leader) {
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              constexpr int kPer = kCols / 16;   // 16-key steps of one column group
-              const uint32_t off = (kk >> 2) * (kTile / 2) + (kk & 3) * 32;
-              mma_bf16_ts(tmem + kOCol, pt + (kk / kPer) * kCols + (kk % kPer) * 8, sdesc_kmajor_sw128(vb + off), idesc,
-                          (pv_next > first || kk > 0) ? 1u : 0u);
-            }
-            mma_commit(&o_done[pv_next % kSBufs]);
-            mma_commit(&v_empty[pv_next & 1]);
-          }
-          __syncwarp();
-          ++pv_next;
-        } else {
-          if ((++idle & 1023) == 0) {   // bounded: give up after the wait limit without progress
-            const uint64_t now = __shfl_sync(0xffffffffu, globaltimer(), 0);
-            if (t_idle == 0) t_idle = now;
-            else if (now - t_idle > limit) {
-              if (leader) set_status(p.status, DF_ERR_TIMEOUT, 66);
-              ok = false;
-            }
-            if (__any_sync(0xffffffffu, p.status && *(volatile int*)p.status == DF_ERR_TIMEOUT)) ok = false;
-          }
-          continue;
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = (kk >> 2) * kSlab + (kk & 3) * kStep;
+          mma_bf16(tm_s, q_desc + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
         }
-        idle = 0;
-        t_idle = 0;
+        mma_commit(&s_full[w]);
+        release(sl, single);
       }
-    }
-    if (!ok && s_next > 0) {   // giving up: the MMAs issued must finish before TMEM is freed
-      if (leader) mma_commit(&drain);
       __syncwarp();
-      mbar_wait(&drain, 0, nullptr, 0);
+      issued = true;
+    };
+    auto issue_pv = [&](int sl, int single, bool first, bool last) {
+      if (leader) {
+        const uint64_t vd = v_desc + sl * (kTile >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          // keys 16 kk ..: 16 rows of 128 bytes further
+          mma_bf16_ts(tm_o, tm_s + kk * 8, vd + kk * (2048 >> 4), idesc_pv, (!first || kk > 0) ? 1u : 0u);
+        }
+        if (last) mma_commit(&o_full[w]);
+        release(sl, single);
+      }
+      __syncwarp();
+    };
+    while (true) {
+      // tiles of a stage: pair K, V; single Ka, Kb, Va, Vb
+      const Kv4Seg& sg = take();
+      const int single = __reduce_max_sync(0xffffffffu, sg.single), count = __reduce_max_sync(0xffffffffu, sg.count);
+      give_back();
+      if (!ok || count == 0) break;
+      const int per = single ? 4 : 2, k_at = single ? w : 0, v_at = single ? 2 + w : 1;
+      int sl, ph;
+      // Q is there, and with it the epilogue has read the previous unit's O
+      at(k_at, sl, ph);
+      if (wait2(&q_full[w], n_seg - 1, &t_full[sl], ph, 63)) {
+        // stream 1 starts half a block behind stream 0, and stays there: each has the
+        // exponentials to itself while the other has the tensor core
+        if (w == 1) pause(kStagger);
+        issue_s(sl, single);
+      }
+      for (int i = 0; i < count && ok; ++i) {
+        at(v_at, sl, ph);
+        if (!wait2(&p_full[w], n_p++, &t_full[sl], ph, 64)) break;
+        issue_pv(sl, single, i == 0, i + 1 == count);
+        at(per, sl, ph);
+        slot = sl;
+        phase = ph;
+        if (i + 1 < count) {
+          at(k_at, sl, ph);
+          if (wait2(&t_full[sl], ph, &t_full[sl], ph, 65)) issue_s(sl, single);
+        }
+      }
+      if (!ok) break;
+    }
+    if (!ok && issued) {   // giving up: the MMAs issued must finish before TMEM is freed
+      if (leader) mma_commit(&drain[w]);
+      __syncwarp();
+      kv4_wait(&drain[w], 0, nullptr, 0);
     }
   } else {
     // ---------------------------------------------------------------- softmax, epilogue
-    // Warp w: TMEM lanes 32 (w % 4) .. + 31, one query row per thread, columns 64 (w / 4) .. + 63
-    // of S (keys) and of O (dimensions).
-    const int grp = warp >> 2;
-    const int r = (warp & 3) * 32 + lane;
-    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    constexpr float kRescale = 8.f;
-    bool ok = any;
-    int j = 0;
-    while (ok && walk.next(p, sg)) {
-      const int row = sg.rt * 128 + r, node = row / p.G;
-      const bool row_ok = node < p.T;
-      const bool live = __any_sync(0xffffffffu, row_ok);
+    // Stream w; the warp's rows are 32 (warp % 4) .. + 31 of it, a thread owns the row of its
+    // TMEM lane.
+    regs_up<kSoftRegs>();
+    const int w = warp >> 2, r0 = (warp & 3) * 32;
+    const uint32_t sp = tmem + ((uint32_t)r0 << 16) + kSCol + w * 128, oaddr = sp - kSCol + kOCol;
+    int n_s = 0;   // S blocks seen so far
+    while (true) {
+      const Kv4Seg& sg = take();   // given back behind the epilogue
+      if (!ok || sg.count == 0) break;
+      const int row0 = sg.rt * p.R + (sg.single ? 0 : w * 128);   // the stream's first row
+      const bool live = row0 + r0 < p.T * p.G;                    // the warp has a row
       if (sg.len == 0 && threadIdx.x == 0) set_status(p.status, DF_ERR_CAPACITY, sg.s);
-      const size_t grow = ((size_t)sg.s * p.T + node) * p.Hq + sg.kvh * p.G + row % p.G;
-      // Q: the row, brought to fp16 by a power of two, into its swizzled place; every S of the
-      // previous unit is complete (its scores were read)
+      // Q into its swizzled places as bf16 (16 lanes a row), then every lane brings its own row to
+      // fp16 by a power of two; every S of the previous unit is complete (o_full).
       float qs;
       {
-        uint4 raw[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) raw[c] = make_uint4(0u, 0u, 0u, 0u);
-        if (row_ok) {
-          const uint4* src = reinterpret_cast<const uint4*>(p.q + grow * 128 + grp * 64);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) raw[c] = src[c];
+        const Rows rows(p, sg.s, sg.kvh, row0 + r0);
+        const uint32_t box = smem_u32(q_smem + w * kTile + r0 * 128);
+        const int c = lane & 15;
+#pragma unroll 2
+        for (int i = 0; i < 16; ++i) {
+          const int lr = i * 2 + (lane >> 4);
+          const long long at = rows.index(p, lr);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"   // no bytes: zeros
+                       ::"r"(box + (c >> 3) * (kTile / 2) + lr * 128 + (((c & 7) ^ (lr & 7)) * 16)),
+                         "l"(p.q + (at < 0 ? 0 : at) * 128 + c * 8), "r"(at < 0 ? 0 : 16) : "memory");
         }
-        float amax = 0.f;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint32_t x[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        unsigned char* mine = q_smem + w * kTile + (r0 + lane) * 128;
+        auto place = [&](int i) { return reinterpret_cast<uint4*>(mine + (i >> 3) * (kTile / 2) + (((i & 7) ^ (lane & 7)) * 16)); };
+        float amax = 0.f, back;
+#pragma unroll 2
+        for (int i = 0; i < 16; ++i) {
+          const uint4 v = *place(i);
+          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xFFFF0000u))));
+            amax = max3(amax, fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xFFFF0000u)));
         }
-        red_sum[grp][r] = amax;
-        soft_sync();
-        float back;
-        const float f = f16_row_factor(fmaxf(red_sum[0][r], red_sum[1][r]), back);
+        const float f = f16_row_factor(amax, back);
         qs = p.scale2 * back;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint32_t x[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll 2
+        for (int i = 0; i < 16; ++i) {
+          const uint4 v = *place(i);
+          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
           uint32_t h[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) h[e] = pack_f16x2(__uint_as_float(x[e] << 16) * f, __uint_as_float(x[e] & 0xFFFF0000u) * f);
-          *reinterpret_cast<uint4*>(q_smem + grp * (kTile / 2) + r * 128 + ((c ^ (r & 7)) * 16)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *place(i) = make_uint4(h[0], h[1], h[2], h[3]);
         }
         fence_proxy_async();
-        mbar_arrive(&q_full);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[w]);
       }
-      const uint32_t* anc_row = p.anc && row_ok ? p.anc + ((size_t)sg.s * p.T + node) * p.W : nullptr;
-      // no row of the tile has its mask before this key
-      const int edge_key = sg.len == 0 ? 0 : p.anc ? sg.N : sg.N + min(p.T - 1, sg.rt * 128 / p.G) + 1;
-      float m_run = -INFINITY, l_part = 0.f;   // the maximum in raw scores
-      for (int i = 0; i < sg.count; ++i, ++j) {
-        const bool w1 = __all_sync(0xffffffffu, mbar_wait(&s_full[j % kSBufs], (j / kSBufs) & 1, p.status, 67));
-        float sv[kCols];
-        float mpart = -INFINITY;
-        const uint32_t sp = tmem + lane_base + (j % kSBufs) * 128 + grp * kCols;
-        if (w1) {
-          tc_fence_after();
-#pragma unroll
-          for (int c = 0; c < kCols; c += 16) tmem_ld16(sp + c, sv + c);
-          tmem_ld_wait();
-          const int key0 = (sg.tile0 + i) * kKB + grp * kCols;
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          if ((sg.tile0 + i + 1) * kKB > edge_key) {
-            uint32_t adm[kCols / 32];
-#pragma unroll
-            for (int x = 0; x < kCols / 32; ++x)
-              adm[x] = row_ok && (anc_row || !p.anc) ? see_bits(anc_row, p.W, sg.N, key0 + 32 * x, node, sg.len) : 0u;
-#pragma unroll
-            for (int c = 0; c < kCols; ++c) {
-              if (!((adm[c >> 5] >> (c & 31)) & 1u)) sv[c] = -INFINITY;
-              m4[c & 3] = fmaxf(m4[c & 3], sv[c]);
+      // no row of the stream has its mask before this key
+      const int edge_key = sg.len == 0 ? 0 : p.anc ? sg.N : sg.N + min(p.T - 1, row0 / p.G) + 1;
+      float m_run = -INFINITY, l = 0.f;   // the maximum in raw scores, the sum
+      const int count = sg.count, stride = sg.single ? 2 * kKB : kKB;
+      int key0 = (sg.tile0 * (sg.single ? 2 : 1) + (sg.single ? w : 0)) * kKB;
+      for (int i = 0; i < count; ++i, ++n_s, key0 += stride) {
+        ok = __all_sync(0xffffffffu, kv4_wait(&s_full[w], n_s & 1, p.status, 67));
+        if (!ok) break;
+        tc_fence_after();
+        if (live) {
+          // the mask first: its code is out of line, and the scores fill the registers
+          const bool edge = key0 + kKB > edge_key;
+          uint32_t adm[4] = {0u, 0u, 0u, 0u};
+          if (edge) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {   // one copy of the code
+              const uint32_t x = row_bits(p, sg, row0 + r0, lane, key0 + 32 * c);
+              adm[0] = c == 0 ? x : adm[0]; adm[1] = c == 1 ? x : adm[1];
+              adm[2] = c == 2 ? x : adm[2]; adm[3] = c == 3 ? x : adm[3];
             }
-          } else {
-#pragma unroll
-            for (int c = 0; c < kCols; ++c) m4[c & 3] = fmaxf(m4[c & 3], sv[c]);
           }
-          mpart = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          float sv[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(sp + c * 32, reinterpret_cast<float(&)[32]>(sv[c * 32]));
+          tmem_ld_wait();
+          if (edge) {
+#pragma unroll
+            for (int e = 0; e < 128; ++e)
+              if (!((adm[e >> 5] >> (e & 31)) & 1u)) sv[e] = -INFINITY;
+          }
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < 128; e += 2) m4[(e >> 1) & 3] = max3(m4[(e >> 1) & 3], sv[e], sv[e + 1]);
+          const float mx = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
+          float alpha = 1.f;
+          if ((mx - m_run) * qs > 8.f) {           // also on the first key a row sees
+            alpha = ex2_approx((m_run - mx) * qs);
+            m_run = mx;
+            l *= alpha;
+          }
+          if (i >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) scale_rows(oaddr, alpha);
+          const float mb = m_run == -INFINITY ? kTcShift : kTcShift - m_run * qs;
+          const uint64_t qs2 = pack2(qs, qs), mb2 = pack2(mb, mb);
+          uint64_t sum[2] = {0, 0};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float pf[16];   // 32 probabilities as fp16, over the scores' own place
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float y0, y1;
+              unpack2(fma2(pack2(sv[c * 32 + e], sv[c * 32 + e + 1]), qs2, mb2), y0, y1);
+              y0 = ex2_approx(y0);
+              y1 = ex2_approx(y1);
+              sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pack2(y0, y1));
+              pf[e >> 1] = __uint_as_float(pack_f16x2(y0, y1));
+            }
+            tmem_st16(sp + c * 16, pf);
+          }
+          float y0, y1;
+          unpack2(add2(sum[0], sum[1]), y0, y1);
+          l += y0 + y1;
         } else {
+          float pf[16];
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) sv[c] = -INFINITY;
+          for (int e = 0; e < 16; ++e) pf[e] = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) tmem_st16(sp + c * 16, pf);
         }
-        red_max[j & 1][grp][r] = mpart;
-        if (!soft_and(w1 && ok)) { ok = false; break; }
-        const float mx = fmaxf(red_max[j & 1][0][r], red_max[j & 1][1][r]);
-        float alpha = 1.f;
-        if ((mx - m_run) * qs > kRescale) {           // also on the first key a row sees
-          alpha = ex2_approx((m_run - mx) * qs);
-          m_run = mx;
-        }
-        uint32_t packed[kCols / 2];
-        if (live && m_run != -INFINITY) {
-          const float mb = kTcShift - m_run * qs;
-          float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < kCols; c += 4) {
-            const float p0 = ex2_approx(fmaf(sv[c], qs, mb)), p1 = ex2_approx(fmaf(sv[c + 1], qs, mb));
-            const float p2 = ex2_approx(fmaf(sv[c + 2], qs, mb)), p3 = ex2_approx(fmaf(sv[c + 3], qs, mb));
-            s4[(c >> 2) & 3] += (p0 + p1) + (p2 + p3);
-            packed[c >> 1] = pack_f16x2(p0, p1);
-            packed[(c >> 1) + 1] = pack_f16x2(p2, p3);
-          }
-          l_part = l_part * alpha + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
-        } else {
-#pragma unroll
-          for (int c = 0; c < kCols / 2; ++c) packed[c] = 0u;
-        }
-        if (i >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
-          // O must hold PV of every earlier block before it is rescaled
-          ok = mbar_wait(&o_done[(j - 1) % kSBufs], ((j - 1) / kSBufs) & 1, p.status, 68) && ok;
-          ok = __all_sync(0xffffffffu, ok);
-          tc_fence_after();
-          const uint32_t oaddr = tmem + lane_base + kOCol + grp * kCols;
-#pragma unroll
-          for (int c = 0; c < kCols; c += 16) {
-            float o[16];
-            tmem_ld16(oaddr + c, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] *= alpha;
-            tmem_st16(oaddr + c, o);
-          }
-        }
-        tmem_st32(sp, packed);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&p_full[j % kSBufs]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[w]);
       }
       if (!ok) break;
       // -------------------------------------------------------------- epilogue
-      ok = mbar_wait(&o_done[(j - 1) % kSBufs], ((j - 1) / kSBufs) & 1, p.status, 69) && ok;
-      red_sum[grp][r] = l_part;
-      if (!soft_and(ok)) { ok = false; break; }
+      ok = __all_sync(0xffffffffu, kv4_wait(&o_full[w], (n_seg - 1) & 1, p.status, 69));
+      if (!ok) break;
       tc_fence_after();
-      const float l = red_sum[0][r] + red_sum[1][r];
       const float m2 = m_run == -INFINITY ? -INFINITY : m_run * qs;
-      const uint32_t oaddr = tmem + lane_base + kOCol + grp * kCols;
-      const bool whole = sg.first && sg.last;
+      const bool whole = sg.first && sg.last && !sg.single;
       const float inv = l > 0.f ? p.v_mul / l : 0.f;
-      const size_t at = (size_t)(blockIdx.x + sg.unit) * 128 + r;
+      const size_t at = (size_t)(blockIdx.x + sg.unit) * p.R + w * 128 + r0;   // the warp's first row in the parts
+      // O goes out by way of the warp's own rows of Q, which no product reads any more: 32 rows x
+      // 128 bytes, swizzled, then 8 lanes write a row's 128 bytes
       if (live) {
-#pragma unroll
-        for (int c = 0; c < kCols; c += 16) {
-          float o[16];
-          tmem_ld16(oaddr + c, o);
+        const Rows rows(p, sg.s, sg.kvh, row0 + r0);
+        unsigned char* box = q_smem + w * kTile + r0 * 128;
+        const int sw = lane & 7;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          float o[32];
+          tmem_ld32(oaddr + c * 32, o);
           tmem_ld_wait();
-          if (row_ok && whole) {
-            uint32_t x[8];
+          if (whole) {   // bf16: two of the four make one row of 128 bytes
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
-            uint4* dst = reinterpret_cast<uint4*>(p.out + grow * 128 + grp * kCols + c);
-            dst[0] = make_uint4(x[0], x[1], x[2], x[3]);
-            dst[1] = make_uint4(x[4], x[5], x[6], x[7]);
-          } else if (row_ok) {
-            float4* dst = reinterpret_cast<float4*>(p.o_part + at * 128 + grp * kCols + c);
+            for (int e = 0; e < 4; ++e) {
+              uint32_t x[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+              for (int y = 0; y < 4; ++y) x[y] = pack_bf16x2(o[8 * e + 2 * y] * inv, o[8 * e + 2 * y + 1] * inv);
+              *reinterpret_cast<uint4*>(box + lane * 128 + ((((c & 1) * 4 + e) ^ sw) * 16)) = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+            if ((c & 1) == 0) continue;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<float4*>(box + lane * 128 + ((e ^ sw) * 16)) =
+                  make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
+          __syncwarp();
+#pragma unroll 2
+          for (int i = 0; i < 8; ++i) {
+            const int lr = i * 4 + (lane >> 3);
+            const long long to = rows.index(p, lr);
+            const uint4 v = *reinterpret_cast<const uint4*>(box + lr * 128 + (((lane & 7) ^ (lr & 7)) * 16));
+            if (to >= 0)
+              *reinterpret_cast<uint4*>(whole ? reinterpret_cast<unsigned char*>(p.out + to * 128 + (c >> 1) * 64 + (lane & 7) * 8)
+                                              : reinterpret_cast<unsigned char*>(p.o_part + (at + lr) * 128 + c * 32 + (lane & 7) * 4)) = v;
+          }
+          __syncwarp();
         }
-        if (row_ok && grp == 0) {
-          if (!whole) p.ml_part[at] = make_float2(m2, l);
-          else if (p.lse) p.lse[grow] = kv4_lse(m2, l, kTcShift);
+        const long long to = rows.index(p, lane);
+        if (to >= 0) {
+          if (!whole) p.ml_part[at + lane] = make_float2(m2, l);
+          else if (p.lse) p.lse[to] = kv4_lse(m2, l, kTcShift);
         }
       }
       if (threadIdx.x == 0) {
-        if (whole) p.range[sg.unit] = make_int2(0, 0);
-        else if (sg.first) p.range[sg.unit].x = blockIdx.x;
-        else if (sg.last) p.range[sg.unit].y = blockIdx.x;
+        if (sg.first) p.range[sg.unit].x = blockIdx.x;
+        if (sg.last) p.range[sg.unit].y = blockIdx.x;
       }
       tc_fence_before();
-      soft_sync();   // red_sum is read before the next unit writes it
-      mbar_arrive(&o_free);
+      give_back();
     }
   }
   tc_fence_before();
@@ -477,8 +592,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const Kv4AttnP
 
 int launch_kv4_attn_tc(Kv4AttnParams p, cudaStream_t st) {
   p.shift = kTcShift;
-  const size_t smem = 1024 + 5 * kTile + kNS * kStage;
+  const size_t smem = 1024 + (2 + kTiles) * kTile + kRaw * kRawBytes;
   if (ensure_dynamic_smem(kv4_attn_tc_kernel, smem) != cudaSuccess) return DF_ERR_CUDA;
+  static const int regs = [] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, kv4_attn_tc_kernel) == cudaSuccess ? at.numRegs : 0;
+  }();
+  if (regs < kLaunchRegs) return DF_ERR_CUDA;   // setmaxnreg would wait for registers that are not there
   launch_k(kv4_attn_tc_kernel, dim3(p.n_cta), dim3(kThreads), smem, st, p);
   return cudaGetLastError() == cudaSuccess ? DF_OK : DF_ERR_CUDA;
 }
