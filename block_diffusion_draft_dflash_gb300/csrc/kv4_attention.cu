@@ -375,6 +375,7 @@ void kv4_attn_plan(int T, int G, Kv4AttnParams& p) {
   p.last_single = p.R == 256 && rows - (long long)(p.nrt - 1) * p.R <= 128;
   p.stage_log2 = p.R == 256 ? 7 : 5;
   p.min_stages = p.R == 256 ? 2 : kWarps;
+  p.change_step = p.R == 256 ? 1 : 2;
   p.n_cta = num_sms() * (p.R == 16 ? 2 : 1);
 }
 size_t up16(size_t x) { return (x + 15) & ~(size_t)15; }

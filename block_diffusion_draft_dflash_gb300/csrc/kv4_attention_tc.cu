@@ -313,13 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const __grid_c
       ph = phase;
       while (sl >= kTiles) { sl -= kTiles; ph ^= 1; }
     };
-    // waits for two barriers, whose first tests overlap
-    auto wait2 = [&](uint64_t* b0, int p0, uint64_t* b1, int p1, int id) {
-      const bool r0 = mbar_try_wait(b0, p0 & 1), r1 = mbar_try_wait(b1, p1 & 1);
-      bool r = r0 || kv4_wait_slow(b0, p0 & 1, p.status, id);
-      r = (r1 || kv4_wait_slow(b1, p1 & 1, p.status, id)) && r;
-      ok = __all_sync(0xffffffffu, ok && r);
-      tc_fence_after();
+    auto wait = [&](uint64_t* bar, int parity, int id) {
+      ok = __all_sync(0xffffffffu, ok && kv4_wait(bar, parity & 1, p.status, id));
       return ok;
     };
     // a tile is free again when both streams have read it; one that a single stream reads is
@@ -365,23 +360,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const __grid_c
       int sl, ph;
       // Q is there, and with it the epilogue has read the previous unit's O
       at(k_at, sl, ph);
-      if (wait2(&q_full[w], n_seg - 1, &t_full[sl], ph, 63)) {
+      if (wait(&t_full[sl], ph, 63) && wait(&q_full[w], n_seg - 1, 63)) {
+        tc_fence_after();
         // stream 1 starts half a block behind stream 0, and stays there: each has the
         // exponentials to itself while the other has the tensor core
         if (w == 1) pause(kStagger);
         issue_s(sl, single);
       }
       for (int i = 0; i < count && ok; ++i) {
-        at(v_at, sl, ph);
-        if (!wait2(&p_full[w], n_p++, &t_full[sl], ph, 64)) break;
-        issue_pv(sl, single, i == 0, i + 1 == count);
+        const bool more = i + 1 < count;
+        int vs, vp;
+        at(v_at, vs, vp);
         at(per, sl, ph);
         slot = sl;
         phase = ph;
-        if (i + 1 < count) {
-          at(k_at, sl, ph);
-          if (wait2(&t_full[sl], ph, &t_full[sl], ph, 65)) issue_s(sl, single);
-        }
+        at(k_at, sl, ph);
+        if (!wait(&t_full[vs], vp, 64) || !wait(&p_full[w], n_p++, 65)) break;
+        tc_fence_after();
+        // K is mostly there by now: then S follows without another wait
+        const bool ready = __any_sync(0xffffffffu, mbar_test_wait(&t_full[sl], ph));
+        issue_pv(vs, single, i == 0, !more);
+        if (!more) break;
+        if (!ready && !wait(&t_full[sl], ph, 66)) break;
+        tc_fence_after();
+        issue_s(sl, single);
       }
       if (!ok) break;
     }
@@ -411,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const __grid_c
         const Rows rows(p, sg.s, sg.kvh, row0 + r0);
         const uint32_t box = smem_u32(q_smem + w * kTile + r0 * 128);
         const int c = lane & 15;
-#pragma unroll 2
+#pragma unroll 4
         for (int i = 0; i < 16; ++i) {
           const int lr = i * 2 + (lane >> 4);
           const long long at = rows.index(p, lr);
@@ -424,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const __grid_c
         unsigned char* mine = q_smem + w * kTile + (r0 + lane) * 128;
         auto place = [&](int i) { return reinterpret_cast<uint4*>(mine + (i >> 3) * (kTile / 2) + (((i & 7) ^ (lane & 7)) * 16)); };
         float amax = 0.f, back;
-#pragma unroll 2
+#pragma unroll 4
         for (int i = 0; i < 16; ++i) {
           const uint4 v = *place(i);
           const uint32_t x[4] = {v.x, v.y, v.z, v.w};
@@ -434,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const __grid_c
         }
         const float f = f16_row_factor(amax, back);
         qs = p.scale2 * back;
-#pragma unroll 2
+#pragma unroll 4
         for (int i = 0; i < 16; ++i) {
           const uint4 v = *place(i);
           const uint32_t x[4] = {v.x, v.y, v.z, v.w};
@@ -527,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const __grid_c
       tc_fence_after();
       const float m2 = m_run == -INFINITY ? -INFINITY : m_run * qs;
       const bool whole = sg.first && sg.last && !sg.single;
-      const float inv = l > 0.f ? p.v_mul / l : 0.f;
+      const float inv = m_run == -INFINITY ? 0.f : p.v_mul / l;
       const size_t at = (size_t)(blockIdx.x + sg.unit) * p.R + w * 128 + r0;   // the warp's first row in the parts
       // O goes out by way of the warp's own rows of Q, which no product reads any more: 32 rows x
       // 128 bytes, swizzled, then 8 lanes write a row's 128 bytes
@@ -570,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const __grid_c
         const long long to = rows.index(p, lane);
         if (to >= 0) {
           if (!whole) p.ml_part[at + lane] = make_float2(m2, l);
-          else if (p.lse) p.lse[to] = kv4_lse(m2, l, kTcShift);
+          else if (p.lse) p.lse[to] = kv4_lse(m2, l, kTcShift);   // m2 = -inf gives -inf
         }
       }
       if (threadIdx.x == 0) {

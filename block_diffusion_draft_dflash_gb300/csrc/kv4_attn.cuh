@@ -30,6 +30,7 @@ struct Kv4AttnParams {
   bool last_single;      // kv4_single of the last tile
   int stage_log2;        // keys of a stage
   int min_stages;        // no share is smaller, while there are several
+  int change_step;       // a seventh of what going over to another unit costs, in stages
   int n_cta;
   float shift;           // probabilities carry 2^shift
   float* o_part;         // [n_cta + units][R][128]: slot CTA + unit
@@ -55,19 +56,25 @@ DF_DEV int kv4_chain(const Kv4AttnParams& p, int N, int rt) {
 // Tiles of a sequence differ in length where a chain has several: a row sees no later node.
 DF_DEV bool kv4_even(const Kv4AttnParams& p) { return p.anc || p.nrt == 1; }
 
-DF_DEV int kv4_head_stages(const Kv4AttnParams& p, int s) {   // of one kv head
-  const int N = p.cache_len[s];
+// ceil(x / d) by a multiplication: magic = floor((2^32 - 1) / d) + 1, d > 1, exact for (x + d) d < 2^32.
+DF_DEV int kv4_parts(int x, int d, uint32_t magic) { return (int)__umulhi((uint32_t)(x + d - 1), magic); }
+
+// The line's length over one kv head of a sequence of N slots: stages, or (per > 1) parts of at
+// most `per` stages.
+DF_DEV int kv4_head_line(const Kv4AttnParams& p, int N, int per, uint32_t magic) {
+  auto line = [&](int stages) { return per == 1 ? stages : kv4_parts(stages, per, magic); };
   if (kv4_even(p)) {
     const int len = kv4_all(p, N);
-    return (p.nrt - 1) * kv4_stages(p, len, false) + kv4_stages(p, len, p.last_single);
+    const int last = line(kv4_stages(p, len, p.last_single));
+    return p.nrt == 1 ? last : (p.nrt - 1) * line(kv4_stages(p, len, false)) + last;
   }
   int n = 0;
 #pragma unroll 1
-  for (int rt = 0; rt < p.nrt; ++rt) n += kv4_stages(p, kv4_chain(p, N, rt), kv4_single(p, rt));
+  for (int rt = 0; rt < p.nrt; ++rt) n += line(kv4_stages(p, kv4_chain(p, N, rt), kv4_single(p, rt)));
   return n;
 }
 
-struct Kv4Seg {        // the part of one unit that lies in a share
+struct Kv4Seg {        // the part of one unit that a CTA works on
   int s, kvh, rt, unit;
   int tile0, count;    // stages [tile0, tile0 + count)
   int N, len;          // cache_len (0 where it does not fit), slots seen
@@ -77,84 +84,134 @@ struct Kv4Seg {        // the part of one unit that lies in a share
 
 // A CTA's walk through its share.  One warp of the CTA walks (code that a kernel runs once
 // costs some 50 cycles an instruction) and hands the units out by shared memory.
+//
+// Where there are enough CTAs every unit is cut into equal parts of at most `per` stages, one
+// for each CTA, with the smallest `per` that the CTAs allow.  Going over to another unit costs
+// as much as some stages (an epilogue, another Q), so this is done unless the largest part
+// exceeds the mean share by more than 7 p.change_step.  Else the shares are equal pieces of the line of
+// all stages, whatever units they cut.
 struct Kv4Walk {
-  int t, t1, end;      // next stage, end of the share, end of sequence s
-  int s, head;         // stages of one kv head of s
+  int t, t1, end;      // next place in the line, end of the share, end of sequence s
+  int s, head;         // line of one kv head of s
+  int per;             // 1: the line counts stages; else parts
+  uint32_t magic;      // of kv4_parts
+
+  DF_DEV static uint32_t magic_of(int d) { return 0xFFFFFFFFu / (uint32_t)d + 1u; }   // 0 for d = 1: not used
 
   // By a whole warp, like next(); false: no share.
   DF_DEV bool init(const Kv4AttnParams& p, int cta, int lane) {
-    int total = 0;     // all stages, then those of the sequences already passed
-    bool found = false;
+    const int N0 = lane < p.b ? p.cache_len[lane] : 0;   // of the first 32 sequences
+    // Pass 0: the sum of all stages.  Pass 1: for 8 lengths of a part, a lane each, the parts
+    // that they make of four sequences at a time.  Then the place in the line that was chosen.
+    int total = 0, mean = 0;
+    per = 1;
+    magic = 0;
 #pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {   // one copy of the code: the sum, then the place in it
+    for (int pass = 0; pass < 2; ++pass) {
+      const int d = max(2, mean) + (lane & 7) * p.change_step;
+      const uint32_t m = pass ? magic_of(d) : 0u;
+      const int step = pass ? 4 : 32, first = pass ? lane >> 3 : lane;
+      int n = 0;
 #pragma unroll 1
-      for (int base = 0; base < p.b && !found; base += 32) {
-        const int h = base + lane < p.b ? kv4_head_stages(p, base + lane) : 0;
-        int inc = h * p.Hkv;
-#pragma unroll 1
-        for (int o = 1; o < 32; o <<= 1) {
-          const int x = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += x;
-        }
-        if (pass == 1) {
-          const int k = __popc(__ballot_sync(0xffffffffu, base + lane < p.b && total + inc <= t));   // sequences before t
-          if (k < 32) {
-            s = base + k;
-            head = __shfl_sync(0xffffffffu, h, k);
-            end = total + __shfl_sync(0xffffffffu, inc, k);
-            found = true;
-          }
-        }
-        total += __shfl_sync(0xffffffffu, inc, 31);
+      for (int base = 0; base < p.b; base += step) {
+        const int i = base + first;
+        const int N = base < 32 ? __shfl_sync(0xffffffffu, N0, i & 31) : i < p.b ? p.cache_len[i] : 0;
+        if (i < p.b) n += kv4_head_line(p, N, pass ? d : 1, m) * p.Hkv;
       }
+      n += __shfl_xor_sync(0xffffffffu, n, 16);
+      n += __shfl_xor_sync(0xffffffffu, n, 8);
       if (pass == 0) {
-        const int n = min((total + p.min_stages - 1) / p.min_stages, p.n_cta);
-        if (cta >= n) return false;
-        const int q = total / n, rest = total - q * n;   // the first `rest` shares have one more
-        t = q * cta + min(cta, rest);
-        t1 = t + q + (cta < rest ? 1 : 0);
-        total = 0;
+        total = __reduce_add_sync(0xffffffffu, lane < 8 ? n : 0);
+        mean = max(p.min_stages, (total + p.n_cta - 1) / p.n_cta);
+      } else {
+        const uint32_t fits = __ballot_sync(0xffffffffu, n <= p.n_cta) & 0xFFu;
+        if (fits) {
+          const int k = __ffs(fits) - 1;
+          per = __shfl_sync(0xffffffffu, d, k);
+          magic = __shfl_sync(0xffffffffu, m, k);
+          total = __shfl_sync(0xffffffffu, n, k);
+        }
       }
     }
-    return true;
+    if (per > 1) {
+      if (cta >= total) return false;
+      t = cta;
+      t1 = cta + 1;
+    } else {
+      const int n = min((total + p.min_stages - 1) / p.min_stages, p.n_cta);
+      if (cta >= n) return false;
+      const int q = total / n, rest = total - q * n;   // the first `rest` shares have one more
+      t = q * cta + min(cta, rest);
+      t1 = t + q + (cta < rest ? 1 : 0);
+    }
+    int before = 0;
+#pragma unroll 1
+    for (int base = 0;; base += 32) {
+      const int N = base == 0 ? N0 : base + lane < p.b ? p.cache_len[base + lane] : 0;
+      const int h = base + lane < p.b ? kv4_head_line(p, N, per, magic) : 0;
+      int inc = h * p.Hkv;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+      }
+      const int k = __popc(__ballot_sync(0xffffffffu, base + lane < p.b && before + inc <= t));   // sequences before t
+      if (k < 32) {
+        s = base + k;
+        head = __shfl_sync(0xffffffffu, h, k);
+        end = before + __shfl_sync(0xffffffffu, inc, k);
+        return true;
+      }
+      before += __shfl_sync(0xffffffffu, inc, 31);
+    }
   }
 
   DF_DEV bool next(const Kv4AttnParams& p, Kv4Seg& g) {
     if (t >= t1) return false;
     if (t == end) {
-      head = kv4_head_stages(p, ++s);
+      head = kv4_head_line(p, p.cache_len[++s], per, magic);
       end += head * p.Hkv;
     }
     int rel = t - (end - head * p.Hkv), rt = 0;
     const int N = p.cache_len[s];
     g.kvh = rel / head;
     rel -= g.kvh * head;
-    int len = kv4_all(p, N), per_unit;
-    if (kv4_even(p)) {   // all tiles but the last have the same stages
-      per_unit = kv4_stages(p, len, false);
-      rt = min(rel / per_unit, p.nrt - 1);
-      rel -= rt * per_unit;
-      if (kv4_single(p, rt)) per_unit = kv4_stages(p, len, true);
-    } else {
+    // the tile, and the place in its own piece of the line
+    int len = kv4_all(p, N), stages, piece;
 #pragma unroll 1
-      for (;; ++rt) {
-        len = kv4_chain(p, N, rt);
-        per_unit = kv4_stages(p, len, kv4_single(p, rt));
-        if (rel < per_unit) break;
-        rel -= per_unit;
+    for (;; ++rt) {
+      if (!kv4_even(p)) len = kv4_chain(p, N, rt);
+      stages = kv4_stages(p, len, kv4_single(p, rt));
+      piece = per == 1 ? stages : kv4_parts(stages, per, magic);
+      if (kv4_even(p) && rt == 0 && p.nrt > 2) {   // all tiles but the last are alike
+        const int skip = min(rel / piece, p.nrt - 1);
+        rel -= skip * piece;
+        rt = skip;
+        if (rt < p.nrt - 1) break;
+        --rt;
+        continue;
       }
+      if (rel < piece) break;
+      rel -= piece;
     }
     g.s = s;
     g.rt = rt;
     g.unit = (s * p.Hkv + g.kvh) * p.nrt + rt;
-    g.tile0 = rel;
-    g.count = min(t1 - t, per_unit - rel);
+    if (per == 1) {
+      g.tile0 = rel;
+      g.count = min(t1 - t, stages - rel);
+      t += g.count;
+    } else {   // equal parts
+      const int q = stages / piece, rest = stages - q * piece;
+      g.tile0 = q * rel + min(rel, rest);
+      g.count = q + (rel < rest ? 1 : 0);
+      ++t;
+    }
     g.len = len;
     g.N = len > 0 ? N : 0;
     g.single = kv4_single(p, rt);
-    g.first = rel == 0;
-    g.last = rel + g.count == per_unit;
-    t += g.count;
+    g.first = g.tile0 == 0;
+    g.last = g.tile0 + g.count == stages;
     return true;
   }
 };

@@ -390,7 +390,8 @@ int dflash_kv4_append(const df_kv4_cache* cache, int layer, const df_bf16* k, co
  * bit j of anc[s][i] set: out = softmax(scale q.k) v, fp32 inside, fp16 probabilities (scaled
  * by a power of two).  The tree's rows must already be in slots N .. N + n_tree - 1.
  * n_tree = 1 with anc NULL is a plain decode step.
- *   q          [b][n_tree][Hq][hd] bf16 (rotated);  Hq a multiple of Hkv
+ *   q          [b][n_tree][Hq][hd] bf16 (rotated);  Hq a multiple of Hkv, at most 4096 Hkv;
+ *              cap <= 2^20
  *   cache_len  [b] int32, N + n_tree <= cap
  *   anc        [b][n_tree][ceil(n_tree/32)] uint32, or NULL: a chain, row i sees tree slots 0 .. i
  *   scale      > 0 and finite
