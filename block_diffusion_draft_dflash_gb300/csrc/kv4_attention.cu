@@ -6,12 +6,15 @@
 // with K, V the values that the cache's codes and scales stand for (kv4.cuh: fp16 numbers, so
 // the fp16 tensor-core products are exact; sums, softmax statistics and outputs are fp32).
 //
-// What bounds it with few rows is the cache, 144 bytes a slot and kv head.  A work item is a
-// stage of 32 slots of one (sequence, kv head); all stages of a call are laid out in one line,
-// which the CTAs cut into equal shares whatever the sequences' lengths.  In a CTA every warp
-// streams stages of its own (bulk copies into a ring of its own, no CTA barrier), decodes codes
-// straight into tensor-core fragments and keeps its own running maximum, sum and output; the
-// warps are merged when the share, or the (sequence, kv head), ends.
+// What bounds it with few rows is the cache, 144 bytes a slot and kv head, and then the
+// instructions that decode it.  Every warp streams stages of 32 slots (bulk copies into a ring
+// of its own, no CTA barrier), decodes codes straight into tensor-core fragments and keeps its
+// own running maximum, sum and output; the warps are merged when the CTA's part of a unit ends.
+//
+// Both products are transposed, S^T = K Q^T and O^T = V^T P^T: the cache is the 16-row operand
+// and the query rows are the 8 columns, so 8 rows (4 heads of a token, say) cost half of what
+// they would as rows.  P goes from the one product's accumulators to the other's operand by
+// an 8 x 8 transposition in registers.
 #include <math.h>
 
 #include "kv4_attn.cuh"
@@ -29,10 +32,43 @@ constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 // row's largest still has all its bits.
 constexpr float kPShift = 12.f;
 
-template <int MT>   // row tiles of 16 per warp
-__global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 2 : 1) kv4_attn_kernel(const __grid_constant__ Kv4AttnParams p) {
+// 8 x 8 fp16 transposition: lane (g, t) has row g, columns 2t, 2t+1, before and after.
+DF_DEV uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// A query row's share of a lane: dimensions 32 t4 .. + 31 as fp16 (brought there by a power of
+// two that the quad agrees on, `back` its inverse), two registers for each of 8 steps.
+DF_DEV void load_q(const df_bf16* src, bool on, int t4, uint32_t (&f)[8][2], float& back) {
+  uint4 raw[4];
+  float amax = 0.f;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) raw[c] = on ? reinterpret_cast<const uint4*>(src + t4 * 32)[c] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+  }
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  const float s = f16_row_factor(amax, back);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      f[2 * c + (e >> 1)][e & 1] = pack_f16x2(__uint_as_float(w[e] << 16) * s, __uint_as_float(w[e] & 0xFFFF0000u) * s);
+  }
+}
+
+template <int NT>   // tiles of 8 query rows
+__global__ void __launch_bounds__(kWarps * 32, 2) kv4_attn_kernel(const __grid_constant__ Kv4AttnParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
-  constexpr int R = 16 * MT;
+  constexpr int R = 8 * NT;
   __shared__ __align__(8) uint64_t bars[kWarps][kStages];
   __shared__ float2 ml[kWarps][R];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
@@ -48,224 +84,198 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 2 : 1) kv4_attn_kernel(
   Kv4Walk walk;
   if (!walk.init(p, blockIdx.x, lane)) return;
   Kv4Seg seg;
-  uint32_t uses = 0;   // stages this warp has loaded so far, modulo 2^32: slot uses % kStages
+  uint32_t slot = 0, phase = 0;   // of the warp's next stage
   bool ok = true;
   while (walk.next(p, seg)) {
-    const int s = seg.s, kvh = seg.kvh, rt = seg.rt, tile0 = seg.tile0, count = seg.count, N = seg.N, len = seg.len;
+    const int s = seg.s, kvh = seg.kvh, tile0 = seg.tile0, count = seg.count, N = seg.N, len = seg.len;
     if (len == 0 && tid == 0) set_status(p.status, DF_ERR_CAPACITY, s);
     const size_t plane = ((size_t)s * p.Hkv + kvh) * p.cap;
-    const int rows = min(R, p.T * p.G - rt * R);   // live rows of the tile
-    const uint8_t *kc = p.p.kc + plane * kKv4Codes, *vc = p.p.vc + plane * kKv4Codes;
-    const uint8_t *ks = p.p.ks + plane * kKv4Scales, *vs = p.p.vs + plane * kKv4Scales;
-    auto issue = [&](int i, uint32_t slot) {   // this warp's i-th stage of the segment
+    const int rows = min(R, p.T * p.G - seg.rt * R);   // live rows of the tile
+    auto issue = [&](int i, uint32_t to) {   // this warp's i-th stage of the unit
       if (lane == 0) {
-        unsigned char* st = ring + slot * kStageBytes;
-        uint64_t* bar = &bars[warp][slot];
+        unsigned char* st = ring + to * kStageBytes;
+        uint64_t* bar = &bars[warp][to];
         const int key0 = (tile0 + warp + i * kWarps) * kStageKeys;
         const uint32_t n = min(kStageKeys, p.cap - key0);   // a multiple of 8
+        const size_t row = plane + key0;
         mbar_arrive_expect_tx(bar, n * 2 * (kKv4Codes + kKv4Scales));
-        bulk_load(st, kc + (size_t)key0 * kKv4Codes, n * kKv4Codes, bar);
-        bulk_load(st + 2 * kStageKeys * kKv4Codes, ks + (size_t)key0 * kKv4Scales, n * kKv4Scales, bar);
-        bulk_load(st + kStageKeys * kKv4Codes, vc + (size_t)key0 * kKv4Codes, n * kKv4Codes, bar);
-        bulk_load(st + kStageKeys * (2 * kKv4Codes + kKv4Scales), vs + (size_t)key0 * kKv4Scales, n * kKv4Scales, bar);
+        bulk_load(st, p.p.kc + row * kKv4Codes, n * kKv4Codes, bar);
+        bulk_load(st + 2 * kStageKeys * kKv4Codes, p.p.ks + row * kKv4Scales, n * kKv4Scales, bar);
+        bulk_load(st + kStageKeys * kKv4Codes, p.p.vc + row * kKv4Codes, n * kKv4Codes, bar);
+        bulk_load(st + kStageKeys * (2 * kKv4Codes + kKv4Scales), p.p.vs + row * kKv4Scales, n * kKv4Scales, bar);
       }
     };
     const int mine = count > warp ? (count - warp + kWarps - 1) / kWarps : 0;
-    for (int i = 0; i < kStages && i < mine; ++i) issue(i, (uses + i) % kStages);
-    // Q fragments.  The products run over dimensions in the order in which a lane finds its
-    // codes: lane t4 of a quad takes dimensions 32 t4 .. 32 t4 + 31, four at a step.
-    uint32_t qf[MT][8][4];
-    float qs[MT][2];   // raw score -> log2 units
+    for (int i = 0; i < kStages && i < mine; ++i) issue(i, (slot + i) % kStages);
+    // Q^T fragments: column n = g of tile q is row 8 q + g.  The products run over dimensions in
+    // the order in which a lane finds its codes: 32 t4 .. + 31, four at a step.
+    uint32_t qf[NT][8][2];
+    float qs[NT][2];   // raw score -> log2 units, of rows 2 t4, 2 t4 + 1 (this lane's columns of S^T)
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int r = rt * R + m * 16 + half * 8 + g;
-        uint4 raw[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) raw[c] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < p.T * p.G) {
-          const df_bf16* src = p.q + (((size_t)s * p.T + r / p.G) * p.Hq + kvh * p.G + r % p.G) * 128 + t4 * 32;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) raw[c] = reinterpret_cast<const uint4*>(src)[c];
-        }
-        float amax = 0.f;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
-        }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        float back;
-        const float f = f16_row_factor(amax, back);
-        qs[m][half] = p.scale2 * back;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            qf[m][2 * c + (e >> 1)][(e & 1) * 2 + half] =
-                pack_f16x2(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xFFFF0000u) * f);
-        }
-      }
+    for (int q = 0; q < NT; ++q) {
+      const int r = seg.rt * R + q * 8 + g, node = r / p.G;
+      float back;
+      load_q(p.q + (((size_t)s * p.T + node) * p.Hq + kvh * p.G + r - node * p.G) * 128, node < p.T, t4, qf[q], back);
+      back *= p.scale2;
+      qs[q][0] = __shfl_sync(0xffffffffu, back, t4 * 8);
+      qs[q][1] = __shfl_sync(0xffffffffu, back, t4 * 8 + 4);
     }
-    float o[MT][16][4], mx[MT][2], l[MT][2];
+    float o[NT][8][4], mx[NT][2], l[NT][2];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int q = 0; q < NT; ++q) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) o[m][j][0] = o[m][j][1] = o[m][j][2] = o[m][j][3] = 0.f;
-      mx[m][0] = mx[m][1] = -INFINITY;
-      l[m][0] = l[m][1] = 0.f;
+      for (int j = 0; j < 8; ++j) o[q][j][0] = o[q][j][1] = o[q][j][2] = o[q][j][3] = 0.f;
+      mx[q][0] = mx[q][1] = -INFINITY;
+      l[q][0] = l[q][1] = 0.f;
     }
+#pragma unroll 1
     for (int i = 0; i < mine; ++i) {
-      const uint32_t slot = uses % kStages;
-      ok = ok && kv4_wait(&bars[warp][slot], (uses / kStages) & 1, p.status, 50);
+      ok = ok && kv4_wait(&bars[warp][slot], phase, p.status, 50);
       ok = __all_sync(0xffffffffu, ok);
       const unsigned char* st = ring + slot * kStageBytes;
       const unsigned char *skc = st, *svc = st + kStageKeys * kKv4Codes;
       const unsigned char *sks = st + 2 * kStageKeys * kKv4Codes, *svs = sks + kStageKeys * kKv4Scales;
       const int key0 = (tile0 + warp + i * kWarps) * kStageKeys;
-      // S: four tiles of 8 keys.  Key of tile q, column n: 16 (q/2) + 8 (q%2) + 4 (n%2) + n/2, so
-      // that lane t4's probabilities belong to keys t4 + 4i, whose value rows it decodes below.
-      float sc[MT][4][4];
+      // S^T: two tiles of 16 keys.  Row x of 8 (of a tile's upper or lower half) is key
+      // 4 (x % 2) + x / 2, so that lane t4's columns of P belong to keys t4 + 4 e, whose value
+      // rows it decodes below.
+      float sc[NT][2][4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m) sc[m][q][0] = sc[m][q][1] = sc[m][q][2] = sc[m][q][3] = 0.f;
-        const int key = q * 8 + (g & 1) * 4 + (g >> 1);
-        const uint4 c = *reinterpret_cast<const uint4*>(skc + key * kKv4Codes + t4 * 16);
-        const uint32_t two = *reinterpret_cast<const uint16_t*>(sks + key * kKv4Scales + t4 * 2);
-        const uint32_t s0 = e4m3x2_to_f16((two & 0xFFu) * 0x00010001u), s1 = e4m3x2_to_f16((two >> 8) * 0x00010001u);
-        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+        for (int q = 0; q < NT; ++q) sc[q][h][0] = sc[q][h][1] = sc[q][h][2] = sc[q][h][3] = 0.f;
+        const int key = h * 16 + (g & 1) * 4 + (g >> 1);   // and 8 further
+        const uint4 ca = *reinterpret_cast<const uint4*>(skc + key * kKv4Codes + t4 * 16);
+        const uint4 cb = *reinterpret_cast<const uint4*>(skc + (key + 8) * kKv4Codes + t4 * 16);
+        const uint32_t ta = *reinterpret_cast<const uint16_t*>(sks + key * kKv4Scales + t4 * 2);
+        const uint32_t tb = *reinterpret_cast<const uint16_t*>(sks + (key + 8) * kKv4Scales + t4 * 2);
+        // both blocks' scales of a key in one word, then either of them in both halves
+        const uint32_t pa = e4m3x2_to_f16(__byte_perm(ta, 0, 0x4140)), pb = e4m3x2_to_f16(__byte_perm(tb, 0, 0x4140));
+        const uint32_t sa[2] = {__byte_perm(pa, 0, 0x1010), __byte_perm(pa, 0, 0x3232)};
+        const uint32_t sb[2] = {__byte_perm(pb, 0, 0x1010), __byte_perm(pb, 0, 0x3232)};
+        const uint32_t wa[4] = {ca.x, ca.y, ca.z, ca.w}, wb[4] = {cb.x, cb.y, cb.z, cb.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          uint32_t f[4];
-          e2m1x8_to_f16(w[e], f);
+          uint32_t fa[4], fb[4];
+          e2m1x8_to_f16(wa[e], fa);
+          e2m1x8_to_f16(wb[e], fb);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) f[x] = hmul2(f[x], e < 2 ? s0 : s1);
+          for (int x = 0; x < 4; ++x) { fa[x] = hmul2(fa[x], sa[e >> 1]); fb[x] = hmul2(fb[x], sb[e >> 1]); }
+          const uint32_t a0[4] = {fa[0], fb[0], fa[1], fb[1]}, a1[4] = {fa[2], fb[2], fa[3], fb[3]};
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            mma_f16_16816(sc[m][q], qf[m][2 * e], f[0], f[1]);
-            mma_f16_16816(sc[m][q], qf[m][2 * e + 1], f[2], f[3]);
+          for (int q = 0; q < NT; ++q) {
+            mma_f16_16816(sc[q][h], a0, qf[q][2 * e][0], qf[q][2 * e][1]);
+            mma_f16_16816(sc[q][h], a1, qf[q][2 * e + 1][0], qf[q][2 * e + 1][1]);
           }
         }
       }
       // log2 units, mask, running maximum
       const bool edge = key0 + kStageKeys > N;
-      uint32_t pf[MT][2][4];
+      uint32_t pf[NT][2][2];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        float mt[2] = {-INFINITY, -INFINITY};
+      for (int q = 0; q < NT; ++q) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[m][q][e] *= qs[m][e >> 1];
+          for (int e = 0; e < 4; ++e) sc[q][h][e] *= qs[q][e & 1];
         if (edge) {
+          uint32_t bits[2] = {0u, 0u};
 #pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            const int r = rt * R + m * 16 + half * 8 + g, node = r / p.G;
+          for (int c = 0; c < 2; ++c) {   // one copy of the code
+            const int r = seg.rt * R + q * 8 + t4 * 2 + c, node = r / p.G;
             const uint32_t* anc = p.anc && node < p.T ? p.anc + ((size_t)s * p.T + node) * p.W : nullptr;
-            uint32_t bits = node < p.T ? kv4_see_bits(anc, p.W, N, key0, node, len) : 0u;
-            bits >>= t4;
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (!((bits >> (q * 8 + e * 4)) & 1u)) {
-                  if (half) sc[m][q][2 + e] = -INFINITY; else sc[m][q][e] = -INFINITY;
-                }
+            const uint32_t x = node < p.T ? kv4_see_bits(anc, p.W, N, key0, node, len) : 0u;
+            bits[0] = c == 0 ? x : bits[0];
+            bits[1] = x;
           }
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (!((bits[e & 1] >> (h * 16 + (e >> 1) * 8 + (g & 1) * 4 + (g >> 1))) & 1u)) sc[q][h][e] = -INFINITY;
         }
+        float mt[2];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mt[e >> 1] = fmaxf(mt[e >> 1], sc[m][q][e]);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          mt[half] = fmaxf(mt[half], __shfl_xor_sync(0xffffffffu, mt[half], 1));
-          mt[half] = fmaxf(mt[half], __shfl_xor_sync(0xffffffffu, mt[half], 2));
-          mt[half] = fmaxf(mt[half], mx[m][half]);
+        for (int c = 0; c < 2; ++c) {
+          mt[c] = fmaxf(fmaxf(sc[q][0][c], sc[q][0][c + 2]), fmaxf(sc[q][1][c], sc[q][1][c + 2]));
+          mt[c] = fmaxf(mt[c], __shfl_xor_sync(0xffffffffu, mt[c], 4));
+          mt[c] = fmaxf(mt[c], __shfl_xor_sync(0xffffffffu, mt[c], 8));
+          mt[c] = fmaxf(mt[c], __shfl_xor_sync(0xffffffffu, mt[c], 16));
+          mt[c] = fmaxf(mt[c], mx[q][c]);
         }
-        if (__any_sync(0xffffffffu, mt[0] > mx[m][0] || mt[1] > mx[m][1])) {
-          const float a0 = mx[m][0] == -INFINITY ? 0.f : ex2_approx(mx[m][0] - mt[0]);
-          const float a1 = mx[m][1] == -INFINITY ? 0.f : ex2_approx(mx[m][1] - mt[1]);
+        if (__any_sync(0xffffffffu, mt[0] > mx[q][0] || mt[1] > mx[q][1])) {
+          const float a0 = mx[q][0] == -INFINITY ? 0.f : ex2_approx(mx[q][0] - mt[0]);
+          const float a1 = mx[q][1] == -INFINITY ? 0.f : ex2_approx(mx[q][1] - mt[1]);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) { o[m][j][0] *= a0; o[m][j][1] *= a0; o[m][j][2] *= a1; o[m][j][3] *= a1; }
-          l[m][0] *= a0;
-          l[m][1] *= a1;
-          mx[m][0] = mt[0];
-          mx[m][1] = mt[1];
+          for (int j = 0; j < 8; ++j) { o[q][j][0] *= a0; o[q][j][1] *= a1; o[q][j][2] *= a0; o[q][j][3] *= a1; }
+          l[q][0] *= a0;
+          l[q][1] *= a1;
+          mx[q][0] = mt[0];
+          mx[q][1] = mt[1];
         }
-        // a row that has seen nothing yet: every x is -inf, and 2^(-inf - 0) = 0
+        // a row that has seen nothing yet: every score is -inf, and 2^(-inf - 0) = 0
         const float b0 = kPShift - (mt[0] == -INFINITY ? 0.f : mt[0]), b1 = kPShift - (mt[1] == -INFINITY ? 0.f : mt[1]);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float p0 = ex2_approx(sc[m][q][0] + b0), p1 = ex2_approx(sc[m][q][1] + b0);
-          const float p2 = ex2_approx(sc[m][q][2] + b1), p3 = ex2_approx(sc[m][q][3] + b1);
-          l[m][0] += p0 + p1;
-          l[m][1] += p2 + p3;
-          pf[m][q >> 1][(q & 1) * 2] = pack_f16x2(p0, p1);
-          pf[m][q >> 1][(q & 1) * 2 + 1] = pack_f16x2(p2, p3);
+        for (int h = 0; h < 2; ++h) {
+          const float p0 = ex2_approx(sc[q][h][0] + b0), p1 = ex2_approx(sc[q][h][1] + b1);
+          const float p2 = ex2_approx(sc[q][h][2] + b0), p3 = ex2_approx(sc[q][h][3] + b1);
+          l[q][0] += p0 + p2;
+          l[q][1] += p1 + p3;
+          pf[q][h][0] = transpose8(pack_f16x2(p0, p1));
+          pf[q][h][1] = transpose8(pack_f16x2(p2, p3));
         }
       }
-      // O: lane g of the column takes dimensions 16 g .. 16 g + 15 (one scale a key), tile j of
-      // 8 columns the j-th of them.  Two keys' codes are merged nibble by nibble, so that one
+      // O^T: lane g takes dimensions 16 g .. 16 g + 15 (one scale a key), tile j rows the 2j-th
+      // and the 2j+1-th of them.  Two keys' codes are merged nibble by nibble, so that one
       // conversion gives the pair of keys that a fragment register holds.
 #pragma unroll
-      for (int k2 = 0; k2 < 2; ++k2) {
+      for (int h = 0; h < 2; ++h) {
         uint2 c[4];
         uint32_t sb[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int key = k2 * 16 + e * 4 + t4;
+          const int key = h * 16 + e * 4 + t4;
           c[e] = *reinterpret_cast<const uint2*>(svc + key * kKv4Codes + g * 8);
           sb[e] = svs[key * kKv4Scales + g];
         }
-        const uint32_t s01 = e4m3x2_to_f16(sb[0] | (sb[1] << 16)), s23 = e4m3x2_to_f16(sb[2] | (sb[3] << 16));
+        const uint32_t s01 = e4m3x2_to_f16(__byte_perm(sb[0], sb[1], 0x5450)), s23 = e4m3x2_to_f16(__byte_perm(sb[2], sb[3], 0x5450));
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           const uint32_t c0 = w ? c[0].y : c[0].x, c1 = w ? c[1].y : c[1].x, c2 = w ? c[2].y : c[2].x, c3 = w ? c[3].y : c[3].x;
           uint32_t e01[4], o01[4], e23[4], o23[4];
-          e2m1x8_to_f16((c0 & 0x0F0F0F0Fu) | ((c1 & 0x0F0F0F0Fu) << 4), e01);
+          e2m1x8_to_f16((c0 & 0x0F0F0F0Fu) | ((c1 << 4) & 0xF0F0F0F0u), e01);
           e2m1x8_to_f16(((c0 >> 4) & 0x0F0F0F0Fu) | (c1 & 0xF0F0F0F0u), o01);
-          e2m1x8_to_f16((c2 & 0x0F0F0F0Fu) | ((c3 & 0x0F0F0F0Fu) << 4), e23);
+          e2m1x8_to_f16((c2 & 0x0F0F0F0Fu) | ((c3 << 4) & 0xF0F0F0F0u), e23);
           e2m1x8_to_f16(((c2 >> 4) & 0x0F0F0F0Fu) | (c3 & 0xF0F0F0F0u), o23);
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const uint32_t be0 = hmul2(e01[x], s01), be1 = hmul2(e23[x], s23);
-            const uint32_t bo0 = hmul2(o01[x], s01), bo1 = hmul2(o23[x], s23);
+            const uint32_t a[4] = {hmul2(e01[x], s01), hmul2(o01[x], s01), hmul2(e23[x], s23), hmul2(o23[x], s23)};
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              mma_f16_16816(o[m][8 * w + 2 * x], pf[m][k2], be0, be1);
-              mma_f16_16816(o[m][8 * w + 2 * x + 1], pf[m][k2], bo0, bo1);
-            }
+            for (int q = 0; q < NT; ++q) mma_f16_16816(o[q][4 * w + x], a, pf[q][h][0], pf[q][h][1]);
           }
         }
       }
       __syncwarp();   // every lane has read the stage
       if (ok && i + kStages < mine) issue(i + kStages, slot);
-      ++uses;
+      if (++slot == kStages) { slot = 0; phase ^= 1; }
     }
     // ---------------------------------------------------------------- merge the warps
-    __syncthreads();   // every ring is read, every copy of the segment has landed
+    __syncthreads();   // every ring is read, every copy of the unit has landed
     float* so = reinterpret_cast<float*>(smem) + warp * R * 128;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int q = 0; q < NT; ++q) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        l[m][half] += __shfl_xor_sync(0xffffffffu, l[m][half], 1);
-        l[m][half] += __shfl_xor_sync(0xffffffffu, l[m][half], 2);
-        const int r = m * 16 + half * 8 + g;
-        if (t4 == 0) ml[warp][r] = make_float2(mx[m][half], l[m][half]);
-        float* dst = so + r * 128 + t4 * 32;
+      for (int c = 0; c < 2; ++c) {
+        l[q][c] += __shfl_xor_sync(0xffffffffu, l[q][c], 4);
+        l[q][c] += __shfl_xor_sync(0xffffffffu, l[q][c], 8);
+        l[q][c] += __shfl_xor_sync(0xffffffffu, l[q][c], 16);
+        const int r = q * 8 + t4 * 2 + c;
+        if (g == 0) ml[warp][r] = make_float2(mx[q][c], l[q][c]);
+        // the row's dimensions 16 g .. + 15, their four pieces in an order that spreads the lanes
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          *reinterpret_cast<float4*>(dst + j) = make_float4(o[m][j][half * 2], o[m][j + 1][half * 2], o[m][j + 2][half * 2], o[m][j + 3][half * 2]);
-          *reinterpret_cast<float4*>(dst + 16 + j) = make_float4(o[m][j][half * 2 + 1], o[m][j + 1][half * 2 + 1], o[m][j + 2][half * 2 + 1], o[m][j + 3][half * 2 + 1]);
-        }
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<float4*>(so + r * 128 + g * 16 + ((j ^ t4) * 4)) =
+              make_float4(o[q][2 * j][c], o[q][2 * j][c + 2], o[q][2 * j + 1][c], o[q][2 * j + 1][c + 2]);
       }
     }
     __syncthreads();
@@ -276,6 +286,7 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 2 : 1) kv4_attn_kernel(
     }
     for (int x = tid; x < rows * 32; x += kWarps * 32) {   // four dimensions of one row
       const int r = x >> 5, d = (x & 31) * 4;
+      const int at_d = (x & 31) >> 2, piece = ((x & 3) ^ ((r >> 1) & 3)) * 4;   // where they lie
       float M = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w][r].x);
@@ -285,13 +296,13 @@ __global__ void __launch_bounds__(kWarps * 32, MT == 1 ? 2 : 1) kv4_attn_kernel(
       for (int w = 0; w < kWarps; ++w) {
         const float2 v = ml[w][r];
         const float f = v.x == -INFINITY ? 0.f : ex2_approx(v.x - M);
-        const float4 ov = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem) + (w * R + r) * 128 + d);
+        const float4 ov = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem) + (w * R + r) * 128 + at_d * 16 + piece);
         L += f * v.y;
         acc.x += f * ov.x; acc.y += f * ov.y; acc.z += f * ov.z; acc.w += f * ov.w;
       }
       if (whole) {
-        const int row = rt * R + r;
-        const size_t grow = ((size_t)s * p.T + row / p.G) * p.Hq + kvh * p.G + row % p.G;
+        const int row = seg.rt * R + r, node = row / p.G;
+        const size_t grow = ((size_t)s * p.T + node) * p.Hq + kvh * p.G + row - node * p.G;
         const float inv = L > 0.f ? p.v_mul / L : 0.f;
         uint2 w2;
         w2.x = pack_bf16x2(acc.x * inv, acc.y * inv);
@@ -356,7 +367,7 @@ int launch_kv4_attn_few(Kv4AttnParams p, cudaStream_t st) {
   p.shift = kPShift;
   const size_t merge = (size_t)kWarps * p.R * 128 * 4;
   const size_t smem = merge > kRingBytes ? merge : kRingBytes;
-  if (p.R == 16) {
+  if (p.R == 8) {
     if (ensure_dynamic_smem(kv4_attn_kernel<1>, smem) != cudaSuccess) return DF_ERR_CUDA;
     launch_k(kv4_attn_kernel<1>, dim3(p.n_cta), dim3(kWarps * 32), smem, st, p);
   } else {
@@ -370,13 +381,13 @@ namespace {
 // Rows, stage and grid of a call, by its rows per kv head.
 void kv4_attn_plan(int T, int G, Kv4AttnParams& p) {
   const long long rows = (long long)T * G;
-  p.R = rows <= 16 ? 16 : 256;
+  p.R = rows <= 8 ? 8 : rows <= 16 ? 16 : 256;
   p.nrt = (int)((rows + p.R - 1) / p.R);
   p.last_single = p.R == 256 && rows - (long long)(p.nrt - 1) * p.R <= 128;
   p.stage_log2 = p.R == 256 ? 7 : 5;
   p.min_stages = p.R == 256 ? 2 : kWarps;
   p.change_step = p.R == 256 ? 1 : 2;
-  p.n_cta = num_sms() * (p.R == 16 ? 2 : 1);
+  p.n_cta = num_sms() * (p.R == 256 ? 1 : 2);
 }
 size_t up16(size_t x) { return (x + 15) & ~(size_t)15; }
 }  // namespace
