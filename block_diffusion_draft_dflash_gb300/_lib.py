@@ -382,7 +382,7 @@ class Kv4Cache:
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.n_layers, self.b, self.n_kv_heads, self.cap = rows
         self.k_exp, self.v_exp = int(k_exp), int(v_exp)
-        self.device = k_codes.device
+        self.device, self.index = k_codes.device, k_codes.get_device()
         self.rows = tuple(rows)
         self.struct = Kv4CacheStruct(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
                                      *rows[:3], 128, rows[3], self.k_exp, self.v_exp)
@@ -397,16 +397,16 @@ class Kv4Cache:
         """Address of an argument that lies on the cache's device (None: 0)."""
         if t is None:
             return 0
-        if t.dtype != dtype or t.device != self.device or tuple(t.shape) != shape or not t.is_contiguous():
+        if t.dtype is not dtype or t.get_device() != self.index or t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on {self.device}")
         return t.data_ptr()
 
     def _ws(self, ws):
         """A call's workspace and stream: the current stream of the current device, which has to be the cache's."""
-        dev = self.device.index
-        if torch.cuda.current_device() != dev or ws.buf.device != self.device:
+        dev = self.index
+        if torch.cuda.current_device() != dev or ws.buf.get_device() != dev:
             raise ValueError(f"the current device and the workspace's have to be the cache's ({self.device})")
-        return ws.buf.data_ptr(), ws.nbytes, torch.cuda.current_stream(dev).cuda_stream
+        return ws.buf.data_ptr(), ws.nbytes, torch._C._cuda_getCurrentRawStream(dev)
 
 
 def kv4_append_workspace_size():

@@ -11,6 +11,7 @@
 
 #include "kv4.cuh"
 #include "kv4.h"
+#include "runtime.h"
 #include "trace.h"
 
 namespace df {
@@ -191,7 +192,8 @@ int launch_kv4_compact(const Kv4CompactArgs& a, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------------------- evict
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
+constexpr int kSelHeld = 49152;   // keys held in shared memory; a longer row's are made anew in every step
 
 // Order of slots for eviction: larger is kept first.  The first n_sink and the last n_recent
 // slots stand above every score; a NaN stands below.
@@ -200,15 +202,17 @@ DF_DEV uint32_t evict_key(float score, int slot, int lo, int hi) {
   return score == score ? float_key(score + 0.f) : 0u;   // + 0: one zero
 }
 
-// One CTA per (layer, sequence, kv head): the key of the last kept slot by radix selection
-// (four digits of 8 bits), then the kept slots in order, the lowest slots first among equal
-// keys.  Every count is a whole number: no order of additions changes the choice.
-__global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictArgs a) {
+// One CTA per (layer, sequence, kv head): the key of the last kept slot, two bits a step (the
+// largest key that `budget` slots reach), then the kept slots in order, the lowest slots first
+// among equal keys.  What bounds it is the comparisons: a histogram of digits costs more, with
+// atomic counters (scores crowd into few digits: 52 us for 288 rows of 8449 scores) and with
+// counters in registers (47 us), than three comparisons of every key in each of at most 16
+// steps.  Every count is a whole number: no order of additions changes the choice.
+__global__ void __launch_bounds__(kSelThreads, 2) kv4_select_kernel(const Kv4EvictArgs a) {
   pdl_wait();
   pdl_trigger();
-  __shared__ int hist[256];
-  __shared__ int sh_bin, sh_want;
-  __shared__ int warp_gt[32], warp_eq[32];
+  __shared__ int sums[17][4];
+  __shared__ int2 counts[kSelThreads / 32];
   const size_t plane = blockIdx.x;
   const int s = (int)((plane / a.Hkv) % a.b);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -218,78 +222,110 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictA
     len = 0;
   }
   const float* score = a.score + plane * a.cap;
-  float* score_out = a.score_out ? a.score_out + plane * a.dst_cap : nullptr;
   int32_t* kept = a.kept + plane * a.budget;
   if (len <= a.budget) {
-    for (int j = tid; j < a.budget; j += kSelThreads) {
-      kept[j] = j < len ? j : -1;
-      if (score_out && j < len) score_out[j] = score[j];
-    }
+    for (int j = tid; j < a.budget; j += kSelThreads) kept[j] = j < len ? j : -1;
     return;
   }
   const int lo = a.n_sink, hi = len - a.n_recent;
-  uint32_t prefix = 0;
-  int want = a.budget;
-#pragma unroll 1
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    for (int i = tid; i < len; i += kSelThreads) {
-      const uint32_t key = evict_key(score[i], i, lo, hi);
-      if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(key >> shift) & 255], 1);
+  if (tid < 68) sums[tid >> 2][tid & 3] = 0;
+  extern __shared__ __align__(16) uint32_t keys[];
+  const bool held = len <= kSelHeld;
+  auto key_at = [&](int i) { return held ? keys[i] : i < len ? evict_key(score[i], i, lo, hi) : 0u; };
+  if (held) {   // a row of scores is 16-byte aligned and as long as cap, a multiple of 8
+#pragma unroll 4
+    for (int i = tid; i < (len + 3) / 4; i += kSelThreads) {
+      const float4 v = reinterpret_cast<const float4*>(score)[i];
+      const int at = 4 * i;
+      reinterpret_cast<uint4*>(keys)[i] =
+          make_uint4(evict_key(v.x, at, lo, hi), at + 1 < len ? evict_key(v.y, at + 1, lo, hi) : 0u,
+                     at + 2 < len ? evict_key(v.z, at + 2, lo, hi) : 0u, at + 3 < len ? evict_key(v.w, at + 3, lo, hi) : 0u);
     }
-    __syncthreads();
-    if (warp == 0) {   // lane l: bins 8l .. 8l+7; the bin that holds the want-th largest key
-      int c[8], sum = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) { c[e] = hist[lane * 8 + e]; sum += c[e]; }
-      int above = sum;   // inclusive sum over lanes from the top
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_down_sync(0xffffffffu, above, o);
-        if (lane + o < 32) above += t;
-      }
-      above -= sum;
-#pragma unroll
-      for (int e = 7; e >= 0; --e) {
-        if (above < want && want <= above + c[e]) { sh_bin = lane * 8 + e; sh_want = want - above; }
-        above += c[e];
-      }
-    }
-    __syncthreads();
-    prefix |= (uint32_t)sh_bin << shift;
-    want = sh_want;
   }
-  // kept: keys above prefix, and the first `want` slots whose key equals it
-  int run_gt = 0, run_eq = 0;
-  for (int i0 = 0; i0 < len; i0 += kSelThreads) {
-    const int i = i0 + tid;
-    const float sc = i < len ? score[i] : 0.f;
-    const uint32_t key = i < len ? evict_key(sc, i, lo, hi) : 0u;
-    const bool gt = i < len && key > prefix, eq = i < len && key == prefix;
-    const uint32_t below = (1u << lane) - 1u;
+  __syncthreads();
+  // slots whose key is at least k[0], k[1], k[2] > 0, over the CTA
+  auto reach = [&](const uint32_t (&k)[3], int step, int (&n)[3]) {
+    int c[3] = {0, 0, 0};
+    if (held) {
+#pragma unroll 2
+      for (int i = tid; i < (len + 3) / 4; i += kSelThreads) {
+        const uint4 v = reinterpret_cast<const uint4*>(keys)[i];
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+          c[x] += (v.x >= k[x] ? 1 : 0) + (v.y >= k[x] ? 1 : 0) + (v.z >= k[x] ? 1 : 0) + (v.w >= k[x] ? 1 : 0);
+      }
+    } else {
+#pragma unroll 4
+      for (int i = tid; i < len; i += kSelThreads) {
+        const uint32_t v = evict_key(score[i], i, lo, hi);
+#pragma unroll
+        for (int x = 0; x < 3; ++x) c[x] += v >= k[x] ? 1 : 0;
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int x = 0; x < 3; ++x) c[x] = __reduce_add_sync(0xffffffffu, c[x]);
+    if (lane < 3) atomicAdd(&sums[step][lane], lane == 0 ? c[0] : lane == 1 ? c[1] : c[2]);
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < 3; ++x) n[x] = sums[step][x];
+  };
+  uint32_t prefix = 0;
+  bool exact = false;   // just `budget` slots reach prefix
+#pragma unroll 1
+  for (int step = 0; step < 16 && !exact; ++step) {
+    const int shift = 30 - 2 * step;
+    const uint32_t k[3] = {prefix | 1u << shift, prefix | 2u << shift, prefix | 3u << shift};
+    int n[3];
+    reach(k, step, n);
+    const int d = (n[0] >= a.budget ? 1 : 0) + (n[1] >= a.budget ? 1 : 0) + (n[2] >= a.budget ? 1 : 0);
+    prefix |= (uint32_t)d << shift;
+    exact = d > 0 && (d == 1 ? n[0] : d == 2 ? n[1] : n[2]) == a.budget;
+  }
+  int want = len;   // of the slots whose key equals prefix: all, where it is exact
+  if (!exact) {
+    int n[3] = {0, 0, 0};
+    const uint32_t k[3] = {prefix + 1u, prefix + 1u, prefix + 1u};
+    if (prefix != 0xFFFFFFFFu) reach(k, 16, n);
+    want = a.budget - n[0];
+  }
+  // kept: keys above prefix, and the first `want` slots whose key equals it.  A warp takes a
+  // piece of the row: it counts both kinds, then, knowing the counts before it, writes its part.
+  constexpr int kSelWarps = kSelThreads / 32;
+  const int piece = ((len + kSelWarps - 1) / kSelWarps + 31) & ~31;
+  const int p0 = min(len, warp * piece), p1 = min(len, p0 + piece);
+  const uint32_t below = (1u << lane) - 1u;
+  int g = 0, e = 0;
+#pragma unroll 4
+  for (int i = p0 + lane; i < p1; i += 32) {
+    const uint32_t k = key_at(i);
+    g += k > prefix ? 1 : 0;
+    e += k == prefix ? 1 : 0;
+  }
+  __syncwarp();
+  g = __reduce_add_sync(0xffffffffu, g);
+  e = __reduce_add_sync(0xffffffffu, e);
+  if (lane == 0) counts[warp] = make_int2(g, e);
+  __syncthreads();
+  g = 0;
+  e = 0;
+  for (int w = 0; w < warp; ++w) { g += counts[w].x; e += counts[w].y; }
+#pragma unroll 2
+  for (int i0 = p0; i0 < p1; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t k = i < p1 ? key_at(i) : 0u;
+    const bool gt = i < p1 && k > prefix, eq = i < p1 && k == prefix;
     const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-    __syncthreads();
-    if (lane == 0) { warp_gt[warp] = __popc(bg); warp_eq[warp] = __popc(be); }
-    __syncthreads();
-    int g = run_gt + __popc(bg & below), e = run_eq + __popc(be & below);
-#pragma unroll 8
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) { g += warp_gt[w]; e += warp_eq[w]; }
-      run_gt += warp_gt[w];
-      run_eq += warp_eq[w];
-    }
-    if (gt || (eq && e < want)) {
-      const int j = g + min(e, want);
-      kept[j] = i;
-      if (score_out) score_out[j] = sc;
-    }
+    const int me = e + __popc(be & below);
+    if (gt || (eq && me < want)) kept[g + __popc(bg & below) + min(me, want)] = i;
+    g += __popc(bg);
+    e += __popc(be);
   }
 }
 
 constexpr int kGatherRows = 64;
 
-// Copies kept rows: a CTA moves kGatherRows rows of one plane, 16 bytes of keys' and values'
+// Copies kept rows and their scores: a CTA moves kGatherRows rows of one plane, 16 bytes of keys' and values'
 // codes per thread.  new_len is written here, after every CTA of the selection has read the
 // lengths, so it may be the same array.
 __global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4EvictArgs a, int chunks) {
@@ -320,13 +356,16 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4EvictArgs a, i
   *reinterpret_cast<uint4*>(a.dst.kc + co) = k;
   *reinterpret_cast<uint4*>(a.dst.vc + co) = v;
   *reinterpret_cast<uint32_t*>(dp + (to + j) * kKv4Scales + (part & 1) * 4) = sc;
+  if (a.score_out && part == 0) a.score_out[to + j] = a.score[from + i];
 }
 
 int launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t st) {
   const long long planes = (long long)a.n_layers * a.b * a.Hkv;
   {
     DF_TRACE("kv4_select", st);
-    launch_k(kv4_select_kernel, dim3((unsigned)planes), dim3(kSelThreads), 0, st, a);
+    const size_t smem = (size_t)(a.cap < kSelHeld ? a.cap : kSelHeld) * 4;
+    if (ensure_dynamic_smem(kv4_select_kernel, smem) != cudaSuccess) return DF_ERR_CUDA;
+    launch_k(kv4_select_kernel, dim3((unsigned)planes), dim3(kSelThreads), smem, st, a);
   }
   DF_TRACE("kv4_gather", st);
   const int chunks = (a.budget + kGatherRows - 1) / kGatherRows;

@@ -412,7 +412,8 @@ int dflash_kv4_attention(const df_kv4_cache* cache, int layer, int n_tree, int H
  * holds there.  Slots >= cache_len are left as they were.  Sums run in a fixed order.
  * After accept_and_compact pass its n_new as n_rows, its src_slot, and the new cache_len: the
  * root and the accepted path vote, rejected nodes do not.
- *   q, lse     [b][n_tree][Hq][hd] bf16, [b][n_tree][Hq] fp32: of dflash_kv4_attention
+ *   q, lse     [b][n_tree][Hq][hd] bf16, [b][n_tree][Hq] fp32: of dflash_kv4_attention;
+ *              cap <= 2^20
  *   n_rows     [b] int32, 0 <= n_rows <= min(n_tree, cache_len), or NULL: n_tree
  *   src_slot   [b][max_src] int32: row 0 is node 0, row j node src_slot[s][j-1] - N
  *              (n_rows <= max_src + 1); or NULL: row j is node j
