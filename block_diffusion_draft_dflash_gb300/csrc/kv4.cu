@@ -19,10 +19,28 @@ namespace df {
 // ------------------------------------------------------------------------------ append
 constexpr int kAppTokens = 64;   // tokens of one kv head per CTA: 8 warps x 4 pairs
 
+// max(|a|, |b|) of two bf16 pairs; a NaN stays one.
+DF_DEV uint32_t absmax2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7FFF7FFFu), "r"(b & 0x7FFF7FFFu));
+  return r;
+}
+DF_DEV uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+DF_DEV uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // 16 lanes hold one row (8 values each, 16-byte loads); the two lanes of a block of 16 agree
 // on its scale with one shuffle.  A CTA takes consecutive tokens of one head, so that its
-// code and scale stores fill whole sectors of the cache.
-__global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4AppendArgs a, float k_down, float v_down) {
+// code and scale stores fill whole sectors of the cache.  Bound by its bytes: 4 x 4096 tokens
+// of 8 heads (153 MB with the held values) in 27 us.
+__global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4AppendArgs a, float k_up, float v_up) {
   pdl_wait();
   pdl_trigger();
   const int chunks = (a.n + kAppTokens - 1) / kAppTokens;
@@ -40,45 +58,56 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4AppendArgs a, 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane & 15;
   const df_bf16* in = is_v ? a.v : a.k;
   df_bf16* held = is_v ? a.v_held : a.k_held;
-  const float down = is_v ? v_down : k_down, up = 1.f / down;   // 2^-exp, 2^exp
+  const float up = is_v ? v_up : k_up, limit = 4096.f * up;   // 2^exp; beyond 448 * 6 * 2^exp all saturate
   uint8_t* codes = is_v ? a.p.vc : a.p.kc;
   uint8_t* scales = is_v ? a.p.vs : a.p.ks;
-  const size_t plane = ((size_t)s * a.Hkv + h) * a.cap;
   const int j0 = chunk * kAppTokens + warp * 8 + (lane >> 4);
+  const df_bf16* src = in + (((size_t)s * a.n + j0) * a.Hkv + h) * 128 + sub * 8;
+  const size_t step = (size_t)2 * a.Hkv * 128;
+  const size_t row0 = ((size_t)s * a.Hkv + h) * a.cap + len + j0;
   uint4 raw[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int j = j0 + 2 * i;
     raw[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (j < nn) raw[i] = *reinterpret_cast<const uint4*>(in + (((size_t)s * a.n + j) * a.Hkv + h) * 128 + sub * 8);
+    if (j0 + 2 * i < nn) raw[i] = *reinterpret_cast<const uint4*>(src + i * step);
   }
-  bool bad = false;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int j = j0 + 2 * i;
     const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-    float x[8], amax = 0.f;
+    float x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float v = __uint_as_float((e & 1) ? (w[e >> 1] & 0xFFFF0000u) : (w[e >> 1] << 16));
-      if (v != v) { bad = true; v = 0.f; }               // recorded, and stored as 0
-      v *= down;
-      x[e] = fminf(fmaxf(v, -4096.f), 4096.f);           // beyond 448 * 6 both saturate
-      amax = fmaxf(amax, fabsf(x[e]));
+    for (int e = 0; e < 4; ++e) {
+      x[2 * e] = __uint_as_float(w[e] << 16);
+      x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
     }
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    const __nv_fp8_storage_t sb = __nv_cvt_float_to_fp8(__fdiv_rn(amax, 6.f), __NV_SATFINITE, __NV_E4M3);
-    const float sc = e4m3_to_f(sb);
-    uint32_t code = 0;
-    if (sc > 0.f) {
-      // x / s to the nearest fp32 number: one step of correction of x * (1 / s), whose
-      // remainder the fma computes exactly
-      const float r = __frcp_rn(sc);
-      float q[8];
+    const uint32_t m2 = absmax2(absmax2(w[0], w[1]), absmax2(w[2], w[3]));
+    float amax = fmaxf(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xFFFF0000u));
+    const bool nan = (m2 & 0xFFFFu) > 0x7F80u || m2 > 0x7F80FFFFu;
+    if (__any_sync(0xffffffffu, nan || amax > limit)) {   // rare
+      if (nan) set_status(a.status, DF_ERR_NAN, s);
+      amax = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float t = x[e] * r;
-        q[e] = fmaf(fmaf(-t, sc, x[e]), r, t);
+        x[e] = x[e] == x[e] ? fminf(fmaxf(x[e], -limit), limit) : 0.f;   // a NaN is stored as 0
+        amax = fmaxf(amax, fabsf(x[e]));
+      }
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    const __nv_fp8_storage_t sb = __nv_cvt_float_to_fp8(__fdiv_rn(amax, 6.f * up), __NV_SATFINITE, __NV_E4M3);
+    const float sc = e4m3_to_f(sb) * up;   // the block's scale with 2^exp
+    uint32_t code = 0;
+    if (sc > 0.f) {
+      // x / sc to the nearest fp32 number: one step of correction of x * (1 / sc), whose
+      // remainder the fma computes exactly
+      const float r = __frcp_rn(sc);
+      const uint64_t r2 = pack_f32x2(r, r), n2 = pack_f32x2(-sc, -sc), z2 = pack_f32x2(-0.f, -0.f);
+      float q[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint64_t v = pack_f32x2(x[2 * e], x[2 * e + 1]);
+        const uint64_t t = fma_f32x2(v, r2, z2);
+        const uint64_t y = fma_f32x2(fma_f32x2(t, n2, v), r2, t);
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(q[2 * e]), "=f"(q[2 * e + 1]) : "l"(y));
       }
       asm("{\n .reg .b8 a, b, c, d;\n"
           " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
@@ -87,8 +116,8 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4AppendArgs a, 
           : "=r"(code)
           : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
     }
-    if (j < nn) {
-      const size_t row = plane + len + j;
+    if (j0 + 2 * i < nn) {
+      const size_t row = row0 + 2 * i;
       *reinterpret_cast<uint32_t*>(codes + row * kKv4Codes + sub * 4) = code;
       if ((sub & 1) == 0) scales[row * kKv4Scales + (sub >> 1)] = sb;
       if (held) {
@@ -97,21 +126,19 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4AppendArgs a, 
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 v = __half22float2(*reinterpret_cast<__half2*>(&f[e]));
-          o[e] = pack_bf16x2(v.x * sc * up, v.y * sc * up);   // six significant bits: exact
+          o[e] = pack_bf16x2(v.x * sc, v.y * sc);   // six significant bits: exact
         }
-        *reinterpret_cast<uint4*>(held + (((size_t)s * a.n + j) * a.Hkv + h) * 128 + sub * 8) =
-            make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(held + (src - in) + i * step) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
   }
-  if (bad) set_status(a.status, DF_ERR_NAN, s);
 }
 
 int launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t st) {
   DF_TRACE("kv4_append", st);
   const int chunks = (a.n + kAppTokens - 1) / kAppTokens;
-  launch_k(kv4_append_kernel, dim3((unsigned)(a.b * a.Hkv * chunks), 2), dim3(256), 0, st, a, ldexpf(1.f, -a.k_exp),
-           ldexpf(1.f, -a.v_exp));
+  launch_k(kv4_append_kernel, dim3((unsigned)(a.b * a.Hkv * chunks), 2), dim3(256), 0, st, a, ldexpf(1.f, a.k_exp),
+           ldexpf(1.f, a.v_exp));
   return cudaGetLastError() == cudaSuccess ? DF_OK : DF_ERR_CUDA;
 }
 
