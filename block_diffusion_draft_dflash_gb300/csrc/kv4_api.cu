@@ -45,6 +45,12 @@ bool caches_apart(const df_kv4_cache* x, const df_kv4_cache* y) {
   return true;
 }
 
+// A softmax scale that stays a number when the keys' exponent goes into it.
+bool scale_ok(float scale, int k_exp) {
+  const float x = std::ldexp(scale * 1.4426950408889634f, k_exp);
+  return scale > 0.f && std::isnormal(x);
+}
+
 }  // namespace
 }  // namespace df
 
@@ -84,7 +90,7 @@ int dflash_kv4_attention(const df_kv4_cache* c, int layer, int n_tree, int Hq, c
                          void* ws, size_t ws_bytes, df_stream stream) {
   DF_NVTX("dflash_kv4_attention");
   DF_TRY(cache_ok(c));
-  if (layer < 0 || layer >= c->n_layers || n_tree < 1 || Hq < 1 || Hq % c->Hkv || !(scale > 0.f) || !std::isfinite(scale))
+  if (layer < 0 || layer >= c->n_layers || n_tree < 1 || Hq < 1 || Hq % c->Hkv || !scale_ok(scale, c->k_exp))
     return DF_ERR_ARG;
   if (c->b == 0) return DF_OK;
   if (!q || !cache_len || !out) return DF_ERR_ARG;
@@ -114,8 +120,8 @@ int dflash_kv4_attention_weights(const df_kv4_cache* c, int layer, int n_tree, i
                                  float* score_out, void* ws, size_t ws_bytes, df_stream stream) {
   DF_NVTX("dflash_kv4_attention_weights");
   DF_TRY(cache_ok(c));
-  if (layer < 0 || layer >= c->n_layers || n_tree < 1 || Hq < 1 || Hq % c->Hkv || !(scale > 0.f) ||
-      !std::isfinite(scale) || !(decay >= 0.f && decay <= 1.f) || max_src < 0)
+  if (layer < 0 || layer >= c->n_layers || n_tree < 1 || Hq < 1 || Hq % c->Hkv || !scale_ok(scale, c->k_exp) ||
+      !(decay >= 0.f && decay <= 1.f) || max_src < 0)
     return DF_ERR_ARG;
   if (c->b == 0) return DF_OK;
   if (!q || !lse || !cache_len || !score || !score_out) return DF_ERR_ARG;

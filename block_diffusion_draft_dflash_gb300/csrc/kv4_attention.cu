@@ -128,10 +128,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_attn_kernel(const __grid_c
       mx[q][0] = mx[q][1] = -INFINITY;
       l[q][0] = l[q][1] = 0.f;
     }
+    int i = 0;
 #pragma unroll 1
-    for (int i = 0; i < mine; ++i) {
-      ok = ok && kv4_wait(&bars[warp][slot], phase, p.status, 50);
-      ok = __all_sync(0xffffffffu, ok);
+    for (; i < mine; ++i) {
+      ok = __all_sync(0xffffffffu, ok && kv4_wait(&bars[warp][slot], phase, p.status, 50));
+      if (!ok) break;
       const unsigned char* st = ring + slot * kStageBytes;
       const unsigned char *skc = st, *svc = st + kStageKeys * kKv4Codes;
       const unsigned char *sks = st + 2 * kStageKeys * kKv4Codes, *svs = sks + kStageKeys * kKv4Scales;
@@ -256,7 +257,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_attn_kernel(const __grid_c
         }
       }
       __syncwarp();   // every lane has read the stage
-      if (ok && i + kStages < mine) issue(i + kStages, slot);
+      if (i + kStages < mine) issue(i + kStages, slot);
+      if (++slot == kStages) { slot = 0; phase ^= 1; }
+    }
+    for (const int out = min(mine, i + kStages); i < out; ++i) {   // given up: the copies on their way must land
+      kv4_wait(&bars[warp][slot], phase, nullptr, 0);
       if (++slot == kStages) { slot = 0; phase ^= 1; }
     }
     // ---------------------------------------------------------------- merge the warps
@@ -310,7 +315,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_attn_kernel(const __grid_c
         *reinterpret_cast<uint2*>(p.out + grow * 128 + d) = w2;
         if (p.lse && d == 0) p.lse[grow] = kv4_lse(M, L, kPShift);
       } else {
-        const size_t at = (size_t)(blockIdx.x + seg.unit) * R + r;
+        const size_t at = (size_t)kv4_slot(p, blockIdx.x, seg.first, seg.last, 0) * R + r;
         *reinterpret_cast<float4*>(p.o_part + at * 128 + d) = acc;
         if (d == 0) p.ml_part[at] = make_float2(M, L);
       }
@@ -335,7 +340,10 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const Kv4AttnParams p)
   // parts: one a CTA, or two of a tile whose halves share their rows
   const int per = kv4_single(p, r / p.R) ? 2 : 1, parts = (c1 - c0 + 1) * per;
   if (parts <= 1) return;
-  auto slot = [&](int i) { return ((size_t)unit + c0 + i / per) * p.R + (i % per) * (p.R / 2) + r % p.R; };
+  auto slot = [&](int i) {
+    const int c = c0 + i / per;
+    return (size_t)kv4_slot(p, c, c == c0, c == c1, s * p.Hkv + kvh) * p.R + (i % per) * (p.R / 2) + r % p.R;
+  };
   // lane i holds part i's maximum and sum (parts behind the 32nd in turn)
   float M = -INFINITY;
   for (int i = lane; i < parts; i += 32) M = fmaxf(M, p.ml_part[slot(i)].x);
@@ -389,6 +397,9 @@ void kv4_attn_plan(int T, int G, Kv4AttnParams& p) {
   p.change_step = p.R == 256 ? 1 : 2;
   p.n_cta = num_sms() * (p.R == 256 ? 1 : 2);
 }
+size_t kv4_attn_slots(int b, int Hkv, const Kv4AttnParams& p) {
+  return (size_t)2 * p.n_cta + (p.last_single ? (size_t)b * Hkv : 0);
+}
 size_t up16(size_t x) { return (x + 15) & ~(size_t)15; }
 }  // namespace
 
@@ -396,7 +407,7 @@ size_t kv4_attn_scratch_bytes(int b, int T, int Hq, int Hkv, int cap) {
   (void)cap;
   Kv4AttnParams p{};
   kv4_attn_plan(T, Hq / Hkv, p);
-  const size_t units = (size_t)b * Hkv * p.nrt, slots = p.n_cta + units;
+  const size_t units = (size_t)b * Hkv * p.nrt, slots = kv4_attn_slots(b, Hkv, p);
   return up16(slots * p.R * (128 * 4 + 8)) + up16(units * sizeof(int2));
 }
 
@@ -410,7 +421,7 @@ int launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t st) {
   p.v_mul = ldexpf(1.f, a.v_exp);
   p.out = a.out; p.lse = a.lse; p.status = a.status;
   kv4_attn_plan(a.T, p.G, p);
-  const size_t units = (size_t)a.b * a.Hkv * p.nrt, slots = p.n_cta + units;
+  const size_t slots = kv4_attn_slots(a.b, a.Hkv, p);
   p.o_part = static_cast<float*>(a.scratch);
   p.ml_part = reinterpret_cast<float2*>(p.o_part + slots * p.R * 128);
   p.range = reinterpret_cast<int2*>(static_cast<unsigned char*>(a.scratch) + up16(slots * p.R * (128 * 4 + 8)));

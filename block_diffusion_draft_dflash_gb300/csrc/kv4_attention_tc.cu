@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const __grid_c
       const float m2 = m_run == -INFINITY ? -INFINITY : m_run * qs;
       const bool whole = sg.first && sg.last && !sg.single;
       const float inv = m_run == -INFINITY ? 0.f : p.v_mul / l;
-      const size_t at = (size_t)(blockIdx.x + sg.unit) * p.R + w * 128 + r0;   // the warp's first row in the parts
+      const size_t at = (size_t)kv4_slot(p, blockIdx.x, sg.first, sg.last, sg.s * p.Hkv + sg.kvh) * p.R + w * 128 + r0;   // the warp's first row in the parts
       // O goes out by way of the warp's own rows of Q, which no product reads any more: 32 rows x
       // 128 bytes, swizzled, then 8 lanes write a row's 128 bytes
       if (live) {

@@ -5,6 +5,7 @@
 // stages of a call lie in one line (sequence-major), which the CTAs cut into equal shares
 // whatever the sequences' lengths.  A unit that lies inside one share is finished by its CTA;
 // the parts of a cut unit go to slots that the combine kernel reads in the order of the CTAs.
+// A share cuts two units at most, the one it begins in and the one it ends in.
 #pragma once
 #include "kv4.cuh"
 #include "kv4.h"
@@ -33,8 +34,8 @@ struct Kv4AttnParams {
   int change_step;       // a seventh of what going over to another unit costs, in stages
   int n_cta;
   float shift;           // probabilities carry 2^shift
-  float* o_part;         // [n_cta + units][R][128]: slot CTA + unit
-  float2* ml_part;       // [n_cta + units][R]: maximum in log2 units, sum
+  float* o_part;         // [slots][R][128]: two of each CTA, then (last_single) one of each kv head
+  float2* ml_part;       // [slots][R]: maximum in log2 units, sum
   int2* range;           // [units]: first and last CTA
   int* status;
 };
@@ -215,6 +216,12 @@ struct Kv4Walk {
     return true;
   }
 };
+
+// Slot of a unit's part: 2 CTA for one that does not begin the unit, 2 CTA + 1 for one that
+// begins but does not end it; a single tile that is not cut has one of its own.
+DF_DEV int kv4_slot(const Kv4AttnParams& p, int cta, bool first, bool last, int head) {
+  return first && last ? 2 * p.n_cta + head : 2 * cta + (first ? 1 : 0);
+}
 
 // 32 bits of a row's visibility for keys j0 .. j0+31.
 KV4_COLD uint32_t kv4_see_bits(const uint32_t* anc, int W, int N, int j0, int node, int len) {

@@ -539,3 +539,102 @@ def test_a_run_of_steps():
     assert st == 0
     for s in range(b):
         check_attention(np64(out)[s], np64(lse)[s], np64(q)[s], *held[0][s], [list(range(41))], [0])
+
+
+# ------------------------------------------------------------ shares, streams, failures
+@pytest.mark.parametrize("b,T,Hq,Hkv,cap,tree", [
+    (40, 1, 32, 8, 400, False),        # more (sequence, kv head) units than CTAs: shares cut the units of few rows
+    (24, 65, 32, 8, 200, True),        # the same for tiles of 256 rows, the last of them with 4
+    (70, 2, 8, 4, 96, False),          # more sequences than a warp has lanes
+    (33, 20, 8, 2, 136, True),
+    (3, 700, 8, 2, 1000, False),       # a chain's tiles differ in length
+    (1, 513, 32, 8, 2000, True),
+])
+def test_attention_over_many_units(b, T, Hq, Hkv, cap, tree):
+    rng = np.random.default_rng(b)
+    lens = [int(x) for x in rng.integers(0, cap - T + 1, b)]
+    lens[0], lens[-1] = 0, cap - T
+    c, k, v = filled(21, 1, b, Hkv, cap, [n + T for n in lens])
+    q = bf16(synth.normal(22, "q", (b, T, Hq, 128)) * 1.5)
+    parents = [random_tree(T, s) for s in range(b)] if tree else [None] * b
+    anc = torch.from_numpy(np.stack([ddtree.ancestor_mask(p) for p in parents]).view(np.int32)).to(DEV) if tree else None
+    out, lse, st = run_attention(c, 0, q, lens, anc)
+    assert st == 0
+    qn, o, l = np64(q), np64(out), np64(lse)
+    for s in sorted({0, b - 1, *rng.integers(0, b, 6).tolist()}):
+        rows = sorted({0, T - 1, *rng.integers(0, T, 5).tolist()})
+        sets = {i: list(range(lens[s])) + [lens[s] + j for j in kv4.visible(parents[s], T, i)] for i in rows}
+        check_attention(o[s], l[s], qn[s], k[0, s].transpose(1, 0, 2), v[0, s].transpose(1, 0, 2), sets, rows)
+
+
+def test_weights_of_a_long_chain_over_many_units():
+    # 300 rows x 2 heads: ten rounds of rows; 80 units
+    b, T, Hq, Hkv, cap = 10, 300, 16, 8, 360
+    lens = [300 + 6 * s for s in range(b)]
+    c, k, v = filled(23, 1, b, Hkv, cap, lens)
+    q = bf16(synth.normal(23, "q", (b, T, Hq, 128)))
+    out, lse, st = run_attention(c, 0, q, [n - T for n in lens], None)
+    assert st == 0
+    score = torch.zeros(1, b, Hkv, cap, device=DEV)
+    assert run_weights(c, 0, q, lse, lens, score) == 0
+    # every (row, head) distributes weight 1; 2 heads a kv head
+    np.testing.assert_allclose(np64(score).sum(-1), np.full((1, b, Hkv), 2.0 * T), rtol=2e-5)
+    for s in (0, b - 1):
+        kk = k[0, s].transpose(1, 0, 2)
+        want = kv4.weights(np64(q)[s], np64(lse)[s], kk, SCALE, np.zeros((Hkv, cap)), lens[s], list(range(T)))
+        E = 130 * 2.0 ** -24 * SCALE * np.abs(np64(q)[s]).sum(-1).max() * np.abs(kk).max() + 2.0 ** -16
+        assert (np.abs(np64(score)[0, s] - want) <= (2 * E + 300 * 2.0 ** -24) * want + 1e-30).all()
+
+
+def test_calls_on_two_streams():
+    # two attentions at once, each with a workspace of its own, give what they give alone
+    cases = []
+    for seed, T, N in ((24, 1, 3000), (25, 80, 900)):
+        c, _, _ = filled(seed, 1, 2, 2, (N + 87) // 8 * 8, [N + T] * 2)     # cap is a multiple of 8
+        q = bf16(synth.normal(seed, "q", (2, T, 8, 128)))
+        lens = i32([N, N // 2])
+        alone = run_attention(c, 0, q, [N, N // 2], None)
+        cases.append((c, q, lens, alone, torch.zeros_like(q), ws_of(_lib.kv4_attention_workspace_size(c, T, 8)), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, q, lens, _, out, ws, st in cases:
+            with torch.cuda.stream(st):
+                _lib.kv4_attention(c, 0, q, lens, None, SCALE, out, ws)
+    torch.cuda.synchronize()
+    for c, q, lens, alone, out, ws, st in cases:
+        assert ws.status() == 0 and torch.equal(out, alone[0])
+
+
+@pytest.mark.parametrize("T", [1, 4, 60])
+def test_attention_gives_up_when_its_waits_run_out(T):
+    # a limit of 1 ns on every wait: the call may report DF_ERR_TIMEOUT, and it ends; the next one is right
+    c, k, v = filled(26, 1, 2, 2, 2400, [2300, 2300])
+    q = bf16(synth.normal(26, "q", (2, T, 8, 128)))
+    ws = ws_of(_lib.kv4_attention_workspace_size(c, T, 8))
+    good = run_attention(c, 0, q, [2200, 500], None, ws)
+    assert good[2] == 0
+    ws.configure(wait_limit_ns=1)
+    for _ in range(3):
+        assert run_attention(c, 0, q, [2200, 500], None, ws)[2] in (0, -7)
+    ws.configure()
+    again = run_attention(c, 0, q, [2200, 500], None, ws)
+    assert again[2] == 0 and torch.equal(again[0], good[0]) and torch.equal(again[1], good[1])
+
+
+def test_binding_refuses_what_the_kernels_would_misread():
+    c = new_cache(1, 2, 2, 64)
+    q, out = torch.zeros(2, 3, 4, 128, dtype=torch.bfloat16, device=DEV), torch.zeros(2, 3, 4, 128, dtype=torch.bfloat16, device=DEV)
+    ws = ws_of(_lib.kv4_attention_workspace_size(c, 3, 4))
+    lens = i32([0, 0])
+    for bad in (dict(q=q.float()), dict(q=q.transpose(1, 2)), dict(q=q[:1]), dict(cache_len=lens.long()), dict(cache_len=lens.cpu()),
+                dict(anc=torch.zeros(2, 3, 2, dtype=torch.int32, device=DEV)), dict(out=out[:, :2]), dict(lse=torch.zeros(2, 3, 3, device=DEV))):
+        kw = dict(q=q, cache_len=lens, anc=None, out=out, lse=None)
+        kw.update(bad)
+        with pytest.raises(ValueError):
+            _lib.kv4_attention(c, 0, kw["q"], kw["cache_len"], kw["anc"], SCALE, kw["out"], ws, lse=kw["lse"])
+    with pytest.raises(_lib.StatusError):
+        _lib.kv4_attention(c, 0, q, lens, None, SCALE, out, ws_of(256))           # a workspace too small
+    with pytest.raises(ValueError):
+        _lib.kv4_attention_weights(c, 0, q, torch.zeros(2, 3, 4, device=DEV), lens, SCALE, torch.zeros(1, 2, 2, 63, device=DEV), ws)
+    with pytest.raises(ValueError):
+        _lib.kv4_append(c, 0, q, q, lens, ws)                                      # 4 heads, the cache has 2
