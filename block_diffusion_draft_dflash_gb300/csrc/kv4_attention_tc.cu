@@ -106,9 +106,9 @@ struct Rows {
   }
   DF_DEV int step(const Kv4AttnParams& p, int x) const { return p.g_magic ? __umulhi(x, p.g_magic) : x; }
   DF_DEV int node(const Kv4AttnParams& p, int k) const { return node0 + step(p, rem0 + k); }
-  DF_DEV long long index(const Kv4AttnParams& p, int k) const {   // -1: behind the last row
+  DF_DEV int at(const Kv4AttnParams& p, int k) const {   // behind `base`; -1: behind the last row
     const int q = step(p, rem0 + k), n = node0 + q;
-    return n < p.T ? base + (long long)n * p.Hq + (rem0 + k - q * p.G) : -1;
+    return n < p.T ? n * p.Hq + (rem0 + k - q * p.G) : -1;
   }
 };
 
@@ -407,39 +407,43 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const __grid_c
       const bool live = row0 + r0 < p.T * p.G;                    // the warp has a row
       if (sg.len == 0 && threadIdx.x == 0) set_status(p.status, DF_ERR_CAPACITY, sg.s);
       // Q into its swizzled places as bf16 (16 lanes a row), then every lane brings its own row to
-      // fp16 by a power of two; every S of the previous unit is complete (o_full).
+      // fp16 by a power of two; every S of the previous unit is complete (o_full).  Everything
+      // is unrolled: one warp's latency is what the first product waits for.
       float qs;
       {
         const Rows rows(p, sg.s, sg.kvh, row0 + r0);
+        const int row_at = rows.at(p, lane);   // the lane's row behind rows.base, -1: none
         const uint32_t box = smem_u32(q_smem + w * kTile + r0 * 128);
         const int c = lane & 15;
-#pragma unroll 4
+        const df_bf16* q = p.q + rows.base * 128 + c * 8;
+#pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int lr = i * 2 + (lane >> 4);
-          const long long at = rows.index(p, lr);
+          const int at = __shfl_sync(0xffffffffu, row_at, lr);
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"   // no bytes: zeros
                        ::"r"(box + (c >> 3) * (kTile / 2) + lr * 128 + (((c & 7) ^ (lr & 7)) * 16)),
-                         "l"(p.q + (at < 0 ? 0 : at) * 128 + c * 8), "r"(at < 0 ? 0 : 16) : "memory");
+                         "l"(q + (size_t)max(at, 0) * 128), "r"(at < 0 ? 0 : 16) : "memory");
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
         unsigned char* mine = q_smem + w * kTile + (r0 + lane) * 128;
         auto place = [&](int i) { return reinterpret_cast<uint4*>(mine + (i >> 3) * (kTile / 2) + (((i & 7) ^ (lane & 7)) * 16)); };
+        uint4 v[16];
         float amax = 0.f, back;
-#pragma unroll 4
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = *place(i);
+#pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const uint4 v = *place(i);
-          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+          const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             amax = max3(amax, fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xFFFF0000u)));
         }
         const float f = f16_row_factor(amax, back);
         qs = p.scale2 * back;
-#pragma unroll 4
+#pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const uint4 v = *place(i);
-          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+          const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
           uint32_t h[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) h[e] = pack_f16x2(__uint_as_float(x[e] << 16) * f, __uint_as_float(x[e] & 0xFFFF0000u) * f);
@@ -535,6 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const __grid_c
       // 128 bytes, swizzled, then 8 lanes write a row's 128 bytes
       if (live) {
         const Rows rows(p, sg.s, sg.kvh, row0 + r0);
+        const int row_at = rows.at(p, lane);
         unsigned char* box = q_smem + w * kTile + r0 * 128;
         const int sw = lane & 7;
 #pragma unroll 1
@@ -558,21 +563,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const __grid_c
                   make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
           __syncwarp();
-#pragma unroll 2
+          const int d = lane & 7;   // a row's 16 bytes of these 128
+          unsigned char* to = whole ? reinterpret_cast<unsigned char*>(p.out + rows.base * 128) + (c >> 1) * 128 + d * 16
+                                    : reinterpret_cast<unsigned char*>(p.o_part + at * 128) + c * 128 + d * 16;
+          const int bytes = whole ? 256 : 512;   // of a row
+#pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int lr = i * 4 + (lane >> 3);
-            const long long to = rows.index(p, lr);
-            const uint4 v = *reinterpret_cast<const uint4*>(box + lr * 128 + (((lane & 7) ^ (lr & 7)) * 16));
-            if (to >= 0)
-              *reinterpret_cast<uint4*>(whole ? reinterpret_cast<unsigned char*>(p.out + to * 128 + (c >> 1) * 64 + (lane & 7) * 8)
-                                              : reinterpret_cast<unsigned char*>(p.o_part + (at + lr) * 128 + c * 32 + (lane & 7) * 4)) = v;
+            const int lr = i * 4 + (lane >> 3), row = __shfl_sync(0xffffffffu, row_at, lr);
+            const uint4 v = *reinterpret_cast<const uint4*>(box + lr * 128 + ((d ^ (lr & 7)) * 16));
+            if (row >= 0) *reinterpret_cast<uint4*>(to + (size_t)(whole ? row : lr) * bytes) = v;
           }
           __syncwarp();
         }
-        const long long to = rows.index(p, lane);
-        if (to >= 0) {
+        if (row_at >= 0) {
           if (!whole) p.ml_part[at + lane] = make_float2(m2, l);
-          else if (p.lse) p.lse[to] = kv4_lse(m2, l, kTcShift);   // m2 = -inf gives -inf
+          else if (p.lse) p.lse[rows.base + row_at] = kv4_lse(m2, l, kTcShift);   // m2 = -inf gives -inf
         }
       }
       if (threadIdx.x == 0) {
