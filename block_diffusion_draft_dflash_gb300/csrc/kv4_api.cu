@@ -96,7 +96,7 @@ int dflash_kv4_attention(const df_kv4_cache* c, int layer, int n_tree, int Hq, c
   if (!q || !cache_len || !out) return DF_ERR_ARG;
   if (!al16(q) || !al16(out) || (anc && !al16(anc))) return DF_ERR_ALIGN;
   // 32-bit row numbers, and stages (of 32 slots and a tile of rows) of the whole call
-  if (c->cap > 1 << 20 || Hq / c->Hkv > 4096 || (long long)n_tree * Hq > (1 << 30) || (long long)c->b * n_tree * Hq / 8 >= kGridLimit ||
+  if (c->cap > 1 << 20 || Hq / c->Hkv > 4096 || (long long)n_tree * Hq > (1 << 30) || (long long)c->b * (((long long)n_tree * Hq + 7) / 8) > kGridLimit ||
       (double)c->b * c->Hkv * (c->cap / 32 + 2) * ((double)n_tree * (Hq / c->Hkv) / 256 + 1) > 1e9)
     return DF_ERR_SHAPE;
   if (!ws || ws_bytes < dflash_kv4_attention_workspace_size(c, n_tree, Hq)) return DF_ERR_WORKSPACE;

@@ -325,42 +325,57 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_attn_kernel(const __grid_c
   }
 }
 
-// One warp per query row of a cut unit: the parts in the order of the CTAs.
-__global__ void __launch_bounds__(256) kv4_combine_kernel(const Kv4AttnParams p) {
+// One warp per query row of a cut unit: the parts in the order of the CTAs.  What bounds it is
+// latency, so the first parts' outputs are on their way before their weights are known.
+constexpr int kCombRows = 8, kCombParts = 8;   // rows of a CTA; parts brought at once
+__global__ void __launch_bounds__(kCombRows * 32) kv4_combine_kernel(const Kv4AttnParams p, int ctas) {   // CTAs of a sequence
+  const int s = blockIdx.x / ctas, at = (int)(blockIdx.x - s * ctas) * kCombRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int node = at / p.Hq, head = at - node * p.Hq;
+  const int kvh = p.g_magic ? __umulhi(head, p.g_magic) : head, r = node * p.G + head - kvh * p.G;
+  const int rt = r / p.R, in_tile = r - rt * p.R;
   pdl_wait();
   pdl_trigger();
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= (long long)p.b * p.T * p.Hq) return;
-  const int head = (int)(row % p.Hq), node = (int)(row / p.Hq % p.T), s = (int)(row / p.Hq / p.T);
-  const int kvh = head / p.G, r = node * p.G + head % p.G;
-  const int unit = (s * p.Hkv + kvh) * p.nrt + r / p.R;
-  const int2 range = p.range[unit];
+  if (node >= p.T) return;
+  const size_t row = ((size_t)s * p.T + node) * p.Hq + head;
+  const int2 range = p.range[(s * p.Hkv + kvh) * p.nrt + rt];
   const int c0 = max(range.x, 0), c1 = min(range.y, p.n_cta - 1);
   // parts: one a CTA, or two of a tile whose halves share their rows
-  const int per = kv4_single(p, r / p.R) ? 2 : 1, parts = (c1 - c0 + 1) * per;
+  const int two = kv4_single(p, rt) ? 1 : 0, parts = (c1 - c0 + 1) << two;
   if (parts <= 1) return;
   auto slot = [&](int i) {
-    const int c = c0 + i / per;
-    return (size_t)kv4_slot(p, c, c == c0, c == c1, s * p.Hkv + kvh) * p.R + (i % per) * (p.R / 2) + r % p.R;
+    const int c = c0 + (i >> two);
+    return (size_t)kv4_slot(p, c, c == c0, c == c1, s * p.Hkv + kvh) * p.R + (i & two) * (p.R / 2) + in_tile;
+  };
+  float4 o[kCombParts];
+  auto bring = [&](int i0) {
+#pragma unroll
+    for (int i = 0; i < kCombParts; ++i)
+      o[i] = i0 + i < parts ? reinterpret_cast<const float4*>(p.o_part + slot(i0 + i) * 128)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
   };
   // lane i holds part i's maximum and sum (parts behind the 32nd in turn)
-  float M = -INFINITY;
-  for (int i = lane; i < parts; i += 32) M = fmaxf(M, p.ml_part[slot(i)].x);
+  float2 v = lane < parts ? p.ml_part[slot(lane)] : make_float2(-INFINITY, 0.f);
+  bring(0);
+  float M = v.x;
+  for (int i = 32 + lane; i < parts; i += 32) M = fmaxf(M, p.ml_part[slot(i)].x);
   M = warp_max(M);
   float L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < parts; i0 += 32) {
-    const float2 v = i0 + lane < parts ? p.ml_part[slot(i0 + lane)] : make_float2(-INFINITY, 0.f);
+  for (int i0 = 0;;) {
     const float f = v.x == -INFINITY ? 0.f : ex2_approx(v.x - M);
     L += warp_sum(f * v.y);
-    const int n = min(32, parts - i0);
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-      const float4 o = reinterpret_cast<const float4*>(p.o_part + slot(i0 + i) * 128)[lane];
-      const float fi = __shfl_sync(0xffffffffu, f, i);
-      acc.x += fi * o.x; acc.y += fi * o.y; acc.z += fi * o.z; acc.w += fi * o.w;
+    const int end = min(i0 + 32, parts);
+    for (int j = i0;;) {
+#pragma unroll
+      for (int i = 0; i < kCombParts; ++i) {   // parts behind the last: 0 times 0
+        const float fi = __shfl_sync(0xffffffffu, f, (j + i) & 31);
+        acc.x += fi * o[i].x; acc.y += fi * o[i].y; acc.z += fi * o[i].z; acc.w += fi * o[i].w;
+      }
+      if ((j += kCombParts) >= end) break;
+      bring(j);
     }
+    if ((i0 += 32) >= parts) break;
+    v = i0 + lane < parts ? p.ml_part[slot(i0 + lane)] : make_float2(-INFINITY, 0.f);
+    bring(i0);
   }
   const float inv = L > 0.f ? p.v_mul / L : 0.f;
   uint2 w2;
@@ -432,8 +447,8 @@ int launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t st) {
   }
   p.shift = p.R == 256 ? kTcShift : kPShift;
   DF_TRACE("kv4_combine", st);
-  const long long nrows = (long long)a.b * a.T * a.Hq;
-  launch_k(kv4_combine_kernel, dim3((unsigned)((nrows + 7) / 8)), dim3(256), 0, st, p);
+  const int ctas = (a.T * a.Hq + kCombRows - 1) / kCombRows;
+  launch_k(kv4_combine_kernel, dim3((unsigned)(a.b * ctas)), dim3(kCombRows * 32), 0, st, p, ctas);
   return cudaGetLastError() == cudaSuccess ? DF_OK : DF_ERR_CUDA;
 }
 
