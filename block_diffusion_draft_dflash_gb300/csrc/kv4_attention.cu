@@ -1,5 +1,4 @@
-// Attention over a KV cache held in 4 bits, for few query rows per kv head, and the attention
-// weight that given rows lay on every slot.
+// Attention over a KV cache held in 4 bits, for few query rows per kv head.
 //
 // Row (s, i, h) sees slots [0, N) and the tree slots N + j of its ancestors, N = cache_len[s]:
 //   out = softmax(scale q K^T) V,  lse = log of the softmax's sum
@@ -37,32 +36,6 @@ DF_DEV uint32_t transpose8(uint32_t x) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
-}
-
-// A query row's share of a lane: dimensions 32 t4 .. + 31 as fp16 (brought there by a power of
-// two that the quad agrees on, `back` its inverse), two registers for each of 8 steps.
-DF_DEV void load_q(const df_bf16* src, bool on, int t4, uint32_t (&f)[8][2], float& back) {
-  uint4 raw[4];
-  float amax = 0.f;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) raw[c] = on ? reinterpret_cast<const uint4*>(src + t4 * 32)[c] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
-  }
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-  const float s = f16_row_factor(amax, back);
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      f[2 * c + (e >> 1)][e & 1] = pack_f16x2(__uint_as_float(w[e] << 16) * s, __uint_as_float(w[e] & 0xFFFF0000u) * s);
-  }
 }
 
 template <int NT>   // tiles of 8 query rows
@@ -449,176 +422,6 @@ int launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t st) {
   DF_TRACE("kv4_combine", st);
   const int ctas = (a.T * a.Hq + kCombRows - 1) / kCombRows;
   launch_k(kv4_combine_kernel, dim3((unsigned)(a.b * ctas)), dim3(kCombRows * 32), 0, st, p, ctas);
-  return cudaGetLastError() == cudaSuccess ? DF_OK : DF_ERR_CUDA;
-}
-
-// --------------------------------------------------------------------- attention weights
-constexpr int kWtRows = 64;    // query rows of a round
-constexpr int kWtKeys = 32;    // keys of a warp and stage
-
-struct Kv4WeightsParams {
-  Kv4WeightsArgs a;
-  Kv4AttnParams walk;   // its units are (sequence, kv head), its stages 256 slots
-  int G;
-  float scale2;         // scale * log2(e) * 2^k_exp
-};
-
-// S^T = K Q^T: the keys are the rows of the product, so a slot's weight is a sum along a lane's
-// own accumulators and one exchange inside the quad.  A warp owns its slots: no atomics, and
-// the order of every sum is fixed.  A CTA converts a round of query rows once and runs over its
-// share of the slots, the next stage's codes on their way meanwhile; further rounds add to what
-// the first has written.
-__global__ void __launch_bounds__(kWarps * 32, 2) kv4_weights_kernel(const __grid_constant__ Kv4WeightsParams p) {
-  __shared__ __align__(16) uint4 qf[kWtRows / 8][4][32];   // [row tile][two steps][lane]
-  __shared__ __align__(16) float2 row_sl[kWtRows];         // raw score -> log2 units, lse in log2 units
-  __shared__ __align__(8) int row_see[kWtRows];            // last slot that the row sees
-  pdl_wait();
-  pdl_trigger();
-  const Kv4WeightsArgs& a = p.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
-  Kv4Walk walk;
-  if (!walk.init(p.walk, blockIdx.x, lane)) return;
-  Kv4Seg seg;
-  while (walk.next(p.walk, seg)) {
-    const int s = seg.s, len = kv4_len(a.cache_len, s, 0, a.cap, a.status);
-    if (len < 0) continue;
-    const int n = a.n_rows ? a.n_rows[s] : a.T;
-    if (n < 0 || n > a.T || n > len || (a.src_slot && n > a.max_src + 1)) {
-      if (tid == 0) set_status(a.status, DF_ERR_ARG, s);
-      continue;
-    }
-    const int base = len - n;   // slots before the first row's own
-    const size_t plane = ((size_t)s * a.Hkv + seg.kvh) * a.cap;
-    const int total = n * p.G;
-    const int first = seg.tile0 * kWarps * kWtKeys + warp * kWtKeys + g;   // this lane's first key of four (8 apart)
-    for (int r0 = 0; r0 == 0 || r0 < total; r0 += kWtRows) {
-      __syncthreads();
-      // four lanes a row: to fp16 fragments
-      {
-        const int r = tid >> 2, q4 = tid & 3;   // row of the round, lane of its quad
-        const int rr = r0 + r, j = rr / p.G;
-        int node = -1;
-        if (rr < total) {
-          node = !a.src_slot ? j : j == 0 ? 0 : a.src_slot[(size_t)s * a.max_src + j - 1] - base;
-          if (node < 0 || node >= a.T) {
-            set_status(a.status, DF_ERR_ARG, s);
-            node = -1;
-          }
-        }
-        const size_t grow = ((size_t)s * a.T + (node < 0 ? 0 : node)) * a.Hq + seg.kvh * p.G + rr - j * p.G;
-        uint32_t f[8][2];
-        float back;
-        load_q(a.q + grow * 128, node >= 0, q4, f, back);
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          qf[r >> 3][c][(r & 7) * 4 + q4] = make_uint4(f[2 * c][0], f[2 * c][1], f[2 * c + 1][0], f[2 * c + 1][1]);
-        if (q4 == 0) {
-          float lse2 = INFINITY;   // such a row adds 2^(-inf) = 0 everywhere
-          if (node >= 0) {
-            const float v = a.lse[grow];
-            if (v != -INFINITY) lse2 = v * 1.4426950408889634f;
-          }
-          row_sl[r] = make_float2(p.scale2 * back, lse2);
-          row_see[r] = base + j;
-        }
-      }
-      __syncthreads();
-      const int tiles = (min(kWtRows, total - r0) + 7) / 8;
-      uint4 c[4];
-      uint32_t two[4];
-      auto load = [&](int i) {   // codes of the i-th stage's four keys
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = first + i * kWarps * kWtKeys + e * 8;
-          c[e] = make_uint4(0u, 0u, 0u, 0u);
-          two[e] = 0u;
-          if (key < len) {
-            c[e] = *reinterpret_cast<const uint4*>(a.p.kc + (plane + key) * kKv4Codes + t4 * 16);
-            two[e] = *reinterpret_cast<const uint16_t*>(a.p.ks + (plane + key) * kKv4Scales + t4 * 2);
-          }
-        }
-      };
-      load(0);
-#pragma unroll 1
-      for (int i = 0; i < seg.count; ++i) {
-        const int key0 = first + i * kWarps * kWtKeys;
-        // K fragments: tile h has keys key0 + 16 h and 8 further as its rows g and g + 8
-        uint32_t kf[2][8][4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t pa = e4m3x2_to_f16(__byte_perm(two[e], 0, 0x4140));
-          const uint32_t sc[2] = {__byte_perm(pa, 0, 0x1010), __byte_perm(pa, 0, 0x3232)};
-          const uint32_t w[4] = {c[e].x, c[e].y, c[e].z, c[e].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t f[4];
-            e2m1x8_to_f16(w[k], f);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) kf[e >> 1][2 * k + (x >> 1)][(x & 1) * 2 + (e & 1)] = hmul2(f[x], sc[k >> 1]);
-          }
-        }
-        if (i + 1 < seg.count) load(i + 1);
-        float mass[4] = {0.f, 0.f, 0.f, 0.f};
-        const bool edge = key0 - g + kWtKeys > base + 1;
-#pragma unroll 1
-        for (int q = 0; q < tiles; ++q) {
-          float d[2][4] = {};
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint4 b = qf[q][x][lane];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              mma_f16_16816(d[h], kf[h][2 * x], b.x, b.y);
-              mma_f16_16816(d[h], kf[h][2 * x + 1], b.z, b.w);
-            }
-          }
-          const float4 sl = *reinterpret_cast<const float4*>(&row_sl[q * 8 + t4 * 2]);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float x[4] = {fmaf(d[h][0], sl.x, -sl.y), fmaf(d[h][1], sl.z, -sl.w), fmaf(d[h][2], sl.x, -sl.y), fmaf(d[h][3], sl.z, -sl.w)};
-            if (edge) {
-              const int2 see = *reinterpret_cast<const int2*>(&row_see[q * 8 + t4 * 2]);
-              const int k = key0 + h * 16;
-              if (k > see.x) x[0] = -INFINITY;
-              if (k > see.y) x[1] = -INFINITY;
-              if (k + 8 > see.x) x[2] = -INFINITY;
-              if (k + 8 > see.y) x[3] = -INFINITY;
-            }
-            mass[2 * h] += ex2_approx(x[0]) + ex2_approx(x[1]);
-            mass[2 * h + 1] += ex2_approx(x[2]) + ex2_approx(x[3]);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          mass[e] += __shfl_xor_sync(0xffffffffu, mass[e], 1);
-          mass[e] += __shfl_xor_sync(0xffffffffu, mass[e], 2);
-        }
-        // lane t4 of a quad writes the t4-th of its keys
-        const int key = key0 + t4 * 8;
-        const float m = t4 == 0 ? mass[0] : t4 == 1 ? mass[1] : t4 == 2 ? mass[2] : mass[3];
-        if (key < len) {
-          const float old = r0 > 0 ? a.score_out[plane + key] : key < base ? a.decay * a.score[plane + key] : 0.f;
-          a.score_out[plane + key] = old + m;
-        }
-      }
-    }
-  }
-}
-
-int launch_kv4_weights(const Kv4WeightsArgs& a, cudaStream_t st) {
-  DF_TRACE("kv4_attention_weights", st);
-  Kv4WeightsParams p{};
-  p.a = a;
-  p.G = a.Hq / a.Hkv;
-  p.scale2 = ldexpf(a.scale * 1.4426950408889634f, a.k_exp);
-  Kv4AttnParams& w = p.walk;
-  w.b = a.b; w.Hkv = a.Hkv; w.cap = a.cap; w.cache_len = a.cache_len;
-  w.T = 0; w.G = 1; w.R = 1; w.nrt = 1;
-  w.stage_log2 = 8;
-  w.min_stages = 1;
-  w.change_step = 1;
-  w.n_cta = num_sms() * 2;
-  launch_k(kv4_weights_kernel, dim3(w.n_cta), dim3(kWarps * 32), 0, st, p);
   return cudaGetLastError() == cudaSuccess ? DF_OK : DF_ERR_CUDA;
 }
 

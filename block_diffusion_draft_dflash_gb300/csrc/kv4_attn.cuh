@@ -259,6 +259,32 @@ DF_DEV bool kv4_wait(uint64_t* bar, uint32_t parity, int* status, int where) {
   return mbar_try_wait(bar, parity) || kv4_wait_slow(bar, parity, status, where);
 }
 
+// A query row's share of a lane: dimensions 32 t4 .. + 31 as fp16 (brought there by a power of
+// two that the quad agrees on, `back` its inverse), two registers for each of 8 steps.
+DF_DEV void load_q(const df_bf16* src, bool on, int t4, uint32_t (&f)[8][2], float& back) {
+  uint4 raw[4];
+  float amax = 0.f;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) raw[c] = on ? reinterpret_cast<const uint4*>(src + t4 * 32)[c] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+  }
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  const float s = f16_row_factor(amax, back);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      f[2 * c + (e >> 1)][e & 1] = pack_f16x2(__uint_as_float(w[e] << 16) * s, __uint_as_float(w[e] & 0xFFFF0000u) * s);
+  }
+}
+
 // Probabilities of the tcgen05 kernel carry 2^7: with the 2^8 that a late maximum may add they stay below 2^15.
 constexpr float kTcShift = 7.f;
 constexpr float kLn2 = 0.6931471805599453f;
