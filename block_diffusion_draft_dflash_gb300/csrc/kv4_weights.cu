@@ -7,8 +7,8 @@
 //
 // Warp roles: one warp brings codes (untiled bulk copies), 8 warps decode them into 128-byte-
 // swizzled fp16 tiles, one issues the products, two groups of 4 warps take the blocks in turn,
-// each with a buffer of 256 TMEM columns.  A unit is one (sequence, kv head); with more than
-// 256 rows it is walked again for the next ones, which add to what the first have written.
+// each with two buffers of 128 TMEM columns.  A unit is one (sequence, kv head); with more than
+// 128 rows it is walked again for the next ones, which add to what the first have written.
 #include <math.h>
 
 #include "kv4_attn.cuh"
@@ -22,10 +22,11 @@ constexpr int kExpWarps = 8, kDecWarps = 8;
 constexpr int kDec0 = kExpWarps, kMmaWarp = kDec0 + kDecWarps, kLoadWarp = kMmaWarp + 1;
 constexpr int kThreads = (kLoadWarp + 1) * 32;
 constexpr int kKB = 128;                       // keys of a block; launch: stage_log2
-constexpr int kRows = 256;                     // query rows of a pass
+constexpr int kRows = 128;                     // query rows of a pass
+constexpr int kBufs = 512 / kRows;             // TMEM buffers of a block's products
 constexpr uint32_t kTile = 128 * 128 * 2;      // one fp16 tile: two slabs of 64 columns
 constexpr uint32_t kQSlab = kRows * 128;       // Q: two slabs of 64 dimensions
-constexpr int kTiles = 3, kRaw = 5, kSegs = 4; // rings of decoded tiles, codes, passes
+constexpr int kTiles = 3, kRaw = 10, kSegs = 4; // rings of decoded tiles, codes, passes
 constexpr int kRawScales = kKB * kKv4Codes;    // codes [key][64], then scales [key][8]
 constexpr int kRawBytes = kRawScales + kKB * kKv4Scales;
 
@@ -48,7 +49,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_weights_kernel(const __grid_c
   unsigned char* q_smem = smem;
   unsigned char* t_smem = q_smem + 2 * kQSlab;
   unsigned char* raw_smem = t_smem + kTiles * kTile;
-  __shared__ __align__(8) uint64_t r_full[kRaw], r_empty[kRaw], t_full[kTiles], t_empty[kTiles], s_full[2], s_empty[2];
+  __shared__ __align__(8) uint64_t r_full[kRaw], r_empty[kRaw], t_full[kTiles], t_empty[kTiles], s_full[kBufs], s_empty[kBufs];
   __shared__ __align__(8) uint64_t q_full, unit_done, drain, seg_full[kSegs], seg_empty[kSegs];
   __shared__ Pass passes[kSegs];
   __shared__ __align__(16) float row_s[kRows], row_nl[kRows];   // raw score -> log2 units, -lse in log2 units
@@ -60,7 +61,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_weights_kernel(const __grid_c
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRaw; ++i) { mbar_init(&r_full[i], 1); mbar_init(&r_empty[i], kDecWarps); }
     for (int i = 0; i < kTiles; ++i) { mbar_init(&t_full[i], kDecWarps); mbar_init(&t_empty[i], 1); }
-    for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], kExpWarps / 2); }
+    for (int i = 0; i < kBufs; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], kExpWarps / 2); }
     for (int i = 0; i < kSegs; ++i) { mbar_init(&seg_full[i], 1); mbar_init(&seg_empty[i], kLoadWarp); }
     mbar_init(&q_full, kExpWarps);
     mbar_init(&unit_done, kExpWarps);
@@ -89,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_weights_kernel(const __grid_c
     ++n_pass;
     return x;
   };
-  auto columns = [](const Pass& x) { return min(kRows, max(1, x.total - x.r0) + 31 & ~31); };   // of the products
+  auto columns = [](const Pass& x) { return min(kRows, (max(1, x.total - x.r0) + 31) & ~31); };   // of the products
 
   if (warp == kLoadWarp) {
     // ---------------------------------------------------------------- bring codes
@@ -178,27 +179,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_weights_kernel(const __grid_c
     }
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- MMA issuer
+    // Whatever an MMA's operands depend on is made warp-uniform (a reduction's result is).
     const bool leader = elect_one();
-    const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);   // warp-uniform operands issue faster
+    const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
     const uint64_t q_desc = sdesc_kmajor_sw128(smem_u32(q_smem)), k_desc = sdesc_kmajor_sw128(smem_u32(t_smem));
     int buf = 0, phase = 0, j = 0;   // tile ring; blocks so far
     while (true) {
       const Pass x = take();
-      if (!ok || x.count == 0) break;
+      const int count = __reduce_max_sync(0xffffffffu, x.count);
+      if (!ok || count == 0) break;
       const uint32_t idesc = idesc_f16_f32(128, __reduce_max_sync(0xffffffffu, columns(x)), false);
       if (!wait(&q_full, n_pass - 1, 75)) break;
-      for (int i = 0; i < x.count; ++i, ++j) {
-        if (!wait(&t_full[buf], phase, 76) || !wait(&s_empty[j & 1], (j >> 1) ^ 1, 77)) break;
+      for (int i = 0; i < count; ++i, ++j) {
+        if (!wait(&t_full[buf], phase, 76) || !wait(&s_empty[j % kBufs], (j / kBufs) ^ 1, 77)) break;
         tc_fence_after();
         if (leader) {
           const uint64_t kd = k_desc + buf * (kTile >> 4);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             const uint32_t step = (kk & 3) * (32 >> 4);
-            mma_bf16(tm + (j & 1) * kRows, kd + (kk >> 2) * (kTile / 2 >> 4) + step, q_desc + (kk >> 2) * (kQSlab >> 4) + step, idesc,
+            mma_bf16(tm + (j % kBufs) * kRows, kd + (kk >> 2) * (kTile / 2 >> 4) + step, q_desc + (kk >> 2) * (kQSlab >> 4) + step, idesc,
                      kk > 0 ? 1u : 0u);
           }
-          mma_commit(&s_full[j & 1]);
+          mma_commit(&s_full[j % kBufs]);
           mma_commit(&t_empty[buf]);
         }
         __syncwarp();
@@ -214,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_weights_kernel(const __grid_c
   } else {
     // ---------------------------------------------------------------- weights
     const int w = warp >> 2, my_key = (warp & 3) * 32 + lane;
-    const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + w * kRows;
+    const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     int j = 0;   // blocks so far
     while (true) {
       const Pass x = take();
@@ -257,15 +260,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_weights_kernel(const __grid_c
       if (lane == 0) mbar_arrive(&q_full);
       if (!wait(&q_full, n_pass - 1, 79)) break;
       const size_t plane = ((size_t)x.s * a.Hkv + x.kvh) * a.cap;
+      // what the slot has already, brought a block ahead; a slot of the rows' own starts at 0
+      const float* from = x.r0 > 0 ? a.score_out : a.score;
+      const float keep = x.r0 > 0 ? 1.f : a.decay;
+      const int known = x.r0 > 0 ? x.len : x.base;
+      auto bring = [&](int i) {
+        const int key = x.key0 + i * kKB + my_key;
+        return i < x.count && key < known ? from[plane + key] : 0.f;
+      };
+      float next = bring((j & 1) ^ w);
       for (int i = 0; i < x.count; ++i, ++j) {
         if ((j & 1) != w) continue;
         const int key = x.key0 + i * kKB + my_key;
-        float old = 0.f;
-        if (key < x.len) {
-          if (x.r0 > 0) old = a.score_out[plane + key];
-          else if (key < x.base) old = a.decay * a.score[plane + key];
-        }
-        if (!wait(&s_full[w], j >> 1, 80)) break;
+        const float old = key < known ? keep * next : 0.f;
+        next = bring(i + 2);
+        if (!wait(&s_full[j % kBufs], j / kBufs, 80)) break;
         tc_fence_after();
         // Row r (of head r % G of node r / G) sees the slots up to its own: the first column that
         // sees this key.
@@ -275,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_weights_kernel(const __grid_c
 #pragma unroll 1
         for (int c = 0; c < cols; c += 32) {
           float v[32];
-          tmem_ld32(at + c, v);
+          tmem_ld32(at + (j % kBufs) * kRows + c, v);
           tmem_ld_wait();
           if (edge) {
 #pragma unroll
@@ -294,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_weights_kernel(const __grid_c
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s_empty[w]);
+        if (lane == 0) mbar_arrive(&s_empty[j % kBufs]);
         float m0, m1;
         unpack2(add2(mass[0], mass[1]), m0, m1);
         if (key < x.len) a.score_out[plane + key] = old + (m0 + m1);
