@@ -231,15 +231,23 @@ DF_DEV uint32_t evict_key(float score, int slot, int lo, int hi) {
 
 // One CTA per (layer, sequence, kv head): the key of the last kept slot, two bits a step (the
 // largest key that `budget` slots reach), then the kept slots in order, the lowest slots first
-// among equal keys.  What bounds it is the comparisons: a histogram of digits costs more, with
-// atomic counters (scores crowd into few digits: 52 us for 288 rows of 8449 scores) and with
-// counters in registers (47 us), than three comparisons of every key in each of at most 16
-// steps.  Every count is a whole number: no order of additions changes the choice.
+// among equal keys.  What bounds it is the comparisons, three of every key in a step, so the
+// steps begin behind the bits that the smallest and the largest score share, and once the
+// bracket holds kSelFew keys at most every warp goes on by itself with a list of those.
+// (A histogram of digits costs more than comparing: 52 us with atomic counters, 47 us with
+// counters in registers, for 288 rows of 8449 scores that take 23 us with all 16 steps over
+// whole rows.)  Every count is a whole number: no order of additions, and no order in that
+// list, changes the choice.
+constexpr int kSelFew = 256;   // eight keys a lane
 __global__ void __launch_bounds__(kSelThreads, 2) kv4_select_kernel(const Kv4EvictArgs a) {
   pdl_wait();
   pdl_trigger();
-  __shared__ int sums[17][4];
-  __shared__ int2 counts[kSelThreads / 32];
+  constexpr int kSelWarps = kSelThreads / 32;
+  __shared__ __align__(16) int4 sums[2][kSelWarps];
+  __shared__ int2 counts[kSelWarps];
+  __shared__ uint32_t least[kSelWarps], most[kSelWarps];
+  __shared__ __align__(16) uint32_t few[kSelFew];
+  __shared__ int n_few;
   const size_t plane = blockIdx.x;
   const int s = (int)((plane / a.Hkv) % a.b);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -254,23 +262,41 @@ __global__ void __launch_bounds__(kSelThreads, 2) kv4_select_kernel(const Kv4Evi
     for (int j = tid; j < a.budget; j += kSelThreads) kept[j] = j < len ? j : -1;
     return;
   }
-  const int lo = a.n_sink, hi = len - a.n_recent;
-  if (tid < 68) sums[tid >> 2][tid & 3] = 0;
+  const int lo = a.n_sink, hi = len - a.n_recent;   // the slots between are chosen by score
+  if (tid == 0) n_few = 0;
+  if (tid < kSelFew) few[tid] = 0u;
   extern __shared__ __align__(16) uint32_t keys[];
   const bool held = len <= kSelHeld;
   auto key_at = [&](int i) { return held ? keys[i] : i < len ? evict_key(score[i], i, lo, hi) : 0u; };
+  uint32_t k_min = 0xFFFFFFFFu, k_max = 0u;
+  auto see = [&](uint32_t k, int i) {
+    if (i >= lo && i < hi) {
+      k_min = min(k_min, k);
+      k_max = max(k_max, k);
+    }
+  };
   if (held) {   // a row of scores is 16-byte aligned and as long as cap, a multiple of 8
 #pragma unroll 4
     for (int i = tid; i < (len + 3) / 4; i += kSelThreads) {
       const float4 v = reinterpret_cast<const float4*>(score)[i];
       const int at = 4 * i;
-      reinterpret_cast<uint4*>(keys)[i] =
-          make_uint4(evict_key(v.x, at, lo, hi), at + 1 < len ? evict_key(v.y, at + 1, lo, hi) : 0u,
-                     at + 2 < len ? evict_key(v.z, at + 2, lo, hi) : 0u, at + 3 < len ? evict_key(v.w, at + 3, lo, hi) : 0u);
+      const uint4 k = make_uint4(evict_key(v.x, at, lo, hi), at + 1 < len ? evict_key(v.y, at + 1, lo, hi) : 0u,
+                                 at + 2 < len ? evict_key(v.z, at + 2, lo, hi) : 0u, at + 3 < len ? evict_key(v.w, at + 3, lo, hi) : 0u);
+      see(k.x, at); see(k.y, at + 1); see(k.z, at + 2); see(k.w, at + 3);
+      reinterpret_cast<uint4*>(keys)[i] = k;
     }
+  } else {
+#pragma unroll 4
+    for (int i = tid; i < len; i += kSelThreads) see(evict_key(score[i], i, lo, hi), i);
   }
+  __syncwarp();
+  k_min = __reduce_min_sync(0xffffffffu, k_min);
+  k_max = __reduce_max_sync(0xffffffffu, k_max);
+  if (lane == 0) { least[warp] = k_min; most[warp] = k_max; }
   __syncthreads();
-  // slots whose key is at least k[0], k[1], k[2] > 0, over the CTA
+  k_min = __reduce_min_sync(0xffffffffu, least[lane % kSelWarps]);
+  k_max = __reduce_max_sync(0xffffffffu, most[lane % kSelWarps]);
+  // slots of the row whose key is at least k[0], k[1], k[2] > 0
   auto reach = [&](const uint32_t (&k)[3], int step, int (&n)[3]) {
     int c[3] = {0, 0, 0};
     if (held) {
@@ -292,51 +318,118 @@ __global__ void __launch_bounds__(kSelThreads, 2) kv4_select_kernel(const Kv4Evi
     __syncwarp();
 #pragma unroll
     for (int x = 0; x < 3; ++x) c[x] = __reduce_add_sync(0xffffffffu, c[x]);
-    if (lane < 3) atomicAdd(&sums[step][lane], lane == 0 ? c[0] : lane == 1 ? c[1] : c[2]);
+    if (lane == 0) sums[step & 1][warp] = make_int4(c[0], c[1], c[2], 0);
     __syncthreads();
-#pragma unroll
-    for (int x = 0; x < 3; ++x) n[x] = sums[step][x];
+    const int4 all = lane < kSelWarps ? sums[step & 1][lane] : make_int4(0, 0, 0, 0);
+    n[0] = __reduce_add_sync(0xffffffffu, all.x);
+    n[1] = __reduce_add_sync(0xffffffffu, all.y);
+    n[2] = __reduce_add_sync(0xffffffffu, all.z);
   };
-  uint32_t prefix = 0;
-  bool exact = false;   // just `budget` slots reach prefix
+  // The bracket: keys from prefix on with the bits above `shift + 1` the same.  It holds the last
+  // kept key; `above` slots lie behind it, `inside` in it.
+  const uint32_t differ = k_min ^ k_max;
+  int above = lo + len - hi, inside = hi - lo;   // not kept by score: keys above all others
+  uint32_t prefix = 0xFFFFFFFFu;
+  bool exact = above >= a.budget;                // `budget` slots have at least the key prefix
+  int shift = -2;
+  if (!exact) {
+    shift = differ ? (31 - __clz(differ)) & ~1 : -2;
+    prefix = shift == 30 ? 0u : k_min >> (shift + 2) << (shift + 2);
+  }
+  // Keys that reach prefix plus 1, 2 and 3 times 2^shift are counted: the bracket shrinks to a quarter.
+  auto narrow = [&](const int (&n)[3]) {
+    const int d = (n[0] >= a.budget ? 1 : 0) + (n[1] >= a.budget ? 1 : 0) + (n[2] >= a.budget ? 1 : 0);
+    prefix |= (uint32_t)d << shift;
+    const int reached = d == 0 ? above + inside : d == 1 ? n[0] : d == 2 ? n[1] : n[2];
+    above = d == 0 ? n[0] : d == 1 ? n[1] : d == 2 ? n[2] : above;
+    inside = reached - above;
+    exact = reached == a.budget;
+    shift -= 2;
+  };
 #pragma unroll 1
-  for (int step = 0; step < 16 && !exact; ++step) {
-    const int shift = 30 - 2 * step;
+  for (int step = 0; shift >= 0 && !exact && inside > kSelFew; ++step) {
     const uint32_t k[3] = {prefix | 1u << shift, prefix | 2u << shift, prefix | 3u << shift};
     int n[3];
     reach(k, step, n);
-    const int d = (n[0] >= a.budget ? 1 : 0) + (n[1] >= a.budget ? 1 : 0) + (n[2] >= a.budget ? 1 : 0);
-    prefix |= (uint32_t)d << shift;
-    exact = d > 0 && (d == 1 ? n[0] : d == 2 ? n[1] : n[2]) == a.budget;
+    narrow(n);
   }
-  int want = len;   // of the slots whose key equals prefix: all, where it is exact
-  if (!exact) {
-    int n[3] = {0, 0, 0};
-    const uint32_t k[3] = {prefix + 1u, prefix + 1u, prefix + 1u};
-    if (prefix != 0xFFFFFFFFu) reach(k, 16, n);
-    want = a.budget - n[0];
+  if (shift >= 0 && !exact) {
+    // the keys inside, in any order: a lane marks those among 32 of its own, a warp takes their places at once
+    for (int base = warp * 32; base < len; base += 32 * kSelThreads) {
+      uint32_t mine = 0u;
+#pragma unroll 4
+      for (int x = 0; x < 32; ++x) {
+        const int i = base + x * kSelThreads + lane;
+        if (i >= len) break;
+        const uint32_t k = key_at(i);
+        if (i >= lo && i < hi && (shift == 30 || (k ^ prefix) >> (shift + 2) == 0u)) mine |= 1u << x;
+      }
+      __syncwarp();
+      const int n = __popc(mine);
+      int at = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += x;
+      }
+      int first = 0;
+      if (lane == 31 && at > 0) first = atomicAdd(&n_few, at);
+      at += __shfl_sync(0xffffffffu, first, 31) - n;
+      for (; mine; mine &= mine - 1) few[at++] = key_at(base + (__ffs(mine) - 1) * kSelThreads + lane);
+      __syncwarp();
+    }
+    __syncthreads();
+    uint32_t k8[kSelFew / 32];
+#pragma unroll
+    for (int x = 0; x < kSelFew / 32; ++x) k8[x] = few[x * 32 + lane];
+    const int listed_above = above;
+#pragma unroll 1
+    while (shift >= 0 && !exact) {
+      int n[3];
+#pragma unroll
+      for (int y = 0; y < 3; ++y) {
+        const uint32_t k = prefix | (uint32_t)(y + 1) << shift;
+        n[y] = 0;
+#pragma unroll
+        for (int x = 0; x < kSelFew / 32; ++x) n[y] += k8[x] >= k ? 1 : 0;
+        n[y] = __reduce_add_sync(0xffffffffu, n[y]) + listed_above;
+      }
+      narrow(n);
+    }
   }
+  const int want = a.budget - above;   // where it is not exact: of the slots whose key equals prefix
   // kept: keys above prefix, and the first `want` slots whose key equals it.  A warp takes a
   // piece of the row: it counts both kinds, then, knowing the counts before it, writes its part.
-  constexpr int kSelWarps = kSelThreads / 32;
   const int piece = ((len + kSelWarps - 1) / kSelWarps + 31) & ~31;
   const int p0 = min(len, warp * piece), p1 = min(len, p0 + piece);
   const uint32_t below = (1u << lane) - 1u;
+  const uint32_t over = exact ? prefix - 1u : prefix;   // kept whatever its slot: a key above this (exact: prefix > 0)
   int g = 0, e = 0;
 #pragma unroll 4
   for (int i = p0 + lane; i < p1; i += 32) {
     const uint32_t k = key_at(i);
-    g += k > prefix ? 1 : 0;
-    e += k == prefix ? 1 : 0;
+    g += k > over ? 1 : 0;
+    e += k == over ? 1 : 0;
   }
   __syncwarp();
   g = __reduce_add_sync(0xffffffffu, g);
   e = __reduce_add_sync(0xffffffffu, e);
   if (lane == 0) counts[warp] = make_int2(g, e);
   __syncthreads();
-  g = 0;
-  e = 0;
-  for (int w = 0; w < warp; ++w) { g += counts[w].x; e += counts[w].y; }
+  const int2 before = lane < warp ? counts[lane] : make_int2(0, 0);   // of the warps before this one
+  g = __reduce_add_sync(0xffffffffu, before.x);
+  e = __reduce_add_sync(0xffffffffu, before.y);
+  if (exact) {
+#pragma unroll 4
+    for (int i0 = p0; i0 < p1; i0 += 32) {
+      const int i = i0 + lane;
+      const bool keep = i < p1 && key_at(i) > over;
+      const uint32_t bits = __ballot_sync(0xffffffffu, keep);
+      if (keep) kept[g + __popc(bits & below)] = i;
+      g += __popc(bits);
+    }
+    return;
+  }
 #pragma unroll 2
   for (int i0 = p0; i0 < p1; i0 += 32) {
     const int i = i0 + lane;
