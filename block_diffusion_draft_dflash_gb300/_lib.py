@@ -404,7 +404,7 @@ class Kv4Cache:
     def _ws(self, ws):
         """A call's workspace and stream: the current stream of the current device, which has to be the cache's."""
         dev = self.index
-        if torch.cuda.current_device() != dev or ws.buf.get_device() != dev:
+        if torch._C._cuda_getDevice() != dev or ws.buf.get_device() != dev:
             raise ValueError(f"the current device and the workspace's have to be the cache's ({self.device})")
         return ws.buf.data_ptr(), ws.nbytes, torch._C._cuda_getCurrentRawStream(dev)
 

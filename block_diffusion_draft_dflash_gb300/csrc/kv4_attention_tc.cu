@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const __grid_c
             amax = max3(amax, fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xFFFF0000u)));
         }
         const float f = f16_row_factor(amax, back);
-        qs = p.scale2 * back;
+        qs = fmaxf(p.scale2 * back, 1.17549435e-38f);   // a masked score times it stays -inf; a real one is as good as 0
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};

@@ -156,7 +156,10 @@ def check_attention(got, got_lse, q, k, v, sets, rows, scale=SCALE):
     out, lse, size = kv4.attend(q[rows], k, v, scale, [sets[i] for i in rows])
     E = 130 * 2.0 ** -24 * np.abs(scale) * np.abs(q[rows]).sum(-1) * np.abs(k).max()
     rel = 2.0 ** -11 + 2.0 ** -11 + 2 * E + 2.0 ** -16
-    assert (np.abs(got[rows] - out) <= 2.0 ** -8 * np.abs(out) + rel[..., None] * size).all()
+    # A probability is an fp16 number that carries 2^7 at least: where it is subnormal its rounding is off by 2^-25
+    # at most, while the sum of all is 2^7 at least, the largest one's: 2^-32 of the value for each key that a row sees.
+    low = 2.0 ** -32 * np.array([len(sets[i]) for i in rows])[:, None, None] * np.abs(v).max()
+    assert (np.abs(got[rows] - out) <= 2.0 ** -8 * np.abs(out) + rel[..., None] * size + low).all()
     fin = np.isfinite(lse)
     np.testing.assert_array_equal(fin, np.isfinite(got_lse[rows]))
     tol = E + 2.0 ** -16 + 2.0 ** -22 * np.abs(np.where(fin, lse, 0))
@@ -240,6 +243,21 @@ def test_attention_queries_far_from_one(size):
                     [list(range(49)), list(range(50))], [0, 1], SCALE / size)
 
 
+@pytest.mark.parametrize("T", [1, 4, 40])
+@pytest.mark.parametrize("k_exp", [-32, 32])
+def test_attention_queries_of_zeros(T, k_exp):
+    # a padded row's weights are equal over what it sees, whatever the keys' exponent
+    c, k, v = filled(27, 1, 1, 2, 200, [130 + T], k_exp=k_exp)
+    q = synth.normal(27, "q", (1, T, 8, 128)) * 2.0 ** -k_exp
+    q[0, T - 1, :] = 0
+    q[0, 0, 3] = 0
+    q = bf16(q)
+    out, lse, st = run_attention(c, 0, q, [130], None)
+    assert st == 0
+    sets = {i: list(range(130 + i + 1)) for i in {0, T // 2, T - 1}}
+    check_attention(np64(out)[0], np64(lse)[0], np64(q)[0], k[0, 0].transpose(1, 0, 2), v[0, 0].transpose(1, 0, 2), sets, sorted(sets))
+
+
 @pytest.mark.parametrize("T", [1, 40])
 def test_attention_records_lengths_that_do_not_fit(T):
     c, k, v = filled(11, 1, 3, 2, 80, [80, 80, 30 + T])
@@ -291,6 +309,9 @@ def run_weights(c, layer, q, lse, lens, score, n_rows=None, src=None, decay=1.0,
     (3, 20, 10, 2, [150, 20, 3], 152, [[0, 3, 19], [0], []], 0.25),           # paths of a tree, one without rows
     (1, 70, 12, 1, [300], 304, [[0] + list(range(2, 66))], 0.0),              # 65 rows x 12 heads: several rounds
     (2, 5, 1, 1, [5, 40], 40, [[0, 1, 2, 3, 4], [0, 4]], 1.0),                # every slot is a row's own
+    (2, 40, 32, 4, [2999, 130], 3000, None, 0.5),                             # 320 rows over parts of a long cache
+    (2, 9, 16, 2, [1500, 3000], 3000, [[], [0, 1, 8]], 0.5),                  # a long sequence that only decays
+    (1, 1, 128, 1, [1025], 1032, None, 1.0),                                  # 128 rows just fill a pass
 ])
 def test_weights(b, T, Hq, Hkv, lens, cap, rows, decay):
     c, k, v = filled(13, 2, b, Hkv, cap, lens)
@@ -408,6 +429,8 @@ def scores(kind, shape, seed):
     (1, 1, 1, 64, [50], 40, 40, 0, "normal"),              # sinks fill the budget
     (1, 1, 2, 9000, [8999], 8998, 0, 8998, "normal"),      # one slot goes
     (1, 1, 1, 70000, [70000], 3000, 4, 64, "ties"),
+    (1, 1, 1, 70000, [69999], 30000, 4, 64, "normal"),     # longer than what one CTA holds
+    (1, 1, 1, 20000, [19997], 300, 0, 1, "normal"),
 ])
 def test_evict(n_layers, b, Hkv, cap, lens, budget, sink, recent, kind):
     c, _, _ = filled(18, n_layers, b, Hkv, cap, lens) if cap < 10000 else (new_cache(n_layers, b, Hkv, cap), None, None)
@@ -619,6 +642,30 @@ def test_attention_gives_up_when_its_waits_run_out(T):
     ws.configure()
     again = run_attention(c, 0, q, [2200, 500], None, ws)
     assert again[2] == 0 and torch.equal(again[0], good[0]) and torch.equal(again[1], good[1])
+
+
+def test_weights_give_up_when_their_waits_run_out():
+    c, k, v = filled(28, 1, 2, 2, 2400, [2300, 900])
+    q = bf16(synth.normal(28, "q", (2, 40, 8, 128)))
+    out, lse, st = run_attention(c, 0, q, [2260, 860], None)
+    assert st == 0
+    ws = ws_of(_lib.kv4_attention_weights_workspace_size(c, 40, 8))
+    score, lens = torch.zeros(1, 2, 2, 2400, device=DEV), i32([2300, 900])
+
+    def call():
+        to = torch.zeros_like(score)
+        _lib.kv4_attention_weights(c, 0, q, lse, lens, SCALE, score, ws, score_out=to)
+        torch.cuda.synchronize()
+        return to, ws.status()
+
+    good = call()
+    assert good[1] == 0
+    ws.configure(wait_limit_ns=1)
+    for _ in range(3):
+        assert call()[1] in (0, -7)
+    ws.configure()
+    again = call()
+    assert again[1] == 0 and torch.equal(again[0], good[0])
 
 
 def test_binding_refuses_what_the_kernels_would_misread():
