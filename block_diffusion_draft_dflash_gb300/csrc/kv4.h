@@ -39,7 +39,7 @@ struct Kv4AttnArgs {
   void* scratch;                // kv4_attn_scratch_bytes
   int* status;
 };
-size_t kv4_attn_scratch_bytes(int b, int T, int Hq, int Hkv, int cap);
+size_t kv4_attn_scratch_bytes(int b, int T, int Hq, int Hkv);
 int launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t st);
 
 struct Kv4WeightsArgs {

@@ -81,7 +81,7 @@ int dflash_kv4_append(const df_kv4_cache* c, int layer, const df_bf16* k, const 
 size_t dflash_kv4_attention_workspace_size(const df_kv4_cache* c, int n_tree, int Hq) {
   if (!c || c->b < 1 || c->Hkv < 1 || n_tree < 1 || Hq < 1 || Hq % c->Hkv) return kAlign;
   Carver cv(nullptr);
-  cv.take<unsigned char>(kv4_attn_scratch_bytes(c->b, n_tree, Hq, c->Hkv, c->cap));
+  cv.take<unsigned char>(kv4_attn_scratch_bytes(c->b, n_tree, Hq, c->Hkv));
   return cv.off;
 }
 
@@ -105,7 +105,7 @@ int dflash_kv4_attention(const df_kv4_cache* c, int layer, int n_tree, int Hq, c
   a.p = planes(c, layer); a.b = c->b; a.T = n_tree; a.Hq = Hq; a.Hkv = c->Hkv; a.cap = c->cap;
   a.q = q; a.cache_len = cache_len; a.anc = anc; a.scale = scale; a.k_exp = c->k_exp; a.v_exp = c->v_exp;
   a.out = out; a.lse = lse; a.status = status_of(ws);
-  a.scratch = cv.take<unsigned char>(kv4_attn_scratch_bytes(c->b, n_tree, Hq, c->Hkv, c->cap));
+  a.scratch = cv.take<unsigned char>(kv4_attn_scratch_bytes(c->b, n_tree, Hq, c->Hkv));
   return launch_kv4_attention(a, (cudaStream_t)stream);
 }
 

@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_attn_kernel(const __grid_c
         *reinterpret_cast<uint2*>(p.out + grow * 128 + d) = w2;
         if (p.lse && d == 0) p.lse[grow] = kv4_lse(M, L, kPShift);
       } else {
-        const size_t at = (size_t)kv4_slot(p, blockIdx.x, seg.first, seg.last, 0) * R + r;
+        const size_t at = (size_t)kv4_slot(blockIdx.x, seg.first) * R + r;
         *reinterpret_cast<float4*>(p.o_part + at * 128 + d) = acc;
         if (d == 0) p.ml_part[at] = make_float2(M, L);
       }
@@ -312,13 +312,9 @@ __global__ void __launch_bounds__(kCombRows * 32) kv4_combine_kernel(const Kv4At
   const size_t row = ((size_t)s * p.T + node) * p.Hq + head;
   const int2 range = p.range[(s * p.Hkv + kvh) * p.nrt + rt];
   const int c0 = max(range.x, 0), c1 = min(range.y, p.n_cta - 1);
-  // parts: one a CTA, or two of a tile whose halves share their rows
-  const int two = kv4_single(p, rt) ? 1 : 0, parts = (c1 - c0 + 1) << two;
+  const int parts = c1 - c0 + 1;
   if (parts <= 1) return;
-  auto slot = [&](int i) {
-    const int c = c0 + (i >> two);
-    return (size_t)kv4_slot(p, c, c == c0, c == c1, s * p.Hkv + kvh) * p.R + (i & two) * (p.R / 2) + in_tile;
-  };
+  auto slot = [&](int i) { return (size_t)kv4_slot(c0 + i, i == 0) * p.R + in_tile; };
   float4 o[kCombParts];
   auto bring = [&](int i0) {
 #pragma unroll
@@ -385,18 +381,14 @@ void kv4_attn_plan(int T, int G, Kv4AttnParams& p) {
   p.change_step = p.R == 256 ? 1 : 2;
   p.n_cta = num_sms() * (p.R == 256 ? 1 : 2);
 }
-size_t kv4_attn_slots(int b, int Hkv, const Kv4AttnParams& p) {
-  return (size_t)2 * p.n_cta + (p.last_single ? (size_t)b * Hkv : 0);
-}
 size_t up16(size_t x) { return (x + 15) & ~(size_t)15; }
 }  // namespace
 
-size_t kv4_attn_scratch_bytes(int b, int T, int Hq, int Hkv, int cap) {
-  (void)cap;
+size_t kv4_attn_scratch_bytes(int b, int T, int Hq, int Hkv) {
   Kv4AttnParams p{};
   kv4_attn_plan(T, Hq / Hkv, p);
-  const size_t units = (size_t)b * Hkv * p.nrt, slots = kv4_attn_slots(b, Hkv, p);
-  return up16(slots * p.R * (128 * 4 + 8)) + up16(units * sizeof(int2));
+  const size_t units = (size_t)b * Hkv * p.nrt;
+  return up16((size_t)2 * p.n_cta * p.R * (128 * 4 + 8)) + up16(units * sizeof(int2));
 }
 
 int launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t st) {
@@ -409,7 +401,7 @@ int launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t st) {
   p.v_mul = ldexpf(1.f, a.v_exp);
   p.out = a.out; p.lse = a.lse; p.status = a.status;
   kv4_attn_plan(a.T, p.G, p);
-  const size_t slots = kv4_attn_slots(a.b, a.Hkv, p);
+  const size_t slots = (size_t)2 * p.n_cta;
   p.o_part = static_cast<float*>(a.scratch);
   p.ml_part = reinterpret_cast<float2*>(p.o_part + slots * p.R * 128);
   p.range = reinterpret_cast<int2*>(static_cast<unsigned char*>(a.scratch) + up16(slots * p.R * (128 * 4 + 8)));

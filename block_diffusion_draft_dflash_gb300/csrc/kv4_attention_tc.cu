@@ -7,7 +7,8 @@
 //   pair    the unit has more than 128 rows: the streams are two row tiles, and a stage is one
 //           block of 128 keys, decoded once for both;
 //   single  it has at most 128: both streams hold the same rows, and a stage is two blocks of
-//           128 keys, one for each.  Their results are merged like those of two CTAs.
+//           128 keys, one for each.  They hold the same rows in the same TMEM lanes, so each
+//           reads both outputs and writes half of the merged one's columns.
 // Either way a stage is two S = Q K^T, two softmax blocks and two O += P V, which makes equal
 // shares of stages (kv4_attn.cuh) equal shares of work.
 //
@@ -118,16 +119,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const __grid_c
   unsigned char* t_smem = q_smem + 2 * kTile;         // kTiles decoded tiles
   unsigned char* raw_smem = t_smem + kTiles * kTile;  // kRaw tiles of codes
   __shared__ __align__(8) uint64_t r_full[kRaw], r_empty[kRaw], t_full[kTiles], t_empty[kTiles];
-  __shared__ __align__(8) uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drain[2];
+  __shared__ __align__(8) uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drain[2], ml_full[2], merged;
   __shared__ __align__(8) uint64_t seg_full[kSegs], seg_empty[kSegs];
   __shared__ Kv4Seg segs[kSegs];
+  __shared__ float2 pair_ml[2][128];   // single: maximum and sum of a stream's rows
   __shared__ uint32_t tmem_slot;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRaw; ++i) { mbar_init(&r_full[i], 1); mbar_init(&r_empty[i], kDecWarps); }
     for (int i = 0; i < kTiles; ++i) { mbar_init(&t_full[i], kDecWarps); mbar_init(&t_empty[i], 2); }
-    for (int i = 0; i < 2; ++i) { mbar_init(&q_full[i], 4); mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4); mbar_init(&o_full[i], 1); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&q_full[i], 4); mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4); mbar_init(&o_full[i], 1); mbar_init(&ml_full[i], 4); }
+    mbar_init(&merged, 8);
     for (int i = 0; i < kSegs; ++i) { mbar_init(&seg_full[i], 1); mbar_init(&seg_empty[i], kLoadWarp); }
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
@@ -347,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const __grid_c
     regs_up<kSoftRegs>();
     const int w = warp >> 2, r0 = (warp & 3) * 32;
     const uint32_t sp = tmem + ((uint32_t)r0 << 16) + kSCol + w * 128, oaddr = sp - kSCol + kOCol;
-    int n_s = 0;   // S blocks seen so far
+    int n_s = 0, n_single = 0;   // S blocks, single units so far
     while (true) {
       const Kv4Seg& sg = take();   // given back behind the epilogue
       if (!ok || sg.count == 0) break;
@@ -479,10 +482,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const __grid_c
       ok = __all_sync(0xffffffffu, kv4_wait(&o_full[w], (n_seg - 1) & 1, p.status, 69));
       if (!ok) break;
       tc_fence_after();
-      const float m2 = m_run == -INFINITY ? -INFINITY : m_run * qs;
-      const bool whole = sg.first && sg.last && !sg.single;
-      const float inv = m_run == -INFINITY ? 0.f : p.v_mul / l;
-      const size_t at = (size_t)kv4_slot(p, blockIdx.x, sg.first, sg.last, sg.s * p.Hkv + sg.kvh) * p.R + w * 128 + r0;   // the warp's first row in the parts
+      float m2 = m_run == -INFINITY ? -INFINITY : m_run * qs, mine = 1.f, other = 0.f;
+      const bool single = sg.single, whole = sg.first && sg.last;
+      if (single) {
+        pair_ml[w][r0 + lane] = make_float2(m2, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ml_full[w]);
+        ok = __all_sync(0xffffffffu, kv4_wait(&ml_full[w ^ 1], n_single & 1, p.status, 56) &&
+                                         kv4_wait(&o_full[w ^ 1], (n_seg - 1) & 1, p.status, 56));
+        if (!ok) break;
+        tc_fence_after();
+        const float2 y = pair_ml[w ^ 1][r0 + lane];
+        const float M = fmaxf(m2, y.x);
+        mine = m2 == -INFINITY ? 0.f : ex2_approx(m2 - M);
+        other = y.x == -INFINITY ? 0.f : ex2_approx(y.x - M);
+        l = mine * l + other * y.y;
+        m2 = M;
+      }
+      const float inv = m2 == -INFINITY ? 0.f : p.v_mul / l;
+      const size_t at = (size_t)kv4_slot(blockIdx.x, sg.first) * p.R + (single ? 0 : w * 128) + r0;   // the warp's first row in the parts
       // O goes out by way of the warp's own rows of Q, which no product reads any more: 32 rows x
       // 128 bytes, swizzled, then 8 lanes write a row's 128 bytes
       if (live) {
@@ -491,10 +509,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const __grid_c
         unsigned char* box = q_smem + w * kTile + r0 * 128;
         const int sw = lane & 7;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = single ? 2 * w : 0; c < (single ? 2 * w + 2 : 4); ++c) {
           float o[32];
           tmem_ld32(oaddr + c * 32, o);
-          tmem_ld_wait();
+          if (single) {
+            float y[32];
+            tmem_ld32((oaddr ^ 128) + c * 32, y);   // the other stream's
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = mine * o[e] + other * y[e];
+          } else {
+            tmem_ld_wait();
+          }
           if (whole) {   // bf16: two of the four make one row of 128 bytes
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -523,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const __grid_c
           }
           __syncwarp();
         }
-        if (row_at >= 0) {
+        if (row_at >= 0 && !(single && w == 1)) {
           if (!whole) p.ml_part[at + lane] = make_float2(m2, l);
           else if (p.lse) p.lse[rows.base + row_at] = kv4_lse(m2, l, kTcShift);   // m2 = -inf gives -inf
         }
@@ -533,6 +559,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const __grid_c
         if (sg.last) p.range[sg.unit].y = blockIdx.x;
       }
       tc_fence_before();
+      if (single) {   // neither goes on before the other has read its output
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&merged);
+        ok = __all_sync(0xffffffffu, kv4_wait(&merged, n_single++ & 1, p.status, 57));
+        if (!ok) break;
+      }
       give_back();
     }
   }

@@ -34,7 +34,7 @@ struct Kv4AttnParams {
   int change_step;       // a seventh of what going over to another unit costs, in stages
   int n_cta;
   float shift;           // probabilities carry 2^shift
-  float* o_part;         // [slots][R][128]: two of each CTA, then (last_single) one of each kv head
+  float* o_part;         // [slots][R][128], two slots of each CTA
   float2* ml_part;       // [slots][R]: maximum in log2 units, sum
   int2* range;           // [units]: first and last CTA
   int* status;
@@ -217,11 +217,8 @@ struct Kv4Walk {
   }
 };
 
-// Slot of a unit's part: 2 CTA for one that does not begin the unit, 2 CTA + 1 for one that
-// begins but does not end it; a single tile that is not cut has one of its own.
-DF_DEV int kv4_slot(const Kv4AttnParams& p, int cta, bool first, bool last, int head) {
-  return first && last ? 2 * p.n_cta + head : 2 * cta + (first ? 1 : 0);
-}
+// Slot of a cut unit's part: 2 CTA + 1 for the one that begins the unit, 2 CTA for any other.
+DF_DEV int kv4_slot(int cta, bool first) { return 2 * cta + (first ? 1 : 0); }
 
 // 32 bits of a row's visibility for keys j0 .. j0+31.
 KV4_COLD uint32_t kv4_see_bits(const uint32_t* anc, int W, int N, int j0, int node, int len) {
