@@ -6,7 +6,9 @@
 // the fp16 tensor-core products are exact; sums, softmax statistics and outputs are fp32).
 //
 // What bounds it with few rows is the cache, 144 bytes a slot and kv head, and then the
-// instructions that decode it.  Every warp streams stages of 32 slots (bulk copies into a ring
+// instructions that decode it: one token of 16 sequences of 9803 to 32768 slots, 8 kv heads (393
+// MB), takes 81 us, 4.9 TB/s, with an instruction issued in 65 % of the schedulers' cycles; 8
+// rows of one sequence of 2000 slots take 8 us, which is latency.  Every warp streams stages of 32 slots (bulk copies into a ring
 // of its own, no CTA barrier), decodes codes straight into tensor-core fragments and keeps its
 // own running maximum, sum and output; the warps are merged when the CTA's part of a unit ends.
 //
@@ -370,7 +372,10 @@ int launch_kv4_attn_few(Kv4AttnParams p, cudaStream_t st) {
 }
 
 namespace {
-// Rows, stage and grid of a call, by its rows per kv head.
+// Rows, stage and grid of a call, by its rows per kv head.  Over 8 sequences of 16000 slots, 8
+// kv heads: 8 rows take 39 us in a tile of 8, 53 us in one of 16, 78 us on tcgen05; 16 rows
+// take 56 us in a tile of 16, 80 us on tcgen05; 32 rows take 95 us in two tiles of 16, 81 us on
+// tcgen05.  A share of fewer stages than warps would leave warps idle.
 void kv4_attn_plan(int T, int G, Kv4AttnParams& p) {
   const long long rows = (long long)T * G;
   p.R = rows <= 8 ? 8 : rows <= 16 ? 16 : 256;
