@@ -126,7 +126,7 @@ int dflash_kv4_attention_weights(const df_kv4_cache* c, int layer, int n_tree, i
   if (c->b == 0) return DF_OK;
   if (!q || !lse || !cache_len || !score || !score_out) return DF_ERR_ARG;
   if (!al16(q) || !al16(score) || !al16(score_out)) return DF_ERR_ALIGN;
-  if (c->cap > 1 << 20 || (long long)n_tree * Hq > (1 << 30) || (double)c->b * c->Hkv * (c->cap / 256 + 2) > 1e9) return DF_ERR_SHAPE;
+  if (c->cap > 1 << 20 || (long long)n_tree * Hq > (1 << 30) || (double)c->b * c->Hkv * (c->cap / 128 + 2) > 1e9) return DF_ERR_SHAPE;
   if (!ws || ws_bytes < dflash_kv4_attention_weights_workspace_size(c, n_tree, Hq)) return DF_ERR_WORKSPACE;
   Kv4WeightsArgs a{};
   a.p = planes(c, layer); a.b = c->b; a.T = n_tree; a.Hq = Hq; a.Hkv = c->Hkv; a.cap = c->cap;

@@ -306,7 +306,7 @@ constexpr int kCombRows = 8, kCombParts = 8;   // rows of a CTA; parts brought a
 __global__ void __launch_bounds__(kCombRows * 32) kv4_combine_kernel(const Kv4AttnParams p, int ctas) {   // CTAs of a sequence
   const int s = blockIdx.x / ctas, at = (int)(blockIdx.x - s * ctas) * kCombRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int node = at / p.Hq, head = at - node * p.Hq;
-  const int kvh = p.g_magic ? __umulhi(head, p.g_magic) : head, r = node * p.G + head - kvh * p.G;
+  const int kvh = head / p.G, r = node * p.G + head - kvh * p.G;
   const int rt = r / p.R, in_tile = r - rt * p.R;
   pdl_wait();
   pdl_trigger();

@@ -431,7 +431,8 @@ int dflash_kv4_attention_weights(const df_kv4_cache* cache, int layer, int n_tre
  * Row src_slot[s][j] moves to slot cache_len[s] - n_acc[s] + j, for j < n_acc[s].
  *   src_slot   [b][max_src] int32, ascending, each at or behind its destination
  *   n_acc      [b] int32, 0 <= n_acc <= max_src
- *   cache_len  [b] int32: the length with the path (accept_and_compact's) */
+ *   cache_len  [b] int32: the length with the path (accept_and_compact's)
+ * A sequence whose list, count or length does not fit is left as it was (DF_ERR_ARG). */
 size_t dflash_kv4_compact_workspace_size(void);
 int dflash_kv4_compact(const df_kv4_cache* cache, const int32_t* src_slot, int max_src, const int32_t* n_acc,
                        const int32_t* cache_len, void* ws, size_t ws_bytes, df_stream stream);
