@@ -142,6 +142,14 @@ int launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t st) {
   return cudaGetLastError() == cudaSuccess ? DF_OK : DF_ERR_CUDA;
 }
 
+// 16 bytes of a row's 64 codes.  Rows are picked here and there: without the hint L2 fetches the
+// neighbouring row with each.
+DF_DEV uint4 load_picked(const uint8_t* p) {
+  uint4 r;
+  asm volatile("ld.global.L2::64B.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+  return r;
+}
+
 // ----------------------------------------------------------------------------- compact
 constexpr int kCmpRows = 32;   // rows of one round: a path of accept_and_compact fits one
 
@@ -185,8 +193,8 @@ __global__ void __launch_bounds__(256) kv4_compact_kernel(const Kv4CompactArgs a
       const int row = i * 8 + (lane >> 2);
       const size_t at = (size_t)__shfl_sync(0xffffffffu, mine, row) * kKv4Codes + (lane & 3) * 16;
       if (r0 + row < n) {
-        k[i] = *reinterpret_cast<const uint4*>(kc + at);
-        v[i] = *reinterpret_cast<const uint4*>(vc + at);
+        k[i] = load_picked(kc + at);
+        v[i] = load_picked(vc + at);
       }
     }
     if (r0 + lane < n) {
@@ -469,7 +477,7 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4EvictArgs a, i
   const int i = j < a.budget ? kept[j] : -1;
   if (i < 0) return;
   const size_t ci = (from + i) * kKv4Codes + part * 16, co = (to + j) * kKv4Codes + part * 16;
-  const uint4 k = *reinterpret_cast<const uint4*>(a.src.kc + ci), v = *reinterpret_cast<const uint4*>(a.src.vc + ci);
+  const uint4 k = load_picked(a.src.kc + ci), v = load_picked(a.src.vc + ci);
   const uint8_t* sp = part < 2 ? a.src.ks : a.src.vs;
   uint8_t* dp = part < 2 ? a.dst.ks : a.dst.vs;
   const uint32_t sc = *reinterpret_cast<const uint32_t*>(sp + (from + i) * kKv4Scales + (part & 1) * 4);
