@@ -362,14 +362,22 @@ __global__ void __launch_bounds__(kSelThreads, 2) kv4_select_kernel(const Kv4Evi
   }
   if (shift >= 0 && !exact) {
     // the keys inside, in any order: a lane marks those among 32 of its own, a warp takes their places at once
-    for (int base = warp * 32; base < len; base += 32 * kSelThreads) {
+    const int quads = (len + 3) / 4;
+    for (int base = warp * 32; base < quads; base += 8 * kSelThreads) {
       uint32_t mine = 0u;
-#pragma unroll 4
-      for (int x = 0; x < 32; ++x) {
-        const int i = base + x * kSelThreads + lane;
-        if (i >= len) break;
-        const uint32_t k = key_at(i);
-        if (i >= lo && i < hi && (shift == 30 || (k ^ prefix) >> (shift + 2) == 0u)) mine |= 1u << x;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const int at = base + x * kSelThreads + lane, i = 4 * at;
+        if (at < quads) {
+          const uint4 v = held ? reinterpret_cast<const uint4*>(keys)[at]
+                               : make_uint4(key_at(i), key_at(i + 1), key_at(i + 2), key_at(i + 3));
+          const uint32_t k[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool in = shift == 30 || (k[e] ^ prefix) >> (shift + 2) == 0u;
+            if (in && i + e >= lo && i + e < hi) mine |= 1u << (4 * x + e);
+          }
+        }
       }
       __syncwarp();
       const int n = __popc(mine);
@@ -382,7 +390,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) kv4_select_kernel(const Kv4Evi
       int first = 0;
       if (lane == 31 && at > 0) first = atomicAdd(&n_few, at);
       at += __shfl_sync(0xffffffffu, first, 31) - n;
-      for (; mine; mine &= mine - 1) few[at++] = key_at(base + (__ffs(mine) - 1) * kSelThreads + lane);
+      for (; mine; mine &= mine - 1) {
+        const int b = __ffs(mine) - 1;
+        few[at++] = key_at(4 * (base + (b >> 2) * kSelThreads + lane) + (b & 3));
+      }
       __syncwarp();
     }
     __syncthreads();
@@ -481,10 +492,12 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4EvictArgs a, i
   const uint8_t* sp = part < 2 ? a.src.ks : a.src.vs;
   uint8_t* dp = part < 2 ? a.dst.ks : a.dst.vs;
   const uint32_t sc = *reinterpret_cast<const uint32_t*>(sp + (from + i) * kKv4Scales + (part & 1) * 4);
+  const bool scored = a.score_out && part == 0;
+  const float w = scored ? a.score[from + i] : 0.f;   // every load before the first store
   *reinterpret_cast<uint4*>(a.dst.kc + co) = k;
   *reinterpret_cast<uint4*>(a.dst.vc + co) = v;
   *reinterpret_cast<uint32_t*>(dp + (to + j) * kKv4Scales + (part & 1) * 4) = sc;
-  if (a.score_out && part == 0) a.score_out[to + j] = a.score[from + i];
+  if (scored) a.score_out[to + j] = w;
 }
 
 int launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t st) {
