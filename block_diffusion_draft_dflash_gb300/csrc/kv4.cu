@@ -4,7 +4,8 @@
 // scale of 16 values whose largest magnitude is a is s = e4m3(a / (6 * 2^exp)) and a value's
 // code e2m1(x / (s * 2^exp)), both rounded to nearest even and saturated.  The inputs are bf16
 // (8 significant bits), the borders between codes have at most 7 after multiplication with s
-// and the divisor 2^exp only shifts, so fp32 quotients that are exact at the borders give the codes that exact arithmetic gives.
+// and the divisor 2^exp only shifts, so fp32 quotients that are exact at the borders give the
+// codes that exact arithmetic gives.
 #include <cuda_fp8.h>
 #include <math.h>
 
