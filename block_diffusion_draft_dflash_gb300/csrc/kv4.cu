@@ -260,12 +260,12 @@ DF_DEV uint32_t evict_key(float score, int slot, int lo, int hi) {
 
 // One CTA per (layer, sequence, kv head): the key of the last kept slot, two bits a step (the
 // largest key that `budget` slots reach), then the kept slots in order, the lowest slots first
-// among equal keys.  What bounds it is the comparisons, three of every key in a step, so the
-// steps begin behind the bits that the smallest and the largest score share, and once the
-// bracket holds kSelFew keys at most every warp goes on by itself with a list of those.
-// 288 rows of 8449 scores take 23 us, 25 us with all 16 steps over whole rows, and more with a
-// histogram of digits: 52 us with atomic counters, 47 us with counters in registers.  Every count is a whole number: no order of additions, and no order in that
-// list, changes the choice.
+// among equal keys.  What bounds it is the comparisons, three of every key in a step, so the steps
+// begin behind the bits that the smallest and the largest score share, and once the bracket holds
+// kSelFew keys at most every warp goes on by itself with a list of those. 288 rows of 8449 scores
+// take 23 us, 25 us with all 16 steps over whole rows, and more with a histogram of digits: 52 us
+// with atomic counters, 47 us with counters in registers.  Every count is a whole number: no order
+// of additions, and no order in that list, changes the choice.
 constexpr int kSelFew = 256;   // eight keys a lane
 __global__ void __launch_bounds__(kSelThreads, 2) kv4_select_kernel(const Kv4EvictArgs a) {
   pdl_wait();

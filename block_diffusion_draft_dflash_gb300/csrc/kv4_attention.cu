@@ -7,10 +7,11 @@
 //
 // What bounds it with few rows is the cache, 144 bytes a slot and kv head, and then the
 // instructions that decode it: one token of 16 sequences of 9803 to 32768 slots, 8 kv heads (393
-// MB), takes 81 us, 4.9 TB/s, with an instruction issued in 65 % of the schedulers' cycles; 8
-// rows of one sequence of 2000 slots take 8 us, which is latency.  Every warp streams stages of 32 slots (bulk copies into a ring
-// of its own, no CTA barrier), decodes codes straight into tensor-core fragments and keeps its
-// own running maximum, sum and output; the warps are merged when the CTA's part of a unit ends.
+// MB), takes 81 us, 4.9 TB/s, with an instruction issued in 65 % of the schedulers' cycles; 8 rows
+// of one sequence of 2000 slots take 8 us, which is latency.  Every warp streams stages of 32 slots
+// (bulk copies into a ring of its own, no CTA barrier), decodes codes straight into tensor-core
+// fragments and keeps its own running maximum, sum and output; the warps are merged when the CTA's
+// part of a unit ends.
 //
 // Both products are transposed, S^T = K Q^T and O^T = V^T P^T: the cache is the 16-row operand
 // and the query rows are the 8 columns, so 8 rows (4 heads of a token, say) cost half of what
