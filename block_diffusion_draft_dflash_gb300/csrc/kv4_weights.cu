@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_weights_kernel(const __grid_c
             const float v = a.lse[grow];
             if (v != -INFINITY) nl = v * -1.4426950408889634f;
           }
-          row_s[r] = p.scale2 * back;
+          row_s[r] = fmaxf(p.scale2 * back, 1.17549435e-38f);   // a masked score times it stays -inf; a real one is as good as 0
           row_nl[r] = nl;
         }
       }

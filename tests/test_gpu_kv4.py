@@ -685,3 +685,56 @@ def test_binding_refuses_what_the_kernels_would_misread():
         _lib.kv4_attention_weights(c, 0, q, torch.zeros(2, 3, 4, device=DEV), lens, SCALE, torch.zeros(1, 2, 2, 63, device=DEV), ws)
     with pytest.raises(ValueError):
         _lib.kv4_append(c, 0, q, q, lens, ws)                                      # 4 heads, the cache has 2
+
+
+# ------------------------------------------------------- rows and lists at the edge of a call
+def vote(c, k, q, lse, lens, paths, scale=SCALE, decay=1.0, layer=0, cap=None):
+    """Scores of a call over paths (nodes of each sequence), and what the oracle makes of it."""
+    b, m = len(paths), max(2, max(len(p) for p in paths))
+    src = np.full((b, m), -1)
+    for s, p in enumerate(paths):
+        src[s, :len(p) - 1] = [lens[s] - len(p) + node for node in p[1:]]
+    score = torch.from_numpy(np.random.default_rng(1).random(c.rows, np.float32)).to(DEV)
+    before = np64(score)
+    ws = ws_of(_lib.kv4_attention_weights_workspace_size(c, q.shape[1], q.shape[2]))
+    _lib.kv4_attention_weights(c, layer, q, lse, i32(lens), scale, score, ws, n_rows=i32([len(p) for p in paths]), src_slot=i32(src),
+                               decay=decay)
+    torch.cuda.synchronize()
+    want = [kv4.weights(np64(q)[s], np64(lse)[s], k[layer, s].transpose(1, 0, 2), scale, before[layer, s], lens[s], p, decay)
+            for s, p in enumerate(paths)]
+    return np64(score)[layer], want, ws.status()
+
+
+def path_lse(k, q, lens, paths, scale):
+    """The oracle's log-sums of the rows of each path."""
+    lse = np.full(q.shape[:3], np.nan, np.float32)
+    for s, p in enumerate(paths):
+        kk = k[0, s].transpose(1, 0, 2)
+        for j, node in enumerate(p):
+            lse[s, node] = kv4.attend(np64(q)[s, node:node + 1], kk, kk, scale, [range(lens[s] - len(p) + j + 1)])[1][0]
+    return torch.from_numpy(lse).to(DEV)
+
+
+def check_votes(got, want, q, k, lens, paths, scale=SCALE):
+    # as in test_weights: a score is off by E at most, a weight by twice that of its value; a sum of rows x heads terms
+    for s, p in enumerate(paths):
+        n = lens[s]
+        E = 130 * 2.0 ** -24 * scale * np.abs(np64(q)[s]).sum(-1).max() * np.abs(k[0, s, :, :n]).max() + 2.0 ** -16
+        assert (np.abs(got[s][:, :n] - want[s][:, :n]) <= (2 * E + 2.0 ** -20) * want[s][:, :n] + 1e-30).all()
+
+
+@pytest.mark.parametrize("k_exp,scale", [(-32, SCALE), (32, SCALE), (-22, SCALE), (0, 1e-8), (0, 2.0 ** -120)])
+@pytest.mark.parametrize("Hq", [2, 16])
+def test_weights_of_query_rows_of_zeros(k_exp, scale, Hq):
+    # such a row's weights are equal over what it sees, and nothing behind that: the first row, one of the path, one head
+    T, lens = 9, [140, 30]
+    c, k, v = filled(29, 1, 2, 2, 200, lens, k_exp=k_exp)
+    q = synth.normal(29, "q", (2, T, Hq, 128)) * 2.0 ** -k_exp
+    q[:, 0] = 0
+    q[:, 4] = 0
+    q[:, 2, Hq - 1] = 0
+    q = bf16(q)
+    paths = [[0, 2, 4, 7, 8], [0, 1, 4]]
+    got, want, st = vote(c, k, q, path_lse(k, q, lens, paths, scale), lens, paths, scale)
+    assert st == 0
+    check_votes(got, want, q, k, lens, paths, scale)
