@@ -24,7 +24,7 @@ struct WsHeader {        // first 256 bytes of every workspace
   int status;            // first device-side error code (0 = none)
   int detail;            // kernel-specific detail for that error
   unsigned long long wait_limit_ns;  // limit of every bounded wait (0 = kWaitLimitNs)
-  int hold;              // test hook: nonzero makes each GEMM wait (bounded) for it to read 0
+  int hold;              // test hook: nonzero makes GEMMs and the 4-bit cache's attention wait (bounded) for it to read 0
   int pad[59];
 };
 static_assert(sizeof(WsHeader) == 256, "header size");

@@ -83,6 +83,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_attn_kernel(const __grid_c
     };
     const int mine = count > warp ? (count - warp + kWarps - 1) / kWarps : 0;
     for (int i = 0; i < kStages && i < mine; ++i) issue(i, (slot + i) % kStages);
+    const int held = kv4_held(p.status);   // on its way beside the rows
     // Q^T fragments: column n = g of tile q is row 8 q + g.  The products run over dimensions in
     // the order in which a lane finds its codes: 32 t4 .. + 31, four at a step.
     uint32_t qf[NT][8][2];
@@ -96,6 +97,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv4_attn_kernel(const __grid_c
       qs[q][0] = __shfl_sync(0xffffffffu, back, t4 * 8);
       qs[q][1] = __shfl_sync(0xffffffffu, back, t4 * 8 + 4);
     }
+    if (held && ok) ok = kv4_hold_clear(p.status, 51, lane);   // held: give up with copies on their way
     float o[NT][8][4], mx[NT][2], l[NT][2];
 #pragma unroll
     for (int q = 0; q < NT; ++q) {

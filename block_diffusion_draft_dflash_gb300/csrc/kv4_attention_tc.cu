@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const __grid_c
     int st = 0, phase = 0;
     Kv4Walk walk;
     Kv4Seg sg;
+    sg.held = kv4_held(p.status);
     bool more = walk.init(p, blockIdx.x, lane);
     while (ok) {
       sg.count = 0;
@@ -344,7 +345,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const __grid_c
       }
       if (!ok) break;
     }
-    if (!ok && issued) {   // giving up: the MMAs issued must finish before TMEM is freed
+    // TMEM is freed and the CTA ends only behind the MMAs issued.  They are done where every unit
+    // was finished, but the softmax warps may have given up when this role had nothing left to issue.
+    if (issued) {
       if (leader) mma_commit(&drain[w]);
       __syncwarp();
       kv4_wait(&drain[w], 0, nullptr, 0);
@@ -485,7 +488,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_tc_kernel(const __grid_c
       }
       if (!ok) break;
       // -------------------------------------------------------------- epilogue
-      ok = __all_sync(0xffffffffu, kv4_wait(&o_full[w], (n_seg - 1) & 1, p.status, 69));
+      // held: give up while the issuers finish the unit, or have left their role behind the last one
+      if (sg.held) ok = kv4_hold_clear(p.status, 55, lane);
+      ok = __all_sync(0xffffffffu, ok && kv4_wait(&o_full[w], (n_seg - 1) & 1, p.status, 69));
       if (!ok) break;
       tc_fence_after();
       float m2 = m_run == -INFINITY ? -INFINITY : m_run * qs, mine = 1.f, other = 0.f;

@@ -81,7 +81,16 @@ struct Kv4Seg {        // the part of one unit that a CTA works on
   int N, len;          // cache_len (0 where it does not fit), slots seen
   int first, last;     // holds the unit's first, last stage
   int single;          // kv4_single
+  int held;            // kv4_held, where a warp hands units out
 };
+
+// The workspace's hold word, which makes a call give up (tests of the failure path).  Read beside
+// the lengths: it costs no time of its own.
+DF_DEV int kv4_held(const int* status) { return *(const volatile int*)(status + 4); }
+// By a whole warp.
+KV4_COLD bool kv4_hold_clear(int* status, int where, int lane) {
+  return __all_sync(0xffffffffu, lane != 0 || wait_hold_clear(status, where));
+}
 
 // A CTA's walk through its share.  One warp of the CTA walks (code that a kernel runs once
 // costs some 50 cycles an instruction) and hands the units out by shared memory.

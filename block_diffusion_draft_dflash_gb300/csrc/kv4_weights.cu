@@ -45,6 +45,7 @@ struct Pass {           // rows r0 .. of a unit over a CTA's part of its keys
   int s, kvh, key0, count;   // first key, blocks
   int len, base;             // slots seen, slots before the first row's own
   int r0, total;             // first row of the pass, rows of the unit
+  int held;                  // kv4_held
 };
 
 __global__ void __launch_bounds__(kThreads, 1) kv4_weights_kernel(const __grid_constant__ Kv4WeightsParams p) {
@@ -101,10 +102,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_weights_kernel(const __grid_c
     int j = 0;   // tiles so far
     Kv4Walk walk;
     Kv4Seg sg;
+    const int held = kv4_held(status);
     bool more = walk.init(p.walk, blockIdx.x, lane);
     while (ok) {
       Pass x{};
       x.r0 = 0;
+      x.held = held;
       if (more) more = walk.next(p.walk, sg);
       if (more) {
         x.s = sg.s;
@@ -213,7 +216,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_weights_kernel(const __grid_c
       }
       if (!ok) break;
     }
-    if (!ok && j > 0) {   // giving up: the MMAs issued must finish before TMEM is freed
+    // TMEM is freed and the CTA ends only behind the MMAs issued.  They are done where every block
+    // was summed, but the weights' warps may have given up when this role had nothing left to issue.
+    if (j > 0) {
       if (leader) mma_commit(&drain);
       __syncwarp();
       kv4_wait(&drain, 0, nullptr, 0);
@@ -263,6 +268,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_weights_kernel(const __grid_c
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full);
       if (!wait(&q_full, n_pass - 1, 79)) break;
+      // held: give up while the issuer is at work, or has left its role behind the last block
+      if (x.held && !(ok = kv4_hold_clear(status, 81, lane))) break;
       const size_t plane = ((size_t)x.s * a.Hkv + x.kvh) * a.cap;
       // what the slot has already, brought a block ahead; a slot of the rows' own starts at 0
       const float* from = x.r0 > 0 ? a.score_out : a.score;

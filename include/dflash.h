@@ -543,8 +543,10 @@ int dflash_workspace_status(void* ws, df_stream stream);
  *                  (0 = the default, 2 s); a wait that runs out records DF_ERR_TIMEOUT and
  *                  its kernel returns without touching TMEM or shared memory still in use
  *   hold           test hook: nonzero makes every projection GEMM of such a call wait for
- *                  the word to read 0 before it issues any tensor-core work.  Nothing clears
- *                  it, so the wait runs out and the call reports DF_ERR_TIMEOUT; set 0 to go on.
+ *                  the word to read 0 before it issues any tensor-core work, and the attention
+ *                  and attention weights of a 4-bit cache before they take what their first
+ *                  copies and products bring.  Nothing clears it, so the wait runs out and the
+ *                  call reports DF_ERR_TIMEOUT; set 0 to go on.
  * Zero-initialised workspaces start with both at 0. */
 int dflash_workspace_configure(void* ws, unsigned long long wait_limit_ns, int hold, df_stream stream);
 /* Static text for a status code. */

@@ -738,3 +738,67 @@ def test_weights_of_query_rows_of_zeros(k_exp, scale, Hq):
     got, want, st = vote(c, k, q, path_lse(k, q, lens, paths, scale), lens, paths, scale)
     assert st == 0
     check_votes(got, want, q, k, lens, paths, scale)
+
+
+# ------------------------------------------------------------------ calls that give up
+def random_cache(b, Hkv, cap):
+    c = new_cache(1, b, Hkv, cap, 0, -2)
+    for t in (c.k_codes, c.k_scales, c.v_codes, c.v_scales):
+        t.random_(0, 256)
+    return c
+
+
+@pytest.mark.parametrize("b,T,Hq,Hkv,lens", [
+    (1, 1, 8, 2, [0]),                     # few rows: one stage
+    (2, 1, 8, 2, [2300, 500]),
+    (2, 4, 8, 2, [2300, 500]),             # 16 rows
+    (40, 1, 32, 8, [300] * 40),            # several units a CTA
+    (1, 17, 8, 8, [0]),                    # tcgen05, half a tile: one stage, then the issuer has nothing left
+    (2, 60, 8, 2, [2300, 500]),
+    (1, 513, 8, 8, [0]),                   # whole tiles
+    (2, 300, 8, 2, [6000, 500]),
+    (24, 65, 32, 8, [130] * 24),           # several units a CTA
+])
+def test_attention_that_is_held_gives_up(b, T, Hq, Hkv, lens):
+    # held for 20 ms behind its first copies and products: the call reports it and ends, and the next one is right
+    c = random_cache(b, Hkv, max(lens) // 8 * 8 + (T + 15) // 8 * 8)
+    q = bf16(synth.normal(30, "q", (b, T, Hq, 128)))
+    ws = ws_of(_lib.kv4_attention_workspace_size(c, T, Hq))
+    good = run_attention(c, 0, q, lens, None, ws)
+    assert good[2] == 0
+    for _ in range(3):
+        ws.configure(wait_limit_ns=20_000_000, hold=True)
+        assert run_attention(c, 0, q, lens, None, ws)[2] == -7
+        ws.configure()
+        again = run_attention(c, 0, q, lens, None, ws)
+        assert again[2] == 0 and torch.equal(again[0], good[0]) and torch.equal(again[1], good[1])
+
+
+@pytest.mark.parametrize("b,T,Hq,Hkv,lens", [
+    (1, 1, 2, 2, [8]),                     # one block, then the issuer has nothing left
+    (2, 40, 8, 2, [2300, 900]),
+    (2, 100, 16, 2, [2300, 900]),          # several passes
+    (8, 16, 32, 8, [4096] * 8),            # more blocks a CTA than products in flight
+    (40, 16, 32, 8, [300] * 40),           # several units a CTA
+])
+def test_weights_that_are_held_give_up(b, T, Hq, Hkv, lens):
+    c = random_cache(b, Hkv, max(lens) // 8 * 8 + 8)
+    q = bf16(synth.normal(31, "q", (b, T, Hq, 128)))
+    lse = run_attention(c, 0, q, [n - T for n in lens], None)[1]
+    ws = ws_of(_lib.kv4_attention_weights_workspace_size(c, T, Hq))
+    score, length = torch.zeros(c.rows, device=DEV), i32(lens)
+
+    def call():
+        to = torch.zeros_like(score)
+        _lib.kv4_attention_weights(c, 0, q, lse, length, SCALE, score, ws, score_out=to)
+        torch.cuda.synchronize()
+        return to, ws.status()
+
+    good = call()
+    assert good[1] == 0
+    for _ in range(3):
+        ws.configure(wait_limit_ns=20_000_000, hold=True)
+        assert call()[1] == -7
+        ws.configure()
+        again = call()
+        assert again[1] == 0 and torch.equal(again[0], good[0])
