@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   // core, so at most PV_{j-1} is still pending when block j's softmax looks at O.
   uint64_t* p_full = s_full + kSBufs;
   uint64_t* o_done = p_full + kSBufs;
-  uint64_t* mma_drain = o_done + kSBufs;  // completion of every MMA issued, when the issuer gives up
+  uint64_t* mma_drain = o_done + kSBufs;  // completion of every MMA issued
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_drain + 1);
   __shared__ float red_max[2][kCG][128];  // [block parity][column group][row]
   __shared__ float red_sum[kCG][128];
@@ -262,8 +262,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         idle = 0;
         t_idle = 0;
       }
-      if (!ok && (s_next > 0 || pv_next > 0)) {
-        // giving up: the MMAs already issued must finish before TMEM is freed
+      if (s_next > 0) {
+        // the MMAs issued must finish before TMEM is freed: the softmax may have given up when
+        // this role had nothing left to issue
         if (leader) mma_commit(mma_drain);
         __syncwarp();
         mbar_wait(mma_drain, 0, nullptr, 0);

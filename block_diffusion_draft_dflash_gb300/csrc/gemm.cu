@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint64_t* tfull = bars + 2 * S;
   uint64_t* tempty = bars + 2 * S + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 4);
-  uint64_t* mma_drain = bars + 2 * S + 5;  // completion of every MMA issued, when the issuer gives up
+  uint64_t* mma_drain = bars + 2 * S + 5;  // completion of every MMA issued
   // argmax epilogue: per warp, per 32-column chunk, per lane (= column) running maximum key
   unsigned long long* run_max = reinterpret_cast<unsigned long long*>(bars + 2 * S + 6);
 
@@ -316,8 +316,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       __syncwarp();
       ++si;
     }
-    if (issued_any && !ok) {
-      // giving up: the MMAs already issued must finish before TMEM is freed
+    if (issued_any) {
+      // the MMAs issued must finish before TMEM is freed: the epilogue may have given up when
+      // this role had nothing left to issue
       if (leader) mma_commit(mma_drain);
       __syncwarp();
       mbar_wait(mma_drain, 0, nullptr, 0);

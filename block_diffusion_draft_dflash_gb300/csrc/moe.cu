@@ -360,8 +360,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       __syncwarp();
       ++si;
     }
-    if (issued_any && !ok) {
-      // giving up: the MMAs already issued must finish before TMEM is freed
+    if (issued_any) {
+      // the MMAs issued must finish before TMEM is freed: the epilogue may have given up when
+      // this role had nothing left to issue
       if (leader) mma_commit(mma_drain);
       __syncwarp();
       mbar_wait(mma_drain, 0, nullptr, 0);
