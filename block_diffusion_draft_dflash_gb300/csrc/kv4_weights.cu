@@ -114,14 +114,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_weights_kernel(const __grid_c
         x.kvh = sg.kvh;
         x.key0 = sg.tile0 * kKB;
         x.count = sg.count;
+        const int32_t* src = a.src_slot + (size_t)x.s * a.max_src;
+        int mine = a.src_slot && lane < a.max_src ? src[lane] : 0;   // of the list, beside the lengths
+        const int n = a.n_rows ? a.n_rows[x.s] : a.T;
         x.len = kv4_len(a.cache_len, x.s, 0, a.cap, status);
         if (x.len < 0) continue;
-        const int n = a.n_rows ? a.n_rows[x.s] : a.T;
-        if (n < 0 || n > a.T || n > x.len || (a.src_slot && n > a.max_src + 1)) {
+        x.base = x.len - n;
+        // rows that the sequence, the tree and the list have, and nodes that the tree has
+        bool fits = n >= 0 && n <= a.T && n <= x.len && (!a.src_slot || n <= a.max_src + 1);
+        if (fits && a.src_slot)
+          for (int r = lane; r < n - 1 && fits; r += 32) {
+            if (r >= 32) mine = src[r];
+            fits = (uint32_t)mine - (uint32_t)x.base < (uint32_t)a.T;
+          }
+        if (!__all_sync(0xffffffffu, fits)) {
           if (lane == 0) set_status(status, DF_ERR_ARG, x.s);
           continue;
         }
-        x.base = x.len - n;
         x.total = n * p.G;
       }
       const size_t row = ((size_t)x.s * a.Hkv + x.kvh) * a.cap + x.key0;
@@ -238,13 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_weights_kernel(const __grid_c
       for (int r = threadIdx.x >> 2; r < cols; r += kExpWarps * 8) {
         const int q4 = lane & 3, rr = x.r0 + r, row = rr / p.G;
         int node = -1;
-        if (rr < x.total) {
-          node = !a.src_slot ? row : row == 0 ? 0 : a.src_slot[(size_t)x.s * a.max_src + row - 1] - x.base;
-          if (node < 0 || node >= a.T) {
-            set_status(status, DF_ERR_ARG, x.s);
-            node = -1;
-          }
-        }
+        if (rr < x.total) node = !a.src_slot ? row : row == 0 ? 0 : a.src_slot[(size_t)x.s * a.max_src + row - 1] - x.base;
         const size_t grow = ((size_t)x.s * a.T + max(node, 0)) * a.Hq + x.kvh * p.G + rr - row * p.G;
         uint32_t f[8][2];
         float back;

@@ -802,3 +802,34 @@ def test_weights_that_are_held_give_up(b, T, Hq, Hkv, lens):
         ws.configure()
         again = call()
         assert again[1] == 0 and torch.equal(again[0], good[0])
+
+
+@pytest.mark.parametrize("b,T,n,at,bad", [
+    (3, 3, 2, 0, 3),                       # a list of one entry: behind the tree, before it, far off on either side
+    (3, 3, 2, 0, -1),
+    (2, 40, 9, 7, 40),
+    (2, 40, 9, 0, 2 ** 31 - 1),
+    (2, 40, 9, 4, -2 ** 31),
+    (2, 90, 70, 33, -1),                   # beyond the first lanes, rows of several passes
+    (2, 90, 70, 68, 90),
+])
+def test_weights_leave_a_sequence_with_a_bad_list_out(b, T, n, at, bad):
+    # its scores stay as they were, decay or not, in place or not; the other sequences' votes are right
+    lens = [300 + 7 * s for s in range(b)]
+    c, k, v = filled(32, 1, b, 2, 400, lens)
+    q = bf16(synth.normal(32, "q", (b, T, 8, 128)))
+    paths = [list(range(n))] * b
+    lse = path_lse(k, q, lens, paths, SCALE)
+    src = np.array([[lens[s] - n + j for j in range(1, n)] for s in range(b)])
+    src[0, at] = np.clip(lens[0] - n + bad, -2 ** 31, 2 ** 31 - 1)
+    score = torch.rand(c.rows, device=DEV)
+    before, out = score.clone(), torch.full_like(score, 5.0)
+    kw = dict(n_rows=[n] * b, src=src, decay=0.5)
+    assert run_weights(c, 0, q, lse, lens, score, score_out=out, **kw) == -1
+    assert torch.equal(score, before) and (out[0, 0] == 5).all()
+    assert run_weights(c, 0, q, lse, lens, score, **kw) == -1
+    assert torch.equal(score[0, 0], before[0, 0])
+    for s in range(1, b):
+        assert torch.equal(score[0, s, :, :lens[s]], out[0, s, :, :lens[s]])
+    check_votes(np64(score)[0][1:], [kv4.weights(np64(q)[s], np64(lse)[s], k[0, s].transpose(1, 0, 2), SCALE, np64(before)[0, s], lens[s],
+                                                 paths[s], 0.5) for s in range(1, b)], q[1:], k[:, 1:], lens[1:], paths[1:])
