@@ -53,10 +53,11 @@ DF_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
 
 // The power of two that brings a row whose largest magnitude is `amax` to [2^12, 2^13): the
 // bf16 row times it is an fp16 row, exactly, but for what lies 2^26 below the largest.
-// `back` is its inverse.  amax = 0 (or no finite number): powers inside the normal range.
+// `back` is its inverse.  Both stay normal numbers: a row below 2^-114 stays smaller, and one
+// without a finite largest takes the powers of the largest numbers.
 DF_DEV float f16_row_factor(float amax, float& back) {
   int e = (int)(__float_as_uint(amax) >> 23);   // biased exponent; amax >= 0
-  e = min(max(e, 13), 240);
+  e = min(max(e, 13), 254);
   back = __uint_as_float((uint32_t)(e - 12) << 23);
   return __uint_as_float((uint32_t)(254 - e + 12) << 23);
 }

@@ -833,3 +833,28 @@ def test_weights_leave_a_sequence_with_a_bad_list_out(b, T, n, at, bad):
         assert torch.equal(score[0, s, :, :lens[s]], out[0, s, :, :lens[s]])
     check_votes(np64(score)[0][1:], [kv4.weights(np64(q)[s], np64(lse)[s], k[0, s].transpose(1, 0, 2), SCALE, np64(before)[0, s], lens[s],
                                                  paths[s], 0.5) for s in range(1, b)], q[1:], k[:, 1:], lens[1:], paths[1:])
+
+
+@pytest.mark.parametrize("size", [2.0 ** 112, 2.0 ** 116, 2.0 ** 119, 2.0 ** 124])
+@pytest.mark.parametrize("T", [1, 4, 40])
+def test_attention_and_weights_of_the_largest_queries(T, size):
+    # a bf16 row up to the type's largest, under a scale that makes ordinary scores of it
+    c, k, v = filled(33, 1, 1, 2, 200, [130 + T])
+    q = bf16(synth.normal(33, "q", (1, T, 8, 128)).clip(-7.9, 7.9) * size)
+    assert torch.isfinite(q).all()
+    scale, kk, vv = 0.1 / size, k[0, 0].transpose(1, 0, 2), v[0, 0].transpose(1, 0, 2)
+    out, lse = torch.zeros_like(q), torch.zeros(1, T, 8, device=DEV)
+    ws = ws_of(_lib.kv4_attention_workspace_size(c, T, 8))
+    if scale < 2.0 ** -126:      # not a normal number, and refused: the smallest power of two that is taken with room
+        with pytest.raises(_lib.StatusError):
+            _lib.kv4_attention(c, 0, q, i32([130]), None, scale, out, ws, lse=lse)
+        scale = 2.0 ** -125
+    _lib.kv4_attention(c, 0, q, i32([130]), None, scale, out, ws, lse=lse)
+    torch.cuda.synchronize()
+    assert ws.status() == 0
+    sets = {i: list(range(130 + i + 1)) for i in {0, T // 2, T - 1}}
+    check_attention(np64(out)[0], np64(lse)[0], np64(q)[0], kk, vv, sets, sorted(sets), scale)
+    lens, paths = [130 + T], [list(range(T))]
+    got, want, st = vote(c, k, q, path_lse(k, q, lens, paths, scale), lens, paths, scale)
+    assert st == 0
+    check_votes(got, want, q, k, lens, paths, scale)
