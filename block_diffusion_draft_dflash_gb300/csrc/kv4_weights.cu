@@ -249,22 +249,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_weights_kernel(const __grid_c
         int node = -1;
         if (rr < x.total) node = !a.src_slot ? row : row == 0 ? 0 : a.src_slot[(size_t)x.s * a.max_src + row - 1] - x.base;
         const size_t grow = ((size_t)x.s * a.T + max(node, 0)) * a.Hq + x.kvh * p.G + rr - row * p.G;
+        const float lse = node >= 0 ? a.lse[grow] : -INFINITY;
         uint32_t f[8][2];
         float back;
         load_q(a.q + grow * 128, node >= 0, q4, f, back);
+        // a NaN belongs to the slots that the row sees: it goes in as the row's numbers, which the mask covers
+        if (lse != lse)
+#pragma unroll
+          for (int c = 0; c < 8; ++c) f[c][0] = f[c][1] = 0x7FFF7FFFu;
         unsigned char* to = q_smem + (q4 >> 1) * kQSlab + r * 128;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           *reinterpret_cast<uint4*>(to + ((((q4 & 1) * 4 + c) ^ (r & 7)) * 16)) =
               make_uint4(f[2 * c][0], f[2 * c][1], f[2 * c + 1][0], f[2 * c + 1][1]);
         if (q4 == 0) {
-          float nl = -INFINITY;   // such a row adds 2^(-inf) = 0 everywhere
-          if (node >= 0) {
-            const float v = a.lse[grow];
-            if (v != -INFINITY) nl = v * -1.4426950408889634f;
-          }
           row_s[r] = fmaxf(p.scale2 * back, 1.17549435e-38f);   // a masked score times it stays -inf; a real one is as good as 0
-          row_nl[r] = nl;
+          // a row that saw nothing adds 2^(-inf) = 0 everywhere; finite above, for a masked score to stay -inf
+          row_nl[r] = lse == -INFINITY ? -INFINITY : fminf(lse * -1.4426950408889634f, 3.402823466e38f);
         }
       }
       fence_proxy_async();

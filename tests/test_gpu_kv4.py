@@ -858,3 +858,27 @@ def test_attention_and_weights_of_the_largest_queries(T, size):
     got, want, st = vote(c, k, q, path_lse(k, q, lens, paths, scale), lens, paths, scale)
     assert st == 0
     check_votes(got, want, q, k, lens, paths, scale)
+
+
+@pytest.mark.parametrize("what", ["lse", "q", "both", "low"])
+def test_weights_keep_a_nan_to_the_slots_that_its_row_sees(what):
+    # row 2 of 5 has a NaN (or a log-sum that no score is as low as): the path's slots behind its own stay numbers
+    lens, T = [140, 40], 5
+    c, k, v = filled(34, 1, 2, 2, 200, lens)
+    q = bf16(synth.normal(34, "q", (2, T, 8, 128)))
+    paths = [list(range(T))] * 2
+    lse = path_lse(k, q, lens, paths, SCALE)
+    if what in ("lse", "both"):
+        lse[0, 2, 5] = torch.nan
+    if what in ("q", "both"):
+        q[0, 2, 5, 77] = torch.nan
+    if what == "low":
+        lse[0, 2, 5] = -3e38
+    with np.errstate(over="ignore", invalid="ignore"):
+        got, want, st = vote(c, k, q, lse, lens, paths)
+    assert st == 0
+    n, bad = lens[0] - T + 3, (np.isinf if what == "low" else np.isnan)      # head 5 belongs to kv head 1
+    assert bad(got[0][1, :n]).all() and bad(want[0][1, :n]).all()
+    rows = bf16(np.nan_to_num(np64(q)))
+    got[0][1, :n], want[0][1, :n] = 0, 0
+    check_votes(got, want, rows, k, lens, paths)
