@@ -295,8 +295,8 @@ DF_DEV void load_q(const df_bf16* src, bool on, int t4, uint32_t (&f)[8][2], flo
 constexpr float kTcShift = 7.f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// ln of the softmax's sum from a maximum and a sum in log2 units.
-DF_DEV float kv4_lse(float m, float l, float shift) { return l > 0.f ? (m - shift + log2f(l)) * kLn2 : -INFINITY; }
+// ln of the softmax's sum from a maximum and a sum in log2 units; a sum of NaN gives NaN.
+DF_DEV float kv4_lse(float m, float l, float shift) { return l == 0.f ? -INFINITY : (m - shift + log2f(l)) * kLn2; }
 
 int launch_kv4_attn_few(Kv4AttnParams p, cudaStream_t st);    // kv4_attention.cu: mma.sync, few rows
 int launch_kv4_attn_tc(Kv4AttnParams p, cudaStream_t st);     // kv4_attention_tc.cu: tcgen05, tiles of 128 rows

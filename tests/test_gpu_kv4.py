@@ -882,3 +882,20 @@ def test_weights_keep_a_nan_to_the_slots_that_its_row_sees(what):
     rows = bf16(np.nan_to_num(np64(q)))
     got[0][1, :n], want[0][1, :n] = 0, 0
     check_votes(got, want, rows, k, lens, paths)
+
+
+@pytest.mark.parametrize("T,N", [(1, 50), (1, 9000), (4, 900), (40, 3000), (200, 700), (300, 0)])
+def test_attention_of_a_row_with_a_nan(T, N):
+    # its output and log-sum are NaN, not those of a row that sees nothing; the other heads and rows are right
+    c, k, v = filled(35, 1, 1, 2, (N + T + 7) // 8 * 8, [N + T])
+    q = bf16(synth.normal(35, "q", (1, T, 8, 128)))
+    clean = q.clone()
+    q[0, T - 1, 3, 100] = torch.nan
+    out, lse, st = run_attention(c, 0, q, [N], None)
+    assert st == 0
+    assert torch.isnan(out[0, T - 1, 3]).all() and torch.isnan(lse[0, T - 1, 3])
+    want, want_lse, _ = run_attention(c, 0, clean, [N], None)
+    out[0, T - 1, 3], lse[0, T - 1, 3] = want[0, T - 1, 3], want_lse[0, T - 1, 3]
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    sets = {i: list(range(N + i + 1)) for i in {0, T - 1}}
+    check_attention(np64(out)[0], np64(lse)[0], np64(clean)[0], k[0, 0].transpose(1, 0, 2), v[0, 0].transpose(1, 0, 2), sets, sorted(sets))
