@@ -457,10 +457,12 @@ def kv4_attention_weights(cache: Kv4Cache, layer, q, lse, cache_len, scale, scor
         raise ValueError(f"q must be [{cache.b}][T][Hq][128]")
     max_src = 0 if src_slot is None else src_slot.shape[1]
     sc = arg(score, f32, cache.rows, "score")
+    length, src = arg(cache_len, i32, (b,), "cache_len"), arg(src_slot, i32, (b, max_src), "src_slot")
+    if src_slot is not None and max_src == 0:
+        src = length        # lists without entries: not the NULL that an empty tensor's address is; never read
     _check("dflash_kv4_attention_weights", load().dflash_kv4_attention_weights(
         cache.ref, layer, T, Hq, arg(q, torch.bfloat16, shape, "q"), arg(lse, f32, shape[:3], "lse"),
-        arg(cache_len, i32, (b,), "cache_len"), arg(n_rows, i32, (b,), "n_rows"),
-        arg(src_slot, i32, (b, max_src), "src_slot"), max_src, scale, decay, sc,
+        length, arg(n_rows, i32, (b,), "n_rows"), src, max_src, scale, decay, sc,
         sc if score_out is None else arg(score_out, f32, cache.rows, "score_out"), *cache._ws(ws)))
 
 

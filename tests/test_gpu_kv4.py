@@ -899,3 +899,20 @@ def test_attention_of_a_row_with_a_nan(T, N):
     assert torch.equal(out, want) and torch.equal(lse, want_lse)
     sets = {i: list(range(N + i + 1)) for i in {0, T - 1}}
     check_attention(np64(out)[0], np64(lse)[0], np64(clean)[0], k[0, 0].transpose(1, 0, 2), v[0, 0].transpose(1, 0, 2), sets, sorted(sets))
+
+
+def test_weights_with_lists_without_entries():
+    # the root alone may vote: more rows do not fit such a list, and they are not the rows of a chain
+    lens = [60, 20]
+    c, k, v = filled(36, 1, 2, 2, 64, lens)
+    q = bf16(synth.normal(36, "q", (2, 3, 4, 128)))
+    lse = path_lse(k, q, lens, [[0, 1], [0]], SCALE)
+    score = torch.rand(c.rows, device=DEV)
+    before = score.clone()
+    empty = torch.zeros(2, 0, dtype=torch.int32, device=DEV)
+    ws = ws_of(_lib.kv4_attention_weights_workspace_size(c, 3, 4))
+    _lib.kv4_attention_weights(c, 0, q, lse, i32(lens), SCALE, score, ws, n_rows=i32([2, 1]), src_slot=empty)
+    torch.cuda.synchronize()
+    assert ws.status() == -1 and torch.equal(score[0, 0], before[0, 0])
+    want = kv4.weights(np64(q)[1], np64(lse)[1], k[0, 1].transpose(1, 0, 2), SCALE, np64(before)[0, 1], 20, [0])
+    check_votes(np64(score)[0][1:], [want], q[1:], k[:, 1:], [20], [[0]])
