@@ -163,8 +163,8 @@ int launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t st) {
 }
 
 // 16 bytes of a row's 64 codes.  Rows are picked here and there: without the hint L2 fetches the
-// neighbouring row with each (half of 36 x 8 x 8449 rows kept: 277 MB read instead of 204, 62 us
-// instead of 58).
+// neighbouring row with each (half of 36 x 8 x 8449 rows kept: 277 MB read instead of 204, 65 us
+// instead of 54).
 DF_DEV uint4 load_picked(const uint8_t* p) {
   uint4 r;
   asm volatile("ld.global.L2::64B.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");

@@ -1,4 +1,5 @@
-// Launch arguments of the kernels of the 4-bit KV cache (kv4.cu, kv4_attention.cu).
+// Launch arguments of the kernels of the 4-bit KV cache (kv4.cu, kv4_attention.cu,
+// kv4_attention_tc.cu, kv4_weights.cu).
 #pragma once
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -7,7 +7,7 @@
 //
 // What bounds it with few rows is the cache, 144 bytes a slot and kv head, and then the
 // instructions that decode it: one token of 16 sequences of 9803 to 32768 slots, 8 kv heads (393
-// MB), takes 81 us, 4.9 TB/s, with an instruction issued in 65 % of the schedulers' cycles; 8 rows
+// MB), takes 81 us, 4.8 TB/s, with an instruction issued in 65 % of the schedulers' cycles; 8 rows
 // of one sequence of 2000 slots take 8 us, which is latency.  Every warp streams stages of 32 slots
 // (bulk copies into a ring of its own, no CTA barrier), decodes codes straight into tensor-core
 // fragments and keeps its own running maximum, sum and output; the warps are merged when the CTA's
@@ -30,8 +30,9 @@ constexpr int kStageKeys = 32;   // launch: stage_log2
 constexpr int kStages = 2;
 constexpr int kStageBytes = kStageKeys * 2 * (kKv4Codes + kKv4Scales);   // K codes, V codes, K scales, V scales
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-// Probabilities are scaled by 2^12 before they are rounded to fp16: what lies 2^26 below the
-// row's largest still has all its bits.
+// Probabilities are scaled by 2^12 before they are rounded to fp16 (the tensor cores' operand; 11
+// significant bits, more than the bf16 output has; their sum is taken before): what lies 2^26 below
+// the row's largest still has all its bits.
 constexpr float kPShift = 12.f;
 
 // 8 x 8 fp16 transposition: lane (g, t) has row g, columns 2t, 2t+1, before and after.

@@ -14,7 +14,9 @@
 //
 // Per block:  S in fp32 (fp16 operands: the cache's values are fp16 numbers, kv4.cuh, so the
 // products are exact), softmax with a running maximum that moves only when a block raises it
-// by more than 2^8, P as fp16 over its own S, O += P V.  One thread owns one row of a stream and
+// by more than 2^8, P as fp16 over its own S, O += P V.  P is an operand of the tensor cores, so it
+// has 16 bits: fp16 keeps 11 significant ones where bf16 would keep 8, more than the output has, and
+// sums of P are taken before the rounding.  One thread owns one row of a stream and
 // holds its 128 scores in registers (given to it by the decoding warps): S is read once, and
 // no exchange between threads is needed.
 //
@@ -22,7 +24,7 @@
 // cycles, the exponentials 1400 (both streams share the special function units and the issue
 // slots with the decoding warps), 300 until the issuer has seen P, 1500 for PV and the next S
 // beside the other stream's, 250 until S is seen: 4200, of which the tensor cores work 2050.
-// Trees of 257 nodes over 2 sequences of 7192 and 8192 slots, 32 heads on 8: 91 us (65 GFLOP).
+// Trees of 257 nodes over 2 sequences of 7192 and 8192 slots, 32 heads on 8: 92 us (65 GFLOP).
 //
 // Warp roles: 4 softmax / epilogue warps and an MMA issuer for each stream, 8 decoding warps and
 // one warp that brings the codes.  Codes arrive by untiled bulk copies (a block's rows are
@@ -111,7 +113,9 @@ DF_DEV void scale_rows(uint32_t oaddr, float alpha) {
   }
 }
 
-// Cycles that stream 1 waits before its first product (trees of 257: 91.4 us, 92.8 us without).
+// Cycles that stream 1 waits before its first product.  Chains gain as trees do once a unit has
+// several stages: 2 x 257 nodes over 8000 slots 89.9 us (90.2 without), 16 x 16 nodes 80.6 (81.1),
+// 4 x 32 nodes 31.5 (32.0); a unit of one stage only waits: 16 nodes over 200 slots 13.0 us (12.3).
 constexpr int kStagger = 1500;
 DF_DEV void pause(int cycles) {
   const long long t0 = clock64();

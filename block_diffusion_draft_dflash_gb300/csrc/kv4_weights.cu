@@ -6,7 +6,7 @@
 // along its own columns: no exchange, no atomics, and the order of every sum is fixed.
 //
 // What bounds it is the decoding (1000 cycles for a block) beside the exponentials, which share
-// the issue slots: 64 rows of each of 8 sequences of 8607 to 16384 slots, 8 kv heads, take 37 us
+// the issue slots: 64 rows of each of 8 sequences of 8607 to 16384 slots, 8 kv heads, take 36 us
 // (with mma.sync and no tile of decoded keys 47 us); 36 rows over 4105 slots take 7 us, latency.
 //
 // Warp roles: one warp brings codes (untiled bulk copies), 8 warps decode them into 128-byte-

@@ -394,10 +394,10 @@ int dflash_kv4_append(const df_kv4_cache* cache, int layer, const df_bf16* k, co
  *              cap <= 2^20
  *   cache_len  [b] int32, N + n_tree <= cap
  *   anc        [b][n_tree][ceil(n_tree/32)] uint32, or NULL: a chain, row i sees tree slots 0 .. i
- *   scale      > 0 and finite
+ *   scale      > 0; scale log2(e) and that times 2^k_exp are normal fp32 numbers
  *   out        [b][n_tree][Hq][hd] bf16; 0 for a row that sees nothing
  *   lse        [b][n_tree][Hq] fp32 out, log of the sum of exp(scale q.k); -inf for a row that
- *              sees nothing; may be NULL */
+ *              sees nothing, NaN for one with a NaN; may be NULL */
 size_t dflash_kv4_attention_workspace_size(const df_kv4_cache* cache, int n_tree, int Hq);
 int dflash_kv4_attention(const df_kv4_cache* cache, int layer, int n_tree, int Hq, const df_bf16* q,
                          const int32_t* cache_len, const uint32_t* anc, float scale, df_bf16* out, float* lse,
@@ -415,8 +415,9 @@ int dflash_kv4_attention(const df_kv4_cache* cache, int layer, int n_tree, int H
  *   q, lse     [b][n_tree][Hq][hd] bf16, [b][n_tree][Hq] fp32: of dflash_kv4_attention;
  *              cap <= 2^20
  *   n_rows     [b] int32, 0 <= n_rows <= min(n_tree, cache_len), or NULL: n_tree
- *   src_slot   [b][max_src] int32: row 0 is node 0, row j node src_slot[s][j-1] - N
- *              (n_rows <= max_src + 1); or NULL: row j is node j
+ *   src_slot   [b][max_src] int32: row 0 is node 0, row j node src_slot[s][j-1] - N, each a
+ *              node of the tree (n_rows <= max_src + 1); or NULL: row j is node j
+ *   scale      as there
  *   decay      0 .. 1
  *   score, score_out  [n_layers][b][Hkv][cap] fp32 (the call's layer is used); may be the same */
 size_t dflash_kv4_attention_weights_workspace_size(const df_kv4_cache* cache, int n_tree, int Hq);
@@ -444,6 +445,12 @@ int dflash_kv4_compact(const df_kv4_cache* cache, const int32_t* src_slot, int m
  * (the lower slot first among equal scores; a NaN below everything).  Rows and scores that
  * stay go to another cache in the order of their slots, so slots stay in order of age; a
  * sequence with at most `budget` slots is copied whole.
+ *
+ * A slot of the new cache is no longer a token's position, and new_len is not the next one.
+ * A caller that evicts keeps each sequence's position in a counter of its own: the rotation of
+ * new queries and keys goes by that, and so do a temperature draw's numbers (keyed to the drawn
+ * token's position) and the drafter's ctx_len; the calls over the 4-bit cache go by cache_len.
+ * Keys keep the rotation with which they were appended.
  *   score      [n_layers][b][Hkv][cap] fp32
  *   cache_len  [b] int32
  *   budget     >= 1, <= to->cap;  n_sink, n_recent >= 0, n_sink + n_recent <= budget
