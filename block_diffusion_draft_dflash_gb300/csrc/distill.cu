@@ -1,0 +1,374 @@
+// Distillation from a teacher's top logits: loss of student rows and its gradient.
+//
+// With e_j = exp((z_j - m) / T), m the row's largest logit, S = sum of e_j over all tokens and R
+// over those outside the teacher's list (t_i, rho):
+//   loss / weight = sum_i t_i (ln t_i - (z_i - m) / T) + sum t ln S + rho (ln rho - ln(R / S))
+//   gradient = weight / T (e_j / S - t_j) in the list, weight / T e_j (1 / S - rho / R) outside
+// R is summed over the tokens outside (a bit for each token marks the list), not taken as S minus
+// the list's part: where the student is sure of the list, that difference has no digits left.
+// Both passes are bound by the row's bytes: loss reads a row once; with the gradient a row is read
+// again from L2 by the CTAs that just read it, and written.
+#include "rows.cuh"
+#include "runtime.h"
+#include "trace.h"
+
+namespace df {
+namespace {
+
+constexpr int kMaxList = 1024;
+constexpr int kPer = kMaxList / kRowThreads;   // entries of a thread
+
+struct Post {            // what a CTA tells the others of its part of a row
+  float largest, rest, listed;   // sums of e_j relative to `largest`
+  float cross, t;                // sum of t_i (ln t_i - (z_i - largest) / T), and of t_i
+  uint32_t bad;                  // 1: NaN or +inf, 2: a bad list
+};
+struct Shared {
+  float post[8][8];      // Post of every CTA of the row
+  float tmp[kRowWarps];
+  uint32_t flags;
+};
+
+// 1 / T in two floats, and log2(e) / T.
+struct Temper {
+  float hi, lo, c;
+  DF_DEV explicit Temper(float T) {
+    hi = 1.f / T;
+    lo = fmaf(-hi, T, 1.f) / T;
+    c = 1.44269504f * hi;
+  }
+  DF_DEV float over(float x) const { return fmaf(x, hi, x * lo); }              // x / T
+  DF_DEV float over(float x, float minus) const { return fmaf(x, hi, -minus) + x * lo; }   // x / T - minus
+};
+
+// A thread's entries of a teacher's list: entry tid + 512 j.
+struct Entries {
+  int id[kPer];
+  float ln_t[kPer], t[kPer];
+  float sum;             // of all t of the list
+  uint32_t bad;          // of this thread's entries
+
+  DF_DEV void load(const DistillArgs& a, const Temper& T, int list, float* tmp) {
+    const int V = a.x.V;
+    float lse = 0.f;
+    bad = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = (int)threadIdx.x + j * kRowThreads;
+      id[j] = i < a.K ? a.id[(size_t)list * a.K + i] : -1;
+      float v = -INFINITY;
+      if (id[j] < -1 || id[j] >= V) {
+        bad |= 2;
+        id[j] = -1;
+      } else if (id[j] >= 0) {
+        v = a.val[(size_t)list * a.K + i];
+        if (!(v < INFINITY)) bad |= 1;
+      }
+      ln_t[j] = v;
+    }
+    if (a.lse) {
+      lse = a.lse[list];
+      if (!(fabsf(lse) < INFINITY)) bad |= 1;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) ln_t[j] = ln_t[j] > -INFINITY ? T.over(ln_t[j], lse) : -INFINITY;
+    } else {
+      // softmax over the list
+      float m = ln_t[0];
+#pragma unroll
+      for (int j = 1; j < kPer; ++j) m = max_nan(m, ln_t[j]);
+      m = warp_max(m);
+      __syncthreads();
+      if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = m;
+      __syncthreads();
+      m = warp_max(tmp[threadIdx.x & (kRowWarps - 1)]);
+      if (!(m > -INFINITY)) bad |= 1;
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        ln_t[j] = ln_t[j] > -INFINITY ? T.over(ln_t[j] - m) : -INFINITY;
+        s += expf(ln_t[j]);
+      }
+      const float ln_s = logf(block_add(s, tmp));
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) ln_t[j] -= ln_s;
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      t[j] = expf(ln_t[j]);
+      s += t[j];
+    }
+    sum = block_add(s, tmp);
+  }
+};
+
+// The list of row r; -1: it does not learn, -2: outside the lists.
+DF_DEV int list_of(const DistillArgs& a, int r) {
+  if (a.weight && a.weight[r] == 0.f) return -1;
+  const int list = a.teacher_row ? a.teacher_row[r] : r;
+  return list < -1 || list >= a.n_teacher ? -2 : list;
+}
+
+// Writes f(x, piece) (VE values) for this CTA's pieces of the gradient's row; U loads ahead.
+// `aligned`: the gradient's pieces start at 16-byte addresses like the student's.
+template <int U, bool READ, class E, class F>
+DF_DEV void write_pieces(const RowPart<E>& p, E* grad, F&& f) {
+  constexpr int VE = RowPart<E>::VE;
+  const bool aligned = (reinterpret_cast<uintptr_t>(grad - p.head) & 15) == 0;
+  uint4* out = reinterpret_cast<uint4*>(grad - p.head);
+  for (int i = p.lo + (int)threadIdx.x; i < p.hi; i += U * kRowThreads) {
+    uint4 v[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      v[j] = RowPart<E>::nothing();
+      if (READ && i + j * kRowThreads < p.hi) v[j] = p.load(i + j * kRowThreads);
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int piece = i + j * kRowThreads;
+      if (piece >= p.hi) break;
+      float x[VE];
+      RowOf<E>::unpack(v[j], x);
+      f(x);
+      if (aligned && p.whole(piece)) {
+        out[piece] = RowOf<E>::pack(x);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          const int k = p.id(piece, e);
+          if ((unsigned)k < (unsigned)p.V) RowOf<E>::set(grad, k, x[e]);
+        }
+      }
+    }
+  }
+}
+template <class E>
+DF_DEV void write_zeros(const RowPart<E>& p, E* grad) {
+  write_pieces<4, false>(p, grad, [](float* x) {
+#pragma unroll
+    for (int e = 0; e < RowPart<E>::VE; ++e) x[e] = 0.f;
+  });
+}
+
+// Gradient of a row's part: the formula of the tokens outside the list for every element, then
+// the list's own over it.  z: the student's logits at the thread's entries, where they lie in the part.
+template <class E>
+DF_DEV void write_gradient(const RowPart<E>& p, E* grad, const Entries& en, const float* z, const bool* mine, float m,
+                           float c, float scale, float inv_s, float rho_over_r) {
+  const float out = fminf(fmaxf(scale * (inv_s - rho_over_r), -3.4e38f), 3.4e38f);
+  write_pieces<4, true>(p, grad, [&](float* x) {
+#pragma unroll
+    for (int e = 0; e < RowPart<E>::VE; ++e) x[e] = ex2_approx((x[e] - m) * c) * out;
+  });
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+    if (mine[j]) RowOf<E>::set(grad, en.id[j], scale * (ex2_approx((z[j] - m) * c) * inv_s - en.t[j]));
+}
+
+// grid: rows x CTAs of a row.
+template <class E>
+__global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a, int ctas) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  Shared& s = *reinterpret_cast<Shared*>(smem);
+  uint32_t* bits = reinterpret_cast<uint32_t*>(smem + sizeof(Shared));   // one for each element of the part
+  constexpr int VE = RowPart<E>::VE;
+  pdl_wait();
+  pdl_trigger();
+  const int rank = ctas == 1 ? 0 : (int)cluster_rank(), tid = threadIdx.x;
+  const int r = blockIdx.x / ctas;
+  const RowPart<E> part(static_cast<const E*>(a.x.data), a.x.ld, r, a.x.V, rank, ctas);
+  E* grad = a.grad ? static_cast<E*>(a.grad) + r * a.ld_grad : nullptr;
+  const int list = list_of(a, r);
+  auto give = [&](float loss, float s0, float s1, float s2) {
+    a.loss[r] = loss;
+    reinterpret_cast<float4*>(a.stats)[r] = make_float4(s0, s1, s2, loss == loss || s0 == s0 ? 0.f : NAN);
+  };
+  if (list < 0) {
+    if (grad) write_zeros(part, grad);
+    if (rank == 0 && tid == 0) {
+      if (list == -1) {
+        give(0.f, 0.f, 0.f, 0.f);
+      } else {
+        set_status(a.status, DF_ERR_ARG, r);
+        give(NAN, NAN, NAN, NAN);
+      }
+    }
+    return;
+  }
+  const Temper T(a.temperature);
+  const int n_words = ((part.hi - part.lo) * VE + 31) / 32;
+  for (int i = tid; i < n_words; i += kRowThreads) bits[i] = 0;
+  if (tid == 0) s.flags = 0;
+  if (ctas > 1) row_sync(ctas);     // every CTA of the cluster runs
+  Entries en;
+  en.load(a, T, list, s.tmp);       // with barriers behind the zeros
+  float z[kPer];
+  bool mine[kPer];
+  const int bit0 = part.lo * VE - part.head;   // element of bit 0
+  uint32_t bad = en.bad;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int b = en.id[j] - bit0;
+    mine[j] = en.id[j] >= 0 && b >= 0 && b < (part.hi - part.lo) * VE;
+    z[j] = mine[j] ? RowOf<E>::value(part.row, en.id[j]) : -INFINITY;
+    if (mine[j] && (atomicOr(&bits[b >> 5], 1u << (b & 31)) >> (b & 31) & 1)) bad |= 2;
+  }
+  if (bad) atomicOr(&s.flags, bad);
+  __syncthreads();
+  // largest logit and the sum outside the list, a thread's own
+  float m = -INFINITY, rest = 0.f, check = -INFINITY;
+  const uint8_t* marks = reinterpret_cast<const uint8_t*>(bits);
+  for (int i = part.lo + tid; i < part.hi; i += 4 * kRowThreads) {
+    uint4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] = i + j * kRowThreads < part.hi ? part.load(i + j * kRowThreads) : RowPart<E>::nothing();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int piece = i + j * kRowThreads;
+      const float big = RowOf<E>::largest(v[j]);
+      check = max_nan(check, big);
+      if (!(big > -INFINITY)) continue;
+      if (big > m) {
+        rest *= ex2_approx((m - big) * T.c);
+        m = big;
+      }
+      float x[VE];
+      RowOf<E>::unpack(v[j], x);
+      uint32_t listed = 0;
+      if (piece < part.hi) {
+        const int q = piece - part.lo;
+        listed = VE == 8 ? marks[q] : (marks[q >> 1] >> ((q & 1) * 4)) & 15u;
+      }
+      if (listed == 0) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) rest += ex2_approx((x[e] - m) * T.c);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VE; ++e)
+          if (!(listed >> e & 1)) rest += ex2_approx((x[e] - m) * T.c);
+      }
+    }
+  }
+  // the CTA's part
+  float big = warp_max(m);
+  __syncthreads();
+  if ((tid & 31) == 0) s.tmp[tid >> 5] = big;
+  if (!(check < INFINITY)) atomicOr(&s.flags, 1u);
+  __syncthreads();
+  big = warp_max(s.tmp[tid & (kRowWarps - 1)]);
+  rest = block_add(m > -INFINITY ? rest * ex2_approx((m - big) * T.c) : 0.f, s.tmp);
+  float in = 0.f, cross = 0.f, tsum = 0.f;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+    if (mine[j]) {
+      if (z[j] > -INFINITY) in += ex2_approx((z[j] - big) * T.c);
+      if (en.t[j] > 0.f) {
+        tsum += en.t[j];
+        cross += z[j] > -INFINITY ? en.t[j] * (en.ln_t[j] - T.over(z[j] - big)) : INFINITY;
+      }
+    }
+  in = block_add(in, s.tmp);
+  cross = block_add(cross, s.tmp);
+  tsum = block_add(tsum, s.tmp);
+  if (tid < ctas) {
+    const float w[6] = {big, rest, in, cross, tsum, __uint_as_float(s.flags)};
+    for (int i = 0; i < 6; ++i) st_remote(at_rank(&s.post[rank][i], tid), w[i]);
+  }
+  row_sync(ctas);
+  m = -INFINITY;
+  bad = 0;
+  for (int i = 0; i < ctas; ++i) {
+    m = fmaxf(m, s.post[i][0]);
+    bad |= __float_as_uint(s.post[i][5]);
+  }
+  if (!(m > -INFINITY)) bad |= 1;
+  if (bad) {
+    if (grad) write_zeros(part, grad);
+    if (rank == 0 && tid == 0) {
+      set_status(a.status, bad & 2 ? DF_ERR_ARG : DF_ERR_NAN, r);
+      give(NAN, NAN, NAN, NAN);
+    }
+    return;
+  }
+  float R = 0.f, S = 0.f;
+  cross = 0.f;
+  for (int i = 0; i < ctas; ++i) {
+    const float mi = s.post[i][0];
+    if (mi > -INFINITY) {
+      const float f = ex2_approx((mi - m) * T.c);
+      R += s.post[i][1] * f;
+      S += s.post[i][2] * f;
+      cross += s.post[i][3] + T.over(m - mi) * s.post[i][4];
+    } else {
+      cross += s.post[i][3];
+    }
+  }
+  S += R;
+  const float rho = a.lse ? fmaxf(1.f - en.sum, 0.f) : 0.f;
+  const float weight = a.weight ? a.weight[r] : 1.f;
+  if (rank == 0 && tid == 0) {
+    const float ln_s = logf(S), ln_r = logf(R);
+    const float kl = cross + en.sum * ln_s + (rho > 0.f ? rho * (logf(rho) - (ln_r - ln_s)) : 0.f);
+    give(weight * kl, m, ln_s, ln_r);
+  }
+  if (grad)
+    write_gradient(part, grad, en, z, mine, m, T.c, T.over(weight), 1.f / S, R > 0.f ? rho / R : 0.f);
+}
+
+// grid: rows x CTAs of a row; they do not depend on each other.
+template <class E>
+__global__ void __launch_bounds__(kRowThreads) distill_backward_kernel(DistillArgs a, int ctas) {
+  __shared__ float tmp[kRowWarps];
+  constexpr int VE = RowPart<E>::VE;
+  pdl_wait();
+  pdl_trigger();
+  const int rank = blockIdx.x % ctas, r = blockIdx.x / ctas;
+  const RowPart<E> part(static_cast<const E*>(a.x.data), a.x.ld, r, a.x.V, rank, ctas);
+  E* grad = static_cast<E*>(a.grad) + r * a.ld_grad;
+  const float4 st = reinterpret_cast<const float4*>(a.stats)[r];
+  const int list = list_of(a, r);
+  if (list == -2 && rank == 0 && threadIdx.x == 0) set_status(a.status, DF_ERR_ARG, r);
+  if (list < 0 || st.x != st.x) {
+    write_zeros(part, grad);
+    return;
+  }
+  const Temper T(a.temperature);
+  Entries en;
+  en.load(a, T, list, tmp);
+  float z[kPer];
+  bool mine[kPer];
+  const int bit0 = part.lo * VE - part.head;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int b = en.id[j] - bit0;
+    mine[j] = en.id[j] >= 0 && b >= 0 && b < (part.hi - part.lo) * VE;
+    z[j] = mine[j] ? RowOf<E>::value(part.row, en.id[j]) : 0.f;
+  }
+  __syncthreads();     // an entry's logit is read before it may be written over
+  const float rho = a.lse ? fmaxf(1.f - en.sum, 0.f) : 0.f;
+  const float scale = T.over((a.weight ? a.weight[r] : 1.f) * (a.grad_loss ? a.grad_loss[r] : 1.f));
+  write_gradient(part, grad, en, z, mine, st.x, T.c, scale, expf(-st.y), st.z > -INFINITY ? rho * expf(-st.z) : 0.f);
+}
+
+int done(cudaError_t e) { return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? DF_OK : DF_ERR_CUDA; }
+
+}  // namespace
+
+int launch_distill(const DistillArgs& a, cudaStream_t st) {
+  const int ctas = row_ctas(a.x.rows, a.x.V);
+  const auto f = a.x.dtype == DF_F32 ? distill_kernel<float> : distill_kernel<uint16_t>;
+  const size_t smem = sizeof(Shared) + ((size_t)(a.x.V + 16) / ctas + 64) / 8 + 16;
+  if (ensure_dynamic_smem(f, smem) != cudaSuccess) return DF_ERR_CUDA;
+  DF_TRACE("distill", st);
+  return done(launch_cluster(f, (unsigned)a.x.rows * ctas, ctas, smem, st, a, ctas));
+}
+int launch_distill_backward(const DistillArgs& a, cudaStream_t st) {
+  const int ctas = row_ctas(a.x.rows, a.x.V);
+  const auto f = a.x.dtype == DF_F32 ? distill_backward_kernel<float> : distill_backward_kernel<uint16_t>;
+  DF_TRACE("distill_backward", st);
+  return done(launch_k(f, dim3((unsigned)a.x.rows * ctas), dim3(kRowThreads), 0, st, a, ctas));
+}
+
+}  // namespace df

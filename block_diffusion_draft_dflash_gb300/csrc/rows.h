@@ -1,0 +1,52 @@
+// Launch arguments of the operators on rows of logits (sample.cu, distill.cu).
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/dflash.h"
+
+namespace df {
+
+struct SampleArgs {
+  df_rows x;
+  int group;                      // rows r of one setting: r / group
+  const float *temperature, *top_p, *min_p;   // [rows / group], each may be null
+  const int32_t* top_k;
+  const float* u;                 // [rows]
+  int32_t* token;                 // [rows]
+  float* logprob;                 // [rows], may be null
+  int32_t* n_kept;                // [rows], may be null
+  int* status;
+};
+int launch_sample(const SampleArgs& a, cudaStream_t st);
+
+struct TopArgs {
+  df_rows x;
+  int K;
+  float temperature;
+  int32_t* id;                    // [rows][K]
+  float *val, *lse;               // [rows][K]; [rows], may be null
+  int* status;
+};
+int launch_top_logits(const TopArgs& a, cudaStream_t st);
+
+struct DistillArgs {
+  df_rows x;                      // the student's logits
+  int K, n_teacher;
+  const int32_t* id;              // [n_teacher][K]
+  const float *val, *lse;         // [n_teacher][K]; [n_teacher] or null
+  const int32_t* teacher_row;     // [rows] or null
+  float temperature;
+  const float *weight, *grad_loss;  // [rows] or null
+  float *loss, *stats;            // [rows]; [rows][4]
+  void* grad;                     // [rows][ld_grad] in the type of x, may be null (backward: not)
+  long long ld_grad;
+  int* status;
+};
+int launch_distill(const DistillArgs& a, cudaStream_t st);
+int launch_distill_backward(const DistillArgs& a, cudaStream_t st);
+
+// CTAs that share a row of V logits, for this many rows: a power of two up to 8 (one cluster).
+int row_ctas(int rows, int V);
+
+}  // namespace df

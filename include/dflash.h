@@ -465,6 +465,102 @@ int dflash_kv4_evict(const df_kv4_cache* cache, const float* score, const int32_
                      void* ws, size_t ws_bytes, df_stream stream);
 
 /* ------------------------------------------------------------------------------------
+ * Rows of logits: draws under top-k, top-p and min-p, largest logits, distillation.
+ *
+ * [DFlash] and [DDTree] "실험 결과" evaluate at temperature 1.0; what is drawn from a target in
+ * serving is usually cut to its likely tokens as well.  [DFlash] "학습 방식도 추론 시나리오에 맞춰
+ * 바꿨다": the drafter learns from the target, early positions of a block counting more.
+ *
+ * A row's tokens stand in order: the larger logit first, the lower id first among equal ones
+ * (-0 and +0 are equal).  -inf masks a token.  A row with a NaN or +inf is recorded
+ * (DF_ERR_NAN) and left out as each call says.
+ * ------------------------------------------------------------------------------------ */
+enum { DF_F32 = 0, DF_BF16 = 1 };
+typedef struct {
+  const void* data;    /* row r starts at element r * ld; data is 16-byte aligned     */
+  int32_t dtype;       /* DF_F32 or DF_BF16                                           */
+  int32_t rows;        /* >= 0                                                        */
+  int32_t V;           /* 1 .. 2^20                                                   */
+  int64_t ld;          /* >= V, any (rows need not be aligned); ld * rows < 2^62      */
+} df_rows;
+
+/* dflash_sample -- a token of every row, drawn with the row's given random number.
+ *
+ * With w_v = exp((l_v - max) / T), of the tokens in order stay
+ *   top_k  the first top_k (<= 0: all),
+ *   top_p  those before which less than top_p times the mass of what top_k left lies (1: all),
+ *   min_p  those with w_v >= min_p (0: all);
+ * each of them keeps the first tokens of the order, and the fewest count.  The token is the
+ * first one in order at which the kept mass exceeds u times all of it.  temperature 0 (and any
+ * below 2^-126): the first token.  Masses are sums of whole numbers of 2^-42 made with a relative
+ * error near 2^-35, so the result does not depend on the order of summation.
+ *   group        row r takes setting r / group; rows is a multiple of it
+ *   temperature, top_k, top_p, min_p   [rows / group] each, or NULL: 1, 0, 1, 0.
+ *                0 <= temperature <= 2^100, 0 < top_p <= 1, 0 <= min_p <= 1
+ *   u            [rows] fp32, 0 <= u < 1
+ *   token        [rows] int32 out; -1 for a row whose tokens are all masked or that was left out
+ *                (a setting or u outside its range: DF_ERR_ARG, recorded)
+ *   logprob      [rows] fp32 out, ln(w_token / kept mass) (-inf with token -1); may be NULL
+ *   n_kept       [rows] int32 out, tokens that stayed (0 with token -1); may be NULL */
+size_t dflash_sample_workspace_size(int rows, int V);
+int dflash_sample(const df_rows* logits, int group, const float* temperature, const int32_t* top_k,
+                  const float* top_p, const float* min_p, const float* u, int32_t* token, float* logprob,
+                  int32_t* n_kept, void* ws, size_t ws_bytes, df_stream stream);
+
+/* dflash_top_logits -- the first K tokens of every row, and the row's log-sum: what a teacher
+ * hands to dflash_distill.
+ *   temperature  > 0, 2^-100 .. 2^100
+ *   id, val      [rows][K] int32, fp32 out, in order; -1 and -inf where a row has fewer tokens
+ *                above -inf.  1 <= K <= 1024
+ *   lse          [rows] fp32 out, ln of the sum of exp(l / temperature); may be NULL
+ * A row left out: ids -1, values -inf, lse NaN. */
+size_t dflash_top_logits_workspace_size(int rows, int V);
+int dflash_top_logits(const df_rows* logits, int K, float temperature, int32_t* id, float* val, float* lse,
+                      void* ws, size_t ws_bytes, df_stream stream);
+
+/* dflash_distill -- loss of student rows against a teacher's top logits, and its gradient.
+ *
+ * A teacher's list (id_i, val_i), i < K, stands for the probabilities t_i = exp(val_i / T - lse)
+ * and rho = max(0, 1 - sum t_i) for "any other token"; with lse NULL for t = softmax(val / T) over
+ * the list, rho = 0.  Against q = softmax(z / T) of the student's row and sigma, its mass
+ * outside the list:
+ *   loss = weight (sum_i t_i (ln t_i - ln q_i) + rho (ln rho - ln sigma))
+ *   dloss / dz_j = weight / T (q_j - t_j)              j in the list
+ *                  weight / T q_j (1 - rho / sigma)    others (lse NULL: weight / T q_j)
+ * Terms with t_i = 0 or rho = 0 are 0.  A student's -inf where the teacher has mass gives an
+ * infinite loss (its gradient stays finite; with sigma = 0 < rho there are no others).
+ *   student      the rows; T = temperature, 2^-100 .. 2^100
+ *   id, val      [n_teacher][K] int32, fp32; entries with id -1 are not there; 1 <= K <= 1024
+ *   lse          [n_teacher] fp32 or NULL
+ *   teacher_row  [rows] int32: the list of row r, -1: the row does not learn; or NULL: list r
+ *                (n_teacher >= rows)
+ *   weight       [rows] fp32 or NULL: 1; with weight 0 the row does not learn
+ *   loss         [rows] fp32 out
+ *   stats        [rows][4] fp32 out: the row's largest logit m, ln sum exp((z - m) / T) over all
+ *                tokens, the same over those outside the list (-inf: none), 0
+ *   grad         [rows][ld_grad] out in the student's type, or NULL; may be the student's own
+ *                array (with its ld); behind V it is left as it was
+ * A row that does not learn has loss 0, stats 0 and a gradient of zeros.  A row left out has loss
+ * and stats NaN and a gradient of zeros: one with a NaN or +inf in it or in its list, with nothing
+ * but -inf in it, or without lse in its list (DF_ERR_NAN); with a list outside 0 .. n_teacher - 1,
+ * an id outside -1 .. V - 1 or one that stands twice in its list (DF_ERR_ARG). */
+size_t dflash_distill_workspace_size(int rows, int V);
+int dflash_distill(const df_rows* student, int K, int n_teacher, const int32_t* id, const float* val,
+                   const float* lse, const int32_t* teacher_row, float temperature, const float* weight,
+                   float* loss, float* stats, void* grad, int64_t ld_grad, void* ws, size_t ws_bytes,
+                   df_stream stream);
+
+/* dflash_distill_backward -- the gradient of sum_r grad_loss[r] loss[r] by the student's logits,
+ * from dflash_distill's arguments and its stats.
+ *   grad_loss    [rows] fp32 or NULL: 1
+ *   Rows that do not learn or were left out have a gradient of zeros; the workspace of
+ *   dflash_distill_workspace_size. */
+int dflash_distill_backward(const df_rows* student, int K, int n_teacher, const int32_t* id, const float* val,
+                            const float* lse, const int32_t* teacher_row, float temperature, const float* weight,
+                            const float* stats, const float* grad_loss, void* grad, int64_t ld_grad, void* ws,
+                            size_t ws_bytes, df_stream stream);
+
+/* ------------------------------------------------------------------------------------
  * dflash_linear -- building block: out (+)= X . W^T on the tensor cores.
  *
  * Every projection of the step (q/k/v, o, gate/up, down, context fusion, LM head) is
