@@ -8,6 +8,7 @@
 // the list's part: where the student is sure of the list, that difference has no digits left.
 // Both passes are bound by the row's bytes: loss reads a row once; with the gradient a row is read
 // again from L2 by the CTAs that just read it, and written.
+#define DF_ROW_THREADS 512
 #include "rows.cuh"
 #include "runtime.h"
 #include "trace.h"
@@ -109,37 +110,44 @@ DF_DEV int list_of(const DistillArgs& a, int r) {
   return list < -1 || list >= a.n_teacher ? -2 : list;
 }
 
-// Writes f(x, piece) (VE values) for this CTA's pieces of the gradient's row; U loads ahead.
-// `aligned`: the gradient's pieces start at 16-byte addresses like the student's.
+// Replaces x (VE values, the student's logits with READ) by f(x) in this CTA's pieces of the
+// gradient's row, U loads ahead.
 template <int U, bool READ, class E, class F>
 DF_DEV void write_pieces(const RowPart<E>& p, E* grad, F&& f) {
   constexpr int VE = RowPart<E>::VE;
+  // the gradient's pieces start at 16-byte addresses like the student's
   const bool aligned = (reinterpret_cast<uintptr_t>(grad - p.head) & 15) == 0;
   uint4* out = reinterpret_cast<uint4*>(grad - p.head);
+  float x[VE];
+  auto set = [&](int piece) {
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      const int k = p.id(piece, e);
+      if ((unsigned)k < (unsigned)p.V) RowOf<E>::set(grad, k, x[e]);
+    }
+  };
   for (int i = p.lo + (int)threadIdx.x; i < p.hi; i += U * kRowThreads) {
     uint4 v[U];
+    if (READ)
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      v[j] = RowPart<E>::nothing();
-      if (READ && i + j * kRowThreads < p.hi) v[j] = p.load(i + j * kRowThreads);
-    }
+      for (int j = 0; j < U; ++j) v[j] = p.whole_or_nothing(i + j * kRowThreads);
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       const int piece = i + j * kRowThreads;
-      if (piece >= p.hi) break;
-      float x[VE];
-      RowOf<E>::unpack(v[j], x);
+      if (READ) RowOf<E>::unpack(v[j], x);
       f(x);
-      if (aligned && p.whole(piece)) {
+      if (piece >= p.hi) continue;
+      if (aligned)
         out[piece] = RowOf<E>::pack(x);
-      } else {
-#pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          const int k = p.id(piece, e);
-          if ((unsigned)k < (unsigned)p.V) RowOf<E>::set(grad, k, x[e]);
-        }
-      }
+      else
+        set(piece);
     }
+  }
+  const int edge = p.my_edge();
+  if (edge >= 0) {
+    if (READ) RowOf<E>::unpack(p.edge(edge), x);
+    f(x);
+    set(edge);
   }
 }
 template <class E>
@@ -197,7 +205,7 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a, int
     return;
   }
   const Temper T(a.temperature);
-  const int n_words = ((part.hi - part.lo) * VE + 31) / 32;
+  const int n_words = ((part.end - part.begin) * VE + 31) / 32;
   for (int i = tid; i < n_words; i += kRowThreads) bits[i] = 0;
   if (tid == 0) s.flags = 0;
   if (ctas > 1) row_sync(ctas);     // every CTA of the cluster runs
@@ -205,12 +213,12 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a, int
   en.load(a, T, list, s.tmp);       // with barriers behind the zeros
   float z[kPer];
   bool mine[kPer];
-  const int bit0 = part.lo * VE - part.head;   // element of bit 0
+  const int bit0 = part.begin * VE - part.head;   // element of bit 0
   uint32_t bad = en.bad;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int b = en.id[j] - bit0;
-    mine[j] = en.id[j] >= 0 && b >= 0 && b < (part.hi - part.lo) * VE;
+    mine[j] = en.id[j] >= 0 && b >= 0 && b < (part.end - part.begin) * VE;
     z[j] = mine[j] ? RowOf<E>::value(part.row, en.id[j]) : -INFINITY;
     if (mine[j] && (atomicOr(&bits[b >> 5], 1u << (b & 31)) >> (b & 31) & 1)) bad |= 2;
   }
@@ -219,38 +227,30 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a, int
   // largest logit and the sum outside the list, a thread's own
   float m = -INFINITY, rest = 0.f, check = -INFINITY;
   const uint8_t* marks = reinterpret_cast<const uint8_t*>(bits);
-  for (int i = part.lo + tid; i < part.hi; i += 4 * kRowThreads) {
-    uint4 v[4];
+  for_pieces<4>(part, [&](const float* x, int piece, bool on) {
+    float big = x[0];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      v[j] = i + j * kRowThreads < part.hi ? part.load(i + j * kRowThreads) : RowPart<E>::nothing();
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int piece = i + j * kRowThreads;
-      const float big = RowOf<E>::largest(v[j]);
-      check = max_nan(check, big);
-      if (!(big > -INFINITY)) continue;
-      if (big > m) {
-        rest *= ex2_approx((m - big) * T.c);
-        m = big;
-      }
-      float x[VE];
-      RowOf<E>::unpack(v[j], x);
-      uint32_t listed = 0;
-      if (piece < part.hi) {
-        const int q = piece - part.lo;
-        listed = VE == 8 ? marks[q] : (marks[q >> 1] >> ((q & 1) * 4)) & 15u;
-      }
-      if (listed == 0) {
-#pragma unroll
-        for (int e = 0; e < VE; ++e) rest += ex2_approx((x[e] - m) * T.c);
-      } else {
-#pragma unroll
-        for (int e = 0; e < VE; ++e)
-          if (!(listed >> e & 1)) rest += ex2_approx((x[e] - m) * T.c);
-      }
+    for (int e = 1; e < VE; ++e) big = max_nan(big, x[e]);
+    check = max_nan(check, big);
+    if (!(big > -INFINITY)) return;
+    if (big > m) {
+      rest *= ex2_approx((m - big) * T.c);
+      m = big;
     }
-  }
+    uint32_t listed = 0;
+    if (on) {
+      const int q = piece - part.begin;
+      listed = VE == 8 ? marks[q] : (marks[q >> 1] >> ((q & 1) * 4)) & 15u;
+    }
+    if (listed == 0) {
+#pragma unroll
+      for (int e = 0; e < VE; ++e) rest += ex2_approx((x[e] - m) * T.c);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VE; ++e)
+        if (!(listed >> e & 1)) rest += ex2_approx((x[e] - m) * T.c);
+    }
+  });
   // the CTA's part
   float big = warp_max(m);
   __syncthreads();
@@ -339,11 +339,11 @@ __global__ void __launch_bounds__(kRowThreads) distill_backward_kernel(DistillAr
   en.load(a, T, list, tmp);
   float z[kPer];
   bool mine[kPer];
-  const int bit0 = part.lo * VE - part.head;
+  const int bit0 = part.begin * VE - part.head;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int b = en.id[j] - bit0;
-    mine[j] = en.id[j] >= 0 && b >= 0 && b < (part.hi - part.lo) * VE;
+    mine[j] = en.id[j] >= 0 && b >= 0 && b < (part.end - part.begin) * VE;
     z[j] = mine[j] ? RowOf<E>::value(part.row, en.id[j]) : 0.f;
   }
   __syncthreads();     // an entry's logit is read before it may be written over
@@ -360,7 +360,7 @@ int launch_distill(const DistillArgs& a, cudaStream_t st) {
   const int ctas = row_ctas(a.x.rows, a.x.V);
   const auto f = a.x.dtype == DF_F32 ? distill_kernel<float> : distill_kernel<uint16_t>;
   const size_t smem = sizeof(Shared) + ((size_t)(a.x.V + 16) / ctas + 64) / 8 + 16;
-  if (ensure_dynamic_smem(f, smem) != cudaSuccess) return DF_ERR_CUDA;
+  if (ensure_dynamic_smem(f, smem) != cudaSuccess || prefer_shared(f) != cudaSuccess) return DF_ERR_CUDA;
   DF_TRACE("distill", st);
   return done(launch_cluster(f, (unsigned)a.x.rows * ctas, ctas, smem, st, a, ctas));
 }

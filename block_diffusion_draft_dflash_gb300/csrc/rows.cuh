@@ -3,16 +3,21 @@
 //
 // A row is read in aligned pieces of 16 bytes, whatever its first address: piece i holds the
 // row's elements i * VE - head .. (VE = 4 fp32 or 8 bf16 values, head = elements between the
-// aligned address below the row and the row).  The first and the last piece may reach over the
-// row's ends; they are read element by element and what lies outside counts as -inf.  The CTAs
-// of a cluster take consecutive runs of pieces.
+// aligned address below the row and the row).  The CTAs of a cluster take consecutive runs of the
+// pieces that lie in the row whole.  The first and the last piece may reach over the row's ends
+// (edges, of the first and the last CTA); they are read element by element, and what lies outside
+// counts as -inf.
 #pragma once
 #include "common.cuh"
 #include "rows.h"
 
 namespace df {
+namespace {   // each file has its own number of threads
 
-constexpr int kRowThreads = 512;
+#ifndef DF_ROW_THREADS
+#define DF_ROW_THREADS 256
+#endif
+constexpr int kRowThreads = DF_ROW_THREADS;   // of a CTA
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr uint32_t kNegInfKey = 0x007FFFFFu;   // float_key(-inf)
 constexpr uint32_t kPosInfKey = 0xFF800000u;   // float_key(+inf); a NaN's key is above it
@@ -178,32 +183,30 @@ struct RowOf<uint16_t> {   // bf16
   }
 };
 
-// One CTA's run of pieces of a row.
+// One CTA's part of a row.
 template <class E>
 struct RowPart {
   static constexpr int VE = RowOf<E>::VE;
   const E* row;          // element 0
   const uint4* pieces;   // piece 0 (its first `head` elements lie before the row)
   int head, V;
-  int first, n_whole;    // pieces that lie in the row whole: first .. first + n_whole - 1
-  int lo, hi;            // this CTA's pieces
+  int lo, hi;            // whole pieces
+  int begin, end;        // with the edges
 
   DF_DEV RowPart(const E* data, long long ld, long long r, int V_, int rank, int ctas) : V(V_) {
     row = data + r * ld;
     head = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(E));
     pieces = reinterpret_cast<const uint4*>(row - head);
-    first = head > 0;
-    const int n = (V + head + VE - 1) / VE;
-    n_whole = max((V + head) / VE - first, 0);
-    const int each = (n + ctas - 1) / ctas;
-    lo = min(rank * each, n);
-    hi = min(lo + each, n);
+    const int first = head > 0, upto = max((V + head) / VE, first);      // whole pieces of the row
+    const int each = (upto - first + ctas - 1) / ctas;
+    lo = min(first + rank * each, upto);
+    hi = min(lo + each, upto);
+    begin = rank == 0 ? 0 : lo;
+    end = rank == ctas - 1 ? (V + head + VE - 1) / VE : hi;
   }
   DF_DEV int id(int piece, int e) const { return piece * VE + e - head; }
-  DF_DEV bool whole(int piece) const { return (unsigned)(piece - first) < (unsigned)n_whole; }
-  // Elements of a piece; -inf outside the row.
-  DF_DEV uint4 load(int piece) const {
-    if (whole(piece)) return pieces[piece];
+  // Elements of an edge; -inf outside the row.
+  DF_DEV uint4 edge(int piece) const {
     float x[VE];
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
@@ -212,25 +215,40 @@ struct RowPart {
     }
     return RowOf<E>::pack(x);
   }
-  static DF_DEV uint4 nothing() {
+  DF_DEV uint4 load(int piece) const { return piece >= lo && piece < hi ? pieces[piece] : edge(piece); }
+  DF_DEV uint4 whole_or_nothing(int piece) const {
     const uint32_t m = RowOf<E>::kNegInf;
-    return make_uint4(m, m, m, m);
+    uint4 v = make_uint4(m, m, m, m);
+    if (piece < hi) v = pieces[piece];
+    return v;
+  }
+  // The edge that this thread reads (thread 0 the first, thread 1 the last), or -1.
+  DF_DEV int my_edge() const {
+    if (threadIdx.x == 0 && begin < lo) return begin;
+    if (threadIdx.x == 1 && end > hi) return end - 1;
+    return -1;
   }
 };
 
-// f(x[VE], piece) for every piece of this thread (pieces lo + t, lo + t + 512, ...), U loads ahead.
+// f(x[VE], piece, on) for every piece of this thread (whole ones lo + t, lo + t + kRowThreads, ...,
+// U loads ahead, and its edge).  on: there is such a piece; else x is -inf.
 template <int U, class E, class F>
 DF_DEV void for_pieces(const RowPart<E>& p, F&& f) {
+  float x[RowPart<E>::VE];
   for (int i = p.lo + (int)threadIdx.x; i < p.hi; i += U * kRowThreads) {
     uint4 v[U];
 #pragma unroll
-    for (int j = 0; j < U; ++j) v[j] = i + j * kRowThreads < p.hi ? p.load(i + j * kRowThreads) : RowPart<E>::nothing();
+    for (int j = 0; j < U; ++j) v[j] = p.whole_or_nothing(i + j * kRowThreads);
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      float x[RowPart<E>::VE];
       RowOf<E>::unpack(v[j], x);
-      f(x, i + j * kRowThreads);
+      f(x, i + j * kRowThreads, i + j * kRowThreads < p.hi);
     }
+  }
+  const int edge = p.my_edge();
+  if (edge >= 0) {
+    RowOf<E>::unpack(p.edge(edge), x);
+    f(x, edge, true);
   }
 }
 
@@ -284,7 +302,7 @@ struct MassScale {
       ref = rintf(a * 1024.f) * (1.f / 1024.f);
     }
     shift = 12288.f - ref;
-    floor = (ref - 64.f) / c_hi;
+    floor = (ref - 63.75f) / c_hi;     // 2^-63.75 counts as 0 (and is the last of 2048 bins of 1/32)
     top = bits(largest);
   }
   DF_DEV float arg(float l) const { return fmaxf(l - base, floor); }
@@ -293,41 +311,50 @@ struct MassScale {
 };
 
 // A thread's share of a mass: two 32-bit sums of the bits of a + 12 (units of 2^-20) and of
-// what is left + 1.5 * 2^-19 (units of 2^-42), which stay exact for 512 elements.
+// what is left + 1.5 * 2^-19 (units of 2^-42), exact for n <= 512 terms.
 struct MassSum {
   uint32_t a = 0, b = 0;
+  int n = 0;           // terms in a and b (kept by the caller)
   uint64_t sum = 0;
-  int n = 0;
   DF_DEV void fold() {
     sum += ((int64_t)(int32_t)(a - (uint32_t)n * 0x41400000u) << 22) + (int32_t)(b - (uint32_t)n * 0x36400000u);
     a = b = 0;
     n = 0;
   }
+  DF_DEV void room(int more) {
+    if (n + more > 512) fold();
+  }
 };
 
-// Adds the mass of logit l.  t_hi, t_lo: the table.
-DF_DEV void add_mass(MassSum& s, const MassScale& c, const float* t_hi, const float* t_lo, float l) {
+// The mass of logit l as the terms of a and b; returns c.bits(l).  table[j]: 2^(j / 1024).
+template <class Table>
+DF_DEV uint32_t mass_terms(const MassScale& c, const Table& table, float l, uint32_t* a, uint32_t* b) {
   const float x = c.arg(l);
   const float t = fmaf(x, c.c_hi, c.shift);
   const float g = t - c.shift;                        // exact
   float r = fmaf(x, c.c_hi, -g);
   r = fmaf(x, c.c_lo, r);
-  const uint32_t u = __float_as_uint(t), j = u & 1023u;
+  const uint32_t u = __float_as_uint(t);
+  const float2 w = table[u & 1023u];
   const float two_n = __uint_as_float(0x3F800000u + ((u & 0xFFFFFC00u) << 13));
-  // 2^r - 1 for |r| <= 2^-11 + 2^-24: the next term is below 2^-51
+  // 2^r - 1 for |r| <= 2^-11 + 2^-24: the next term is below 2^-50
   const float p = r * fmaf(r, fmaf(r, 0.0555041086648f, 0.2402265069591f), 0.6931471805599f);
-  const float hi = t_hi[j] * two_n, q = fmaf(hi, p, t_lo[j] * two_n);
+  const float hi = w.x * two_n, q = fmaf(hi, p, w.y * two_n);
   const float f1 = (hi + q) + 12.f, f2 = f1 - 12.f;
   const float f3 = ((hi - f2) + q) + 2.86102294921875e-6f;   // 1.5 * 2^-19
-  s.a += __float_as_uint(f1);
-  s.b += __float_as_uint(f3);
-  ++s.n;
+  *a = __float_as_uint(f1);
+  *b = __float_as_uint(f3);
+  return u;
 }
-DF_DEV uint64_t mass_of(const MassScale& c, const float* t_hi, const float* t_lo, float l) {
-  MassSum s;
-  add_mass(s, c, t_hi, t_lo, l);
-  s.fold();
-  return s.sum;
+// Adds it (the caller counts the term).
+template <class Table>
+DF_DEV uint32_t add_mass(MassSum& s, const MassScale& c, const Table& table, float l) {
+  uint32_t a, b;
+  const uint32_t u = mass_terms(c, table, l, &a, &b);
+  s.a += a;
+  s.b += b;
+  return u;
 }
 
+}  // namespace
 }  // namespace df

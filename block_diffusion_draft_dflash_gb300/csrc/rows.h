@@ -7,6 +7,10 @@
 
 namespace df {
 
+struct SampleLeft {               // a row that one pass did not decide
+  uint64_t about;                 // about its mass, 0: not known
+  uint32_t largest, on;           // key of its largest logit; 0: decided
+};
 struct SampleArgs {
   df_rows x;
   int group;                      // rows r of one setting: r / group
@@ -16,6 +20,7 @@ struct SampleArgs {
   int32_t* token;                 // [rows]
   float* logprob;                 // [rows], may be null
   int32_t* n_kept;                // [rows], may be null
+  SampleLeft* left;               // [rows]
   int* status;
 };
 int launch_sample(const SampleArgs& a, cudaStream_t st);

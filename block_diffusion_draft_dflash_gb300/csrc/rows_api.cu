@@ -45,8 +45,10 @@ using namespace df;
 extern "C" {
 
 size_t dflash_sample_workspace_size(int rows, int V) {
-  (void)rows; (void)V;
-  return kAlign;
+  (void)V;
+  Carver cv(nullptr);
+  cv.take<SampleLeft>(rows > 0 ? (size_t)rows : 1);
+  return cv.off;
 }
 
 int dflash_sample(const df_rows* x, int group, const float* temperature, const int32_t* top_k, const float* top_p,
@@ -61,6 +63,8 @@ int dflash_sample(const df_rows* x, int group, const float* temperature, const i
   SampleArgs a{};
   a.x = *x; a.group = group; a.temperature = temperature; a.top_k = top_k; a.top_p = top_p; a.min_p = min_p; a.u = u;
   a.token = token; a.logprob = logprob; a.n_kept = n_kept; a.status = status_of(ws);
+  Carver cv(ws);
+  a.left = cv.take<SampleLeft>((size_t)x->rows);
   return launch_sample(a, (cudaStream_t)stream);
 }
 

@@ -1,6 +1,7 @@
 // Per-device host state (see runtime.h).
 #include <map>
 #include <mutex>
+#include <set>
 #include <utility>
 
 #include "runtime.h"
@@ -10,6 +11,7 @@ namespace {
 std::mutex mu;
 std::map<int, int> sm_count;                                // device -> SMs
 std::map<std::pair<int, const void*>, size_t> smem_set;     // (device, kernel) -> bytes allowed
+std::set<std::pair<int, const void*>> shared_preferred;     // (device, kernel) told prefer_shared
 
 int current_device() {
   int dev = 0;
@@ -39,6 +41,16 @@ cudaError_t ensure_dynamic_smem(const void* func, size_t bytes) {
   if (have >= bytes) return cudaSuccess;
   const cudaError_t e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e == cudaSuccess) have = bytes;
+  return e;
+}
+
+cudaError_t prefer_shared(const void* func) {
+  const int dev = current_device();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> g(mu);
+  if (shared_preferred.count({dev, func})) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(func, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess) shared_preferred.insert({dev, func});
   return e;
 }
 

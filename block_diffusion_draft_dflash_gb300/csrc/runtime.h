@@ -22,4 +22,13 @@ cudaError_t ensure_dynamic_smem(F* func, size_t bytes) {
   return ensure_dynamic_smem(reinterpret_cast<const void*>(func), bytes);
 }
 
+// Asks for the largest shared-memory part of the SM's memory for `func` (once per device and
+// kernel): without it the split that is chosen may hold one CTA where the registers allow more.
+cudaError_t prefer_shared(const void* func);
+
+template <typename F>
+cudaError_t prefer_shared(F* func) {
+  return prefer_shared(reinterpret_cast<const void*>(func));
+}
+
 }  // namespace df

@@ -2,19 +2,24 @@
 //
 // A row's tokens stand in order of (logit descending, id ascending), as numbers comp = key << 32
 // | ~id that are all different (key: the logit as an order-preserving integer).  Every filter
-// keeps a prefix of that order, so a draw needs borders in it: the comp at which a count or a
+// keeps a prefix of that order, so a draw needs borders in it: the token at which a count or a
 // mass is reached.
 //
-// Few tokens (top-k up to 1024, the largest logits): one pass keeps the largest logit of each of
-// up to 4096 groups (the elements that one thread reads).  The k-th largest of these is a lower
-// bound of the k-th largest logit, and only the few groups that reach it are read again (from
-// L2): hardly more than k candidates, which one CTA sorts.
-// Any number of tokens: a second pass sums the masses and counts tokens in 1024 bins of 1/16 of
-// a power of two of probability.  The counts say in which bin a border should lie; a third pass
-// sums the mass before that bin and its neighbours exactly and lists their tokens, and if the
-// border is not among them the next bin is chosen between exact masses.  Where a bin has too many
-// tokens, its range of keys is cut by 1024 again until one key is left, whose tokens stand in
-// order of their ids.
+// A list of the first tokens.  One pass keeps the largest logit of each of 2048 groups (the
+// elements that one thread reads).  The k-th largest of these is a lower bound of the k-th largest
+// logit, and only the few groups that reach it are read again (from L2): hardly more than k
+// candidates, which one CTA sorts.  That is all for a top-k up to 1024, for the largest logits and
+// for min-p alone (whose bound is known).
+// Mass alone (top-p, or nothing cut).  The first pass also sums exp((l - max) / T) in fp32, which
+// gives the row's mass within 2^-15.  If both ends of that interval put the borders on the same
+// tokens of the list, they are right; a sure row's are.
+// Otherwise a pass counts tokens in 2048 bins of 1/32 of a power of two of probability, from which
+// follows where a border should lie; one more pass sums all masses, and those before the bins of
+// the two borders, exactly, and lists these bins' tokens.  A border that is not among them is
+// looked for bin by bin between exact masses.  Where a bin has too many tokens, its range of keys
+// is cut by 2048 again until one key is left, whose tokens stand in order of their ids.
+#include <algorithm>
+
 #include "rows.cuh"
 #include "runtime.h"
 #include "trace.h"
@@ -22,10 +27,16 @@
 namespace df {
 namespace {
 
-constexpr int kListCap = 2048;     // candidates that one CTA sorts
-constexpr int kMaxTop = 1024;      // tokens that the first way can find
-constexpr int kBins = 1024;
-constexpr int kMaxGroups = 4096;
+constexpr int kListCap = 2048;     // tokens that one CTA sorts
+constexpr int kHalf = kListCap / 2;
+constexpr int kMaxTop = 1024;      // top-k and K that the list of the first tokens is used for
+constexpr int kLikely = 128;       // tokens listed (at least) where mass alone decides
+constexpr int kBuckets = 512;      // of threshold() and sort_list()
+constexpr int kBins = 2048;
+constexpr int kBinBits = 11;
+constexpr uint32_t kCountMask = (1u << 19) - 1;   // a bin's tokens; above it the sum of their places in the bin
+constexpr int kSub = 8;            // groups of a thread times CTAs of a row
+constexpr uint32_t kNone = 1u << 20, kAbove = 1u << 21;   // no bin of a level: below it, above it
 constexpr uint32_t kAround = 512;  // tokens listed on either side of the bin where a border should be
 
 __device__ const Pow2Table kPow2;
@@ -36,23 +47,31 @@ struct Bins {          // running sums over bins: tokens, and about their mass
 };
 struct Shared {
   union {
-    uint32_t group_key[kMaxGroups];          // of the whole row, in the first CTA
-    uint64_t list[kListCap];                 // candidates, in the first CTA
+    uint32_t group_key[kSub * kRowThreads];  // of the whole row, in the first CTA
+    uint64_t list[kListCap];                 // the first CTA's is the row's
   };
-  Bins bins, fine;
-  uint32_t hist[kBins];
-  float t_hi[1024], t_lo[1024];
+  union {
+    Bins bins;
+    uint64_t each_mass[kListCap];            // of the list's tokens
+  };
+  union {
+    uint32_t hist[kBins];
+    uint16_t chosen[kSub * kRowThreads];     // groups that one CTA reads again
+  };
+  float2 table[1024];
   // written by the first CTA in every CTA
   uint32_t word[8];
   // collected in the first CTA
-  uint64_t mass, mass_in;
-  uint32_t n_list, key_min, key_max, equal[8], at_id;
+  uint64_t mass, mass_in, mass_2;
+  uint32_t n_list, n_list2, key_min, key_max, equal[8], at_id, live;
+  float tail[8], sums[8];
   // one CTA's own
   uint64_t tmp64[kRowWarps];
   uint32_t tmp32[kRowWarps];
   float tmpf[kRowWarps];
   uint64_t found_comp, found_mass;
-  uint32_t found_n, found;
+  uint32_t found_n, found, n_chosen;
+  uint16_t rows[kRowThreads];
 };
 
 DF_DEV uint32_t logit_key(float l) { return float_key(l + 0.f); }   // -0 as +0
@@ -60,11 +79,47 @@ DF_DEV uint64_t comp_of(uint32_t key, int id) { return ((uint64_t)key << 32) | (
 DF_DEV uint32_t key_of(uint64_t comp) { return (uint32_t)(comp >> 32); }
 DF_DEV int id_of(uint64_t comp) { return (int)~(uint32_t)comp; }
 
+struct GlobalTable {
+  DF_DEV float2 operator[](uint32_t j) const { return make_float2(kPow2.hi[j], kPow2.lo[j]); }
+};
+DF_DEV uint64_t mass_of(const MassScale& c, float l) {
+  MassSum m;
+  add_mass(m, c, GlobalTable{}, l);
+  m.n = 1;
+  m.fold();
+  return m.sum;
+}
+
 // A border in the order: its token, the tokens up to it and their mass.
 struct Border {
   uint64_t comp, mass;
   uint32_t n;
 };
+
+// f * m for f = 0 .. 1, rounded down; *more: it was not a whole number.
+DF_DEV uint64_t part_of(float f, uint64_t m, bool* more) {
+  const uint32_t b = __float_as_uint(f) & 0x7FFFFFFFu, e = b >> 23;
+  const uint64_t mant = e ? (b & 0x7FFFFFu) | 0x800000u : b;
+  const int shift = 150 - (int)max(e, 1u);                     // f = mant / 2^shift
+  const uint64_t lo = m * mant, hi = __umul64hi(m, mant);      // hi < 2^24
+  if (shift >= 64) {
+    const int s = shift - 64;
+    *more = lo != 0 || (s < 64 && (hi & ((1ull << s) - 1)) != 0) || (s >= 64 && hi != 0);
+    return s < 64 ? hi >> s : 0;
+  }
+  *more = (lo & ((1ull << shift) - 1)) != 0;
+  return (hi << (64 - shift)) | (lo >> shift);
+}
+// First mass above u * m, and first mass that reaches p * m.
+DF_DEV uint64_t mass_above(float u, uint64_t m) {
+  bool more;
+  return part_of(u, m, &more) + 1;
+}
+DF_DEV uint64_t mass_share(float p, uint64_t m) {
+  bool more;
+  const uint64_t x = part_of(p, m, &more);
+  return x + more ? x + more : 1;
+}
 
 template <class E>
 struct RowWork {
@@ -83,176 +138,331 @@ struct RowWork {
       for (int i = 0; i < n; ++i) st_remote(at_rank(&s.word[i], tid), w[i]);
   }
 
-  // -------------------------------------------------------------------------- largest logits
-  int sub;             // groups of a thread: 4 / ctas, at least 1
-  float top[4];        // their largest logits (the first `sub`)
+  // -------------------------------------------------------------------------- the first tokens
+  float top[kSub];     // largest logits of this thread's groups (the first kSub / ctas)
+  float sum[kSub];     // with SUMS: their sums of 2^((l - ref) c)
+  float ref;           // a logit of the thread at most 8 / c below its largest
 
-  // Reads the row; SUMS: also a running log-sum (max, sum of 2^((l - max) c)) of the thread.
+  // Reads the row.  SUMS: also the groups' sums, and with `count` the number of logits above -inf.
   template <bool SUMS>
-  DF_DEV void read_tops(float c, float* run_max, float* run_sum) {
-    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-    float rm = -INFINITY, rs = 0.f;
-    for (int i = part.lo + tid; i < part.hi; i += 4 * kRowThreads) {
-      uint4 v[4];
+  DF_DEV void read_tops(float c, bool count, uint32_t* live) {
+    float m[kSub];
+    uint32_t n_live = 0;
+    ref = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        v[j] = i + j * kRowThreads < part.hi ? part.load(i + j * kRowThreads) : RowPart<E>::nothing();
+    for (int j = 0; j < kSub; ++j) m[j] = -INFINITY, sum[j] = 0.f;
+    // four groups' pieces, largest logit `big`
+    auto add = [&](const uint4* v, int n, float big, float* to) {
+      if ((big - ref) * c > 8.f) {      // also the first time
+        const float f = ref > -INFINITY ? ex2_approx((ref - big) * c) : 0.f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float big = RowOf<E>::largest(v[j]);
-        m[j] = max_nan(m[j], big);
-        if (SUMS && big > -INFINITY) {
-          if (big > rm) {
-            rs *= ex2_approx((rm - big) * c);
-            rm = big;
-          }
-          float x[VE];
-          RowOf<E>::unpack(v[j], x);
+        for (int j = 0; j < kSub; ++j) sum[j] *= f;
+        ref = big;
+      }
+      if (!(ref > -INFINITY)) return;
 #pragma unroll
-          for (int e = 0; e < VE; ++e) rs += ex2_approx((x[e] - rm) * c);
+      for (int j = 0; j < n; ++j) {
+        float x[VE];
+        RowOf<E>::unpack(v[j], x);
+        if (count)
+#pragma unroll
+          for (int e = 0; e < VE; ++e) n_live += x[e] > -INFINITY;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) x[e] = ex2_approx((x[e] - ref) * c);
+#pragma unroll
+        for (int w = VE / 2; w > 0; w >>= 1)
+#pragma unroll
+          for (int e = 0; e < w; ++e) x[e] += x[e + w];
+        to[j] += x[0];
+      }
+    };
+    constexpr int U = SUMS ? 4 : 8;
+    for (int i0 = part.lo + tid; i0 < part.hi; i0 += kSub * kRowThreads) {
+#pragma unroll
+      for (int h = 0; h < kSub; h += U) {
+        uint4 v[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) v[j] = part.whole_or_nothing(i0 + (h + j) * kRowThreads);
+        float big = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+          const float l = RowOf<E>::largest(v[j]);
+          m[h + j] = max_nan(m[h + j], l);
+          if (SUMS) big = fmaxf(big, l);
         }
+        if (SUMS) add(v, U, big, sum + h);
       }
     }
-    sub = ctas == 1 ? 4 : ctas == 2 ? 2 : 1;
-    if (sub == 4) {
-      top[0] = m[0]; top[1] = m[1]; top[2] = m[2]; top[3] = m[3];
-    } else {
-      top[0] = max_nan(m[0], m[1]);
-      top[1] = max_nan(m[2], m[3]);
-      if (sub == 1) top[0] = max_nan(top[0], top[1]);
+    const int edge = part.my_edge();       // goes with the thread's first group
+    if (edge >= 0) {
+      const uint4 v = part.edge(edge);
+      const float l = RowOf<E>::largest(v);
+      m[0] = max_nan(m[0], l);
+      if (SUMS) add(&v, 1, l, sum);
     }
-    if (SUMS) { *run_max = rm; *run_sum = rs; }
+    const int sub = kSub / ctas;
 #pragma unroll
-    for (int g = 0; g < 4; ++g)
+    for (int j = 0; j < kSub; ++j) top[j] = m[j];
+#pragma unroll
+    for (int n = kSub / 2; n > 0; n >>= 1)
+      if (sub <= n)
+#pragma unroll
+        for (int j = 0; j < n; ++j) {
+          top[j] = max_nan(top[2 * j], top[2 * j + 1]);
+          if (SUMS) sum[j] = sum[2 * j] + sum[2 * j + 1];
+        }
+#pragma unroll
+    for (int g = 0; g < kSub; ++g)
       if (g < sub)
         st_remote(at_rank(&s.group_key[(rank * sub + g) * kRowThreads + tid], 0),
                   top[g] == top[g] ? logit_key(top[g]) : 0xFFFFFFFFu);
+    if (SUMS) *live = n_live;
   }
 
-  // First CTA, behind a row_sync: the largest key, and for k > 0 a key that at least k of the
-  // groups reach (at least 1 above -inf's).
+  // First CTA, behind a row_sync: the largest key, and for k > 1 a key above -inf's that at least k
+  // groups reach, or all that have a token.  Groups are counted in bins between the largest
+  // and the smallest, and the smallest key of the bins that hold the first k is taken.
   DF_DEV uint32_t threshold(int k, uint32_t* largest) {
-    uint32_t key[8];
-    uint32_t big = 0;
-    const int n = ctas * sub;
+    uint32_t key[kSub];
+    uint32_t big = 0, small = 0xFFFFFFFFu;
+    if (k > 1)
+      for (int b = tid; b < kBuckets; b += kRowThreads) s.hist[b] = 0;
+    if (tid == 0) s.key_max = 0, s.key_min = 0xFFFFFFFFu, s.found = kBuckets;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      key[j] = j < n ? s.group_key[j * kRowThreads + tid] : 0;
+    for (int j = 0; j < kSub; ++j) {
+      key[j] = s.group_key[j * kRowThreads + tid];
       big = max(big, key[j]);
+      if (key[j] > kNegInfKey) small = min(small, key[j]);
     }
+    __syncthreads();
     big = __reduce_max_sync(0xffffffffu, big);
+    small = __reduce_min_sync(0xffffffffu, small);
+    if ((tid & 31) == 0) {
+      atomicMax(&s.key_max, big);
+      atomicMin(&s.key_min, small);
+    }
     __syncthreads();
-    if ((tid & 31) == 0) s.tmp32[tid >> 5] = big;
-    __syncthreads();
-    big = __reduce_max_sync(0xffffffffu, s.tmp32[tid & (kRowWarps - 1)]);
+    big = s.key_max;
     *largest = big;
     if (k <= 1 || big <= kNegInfKey || big >= kPosInfKey) return big;
-    // lo: reached by k groups or the smallest finite key; hi: reached by fewer
-    uint32_t lo = kNegInfKey + 1, hi = big;
-    const int enough = k + (k >> 3) + 4;
-    for (int step = 0; step < 32 && hi - lo > 1; ++step) {
-      const uint32_t mid = lo + ((hi - lo) >> 1);
-      uint32_t c = 0;
+    const float bigf = key_float(big), scale_to = (float)kBuckets / (bigf - key_float(s.key_min));
+    auto bin = [&](uint32_t kk) { return min((int)((bigf - key_float(kk)) * scale_to), kBuckets - 1); };   // NaN: 0
 #pragma unroll
-      for (int j = 0; j < 8; ++j) c += key[j] >= mid;
-      c = block_add(c, s.tmp32);
-      if ((int)c >= k) {
-        lo = mid;
-        if ((int)c <= enough) break;
-      } else {
-        hi = mid;
-      }
+    for (int j = 0; j < kSub; ++j)
+      if (key[j] > kNegInfKey) atomicAdd(&s.hist[bin(key[j])], 1u);
+    __syncthreads();
+    constexpr int PER = kBuckets / kRowThreads;
+    uint32_t c[PER], mine = 0, all;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) mine += c[j] = s.hist[tid * PER + j];
+    uint32_t run = block_scan(mine, s.tmp32, &all);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      if (run < (uint32_t)k && run + c[j] >= (uint32_t)k) s.found = tid * PER + j;
+      run += c[j];
     }
-    return lo;
+    if (tid == 0) s.key_max = 0xFFFFFFFFu;
+    __syncthreads();
+    const int last = (int)s.found;
+    small = 0xFFFFFFFFu;
+#pragma unroll
+    for (int j = 0; j < kSub; ++j)
+      if (key[j] > kNegInfKey && bin(key[j]) <= last) small = min(small, key[j]);
+    small = __reduce_min_sync(0xffffffffu, small);
+    if ((tid & 31) == 0) atomicMin(&s.key_max, small);
+    __syncthreads();
+    return (int)all < k ? kNegInfKey + 1 : s.key_max;
   }
 
-  // Every warp puts the elements that reach `least` of its threads' groups on the first CTA's list.
-  DF_DEV void list_tops(uint32_t least) {
-    const int lane = tid & 31, per = 4 / sub;
+  // Puts the elements that reach `least` on the row's list: the groups that reach it are read
+  // again, by all threads.  Every CTA lists its own and hands them to the first one.  SUMS: the sum
+  // of the others, relative to the largest logit, goes to the first CTA's tail: of the groups not
+  // read again from the first pass, of those that are from this one, so that no large term that is
+  // on the list has left its rounding there.  Its sums: of all groups.
+  template <bool SUMS>
+  DF_DEV void list_tops(uint32_t least, float largest, float c) {
+    const int lane = tid & 31, sub = kSub / ctas, per = ctas;
+    float tail = 0.f, all = 0.f;
+    if (tid == 0) s.n_chosen = 0;
+    __syncthreads();
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
+    for (int g = 0; g < kSub; ++g) {
       if (g >= sub) break;
-      uint32_t who = __ballot_sync(0xffffffffu, logit_key(top[g]) >= least);
-      while (who) {
-        const int t0 = (tid & ~31) + __ffs(who) - 1;
-        who &= who - 1;
-        for (int q = lane;; q += 32) {
-          const int i = part.lo + t0 + (g * per + q % per) * kRowThreads + (q / per) * 4 * kRowThreads;
-          if (part.lo + t0 + (q / per) * 4 * kRowThreads >= part.hi) break;
-          if (i >= part.hi) continue;
-          float x[VE];
-          RowOf<E>::unpack(part.load(i), x);
+      const bool yes = logit_key(top[g]) >= least;
+      if (SUMS) {
+        all += sum[g];
+        if (!yes) tail += sum[g];
+      }
+      const uint32_t who = __ballot_sync(0xffffffffu, yes);
+      if (who == 0) continue;
+      uint32_t at = 0;
+      if (lane == 0) at = atomicAdd(&s.n_chosen, (uint32_t)__popc(who));
+      at = __shfl_sync(0xffffffffu, at, 0);
+      if (yes) s.chosen[at + __popc(who & ((1u << lane) - 1))] = (uint16_t)(g * kRowThreads + tid);
+    }
+    if (SUMS) {
+      const float f = ref > -INFINITY ? ex2_approx((ref - largest) * c) : 0.f;
+      tail *= f;
+      all *= f;
+    }
+    __syncthreads();
+    auto look = [&](const uint4& v, int piece) {
+      if (!SUMS && !(logit_key(RowOf<E>::largest(v)) >= least)) return;
+      float x[VE];
+      RowOf<E>::unpack(v, x);
 #pragma unroll
-          for (int e = 0; e < VE; ++e) {
-            const uint32_t key = logit_key(x[e]);
-            if (key >= least) put(key, part.id(i, e));
-          }
+      for (int e = 0; e < VE; ++e) {
+        const uint32_t key = logit_key(x[e]);
+        if (key >= least) {
+          const uint32_t at = atomicAdd(&s.n_list, 1u);
+          if (at < kListCap) s.list[at] = comp_of(key, part.id(piece, e));
+        } else if (SUMS) {
+          tail += ex2_approx((x[e] - largest) * c);
         }
       }
+    };
+    const int each = (part.hi - part.lo + kSub * kRowThreads - 1) / (kSub * kRowThreads) * per;   // pieces of a group
+    const int n = (int)s.n_chosen * each;
+    for (int q0 = tid; q0 < n; q0 += 4 * kRowThreads) {
+      uint4 v[4];
+      int piece[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int q = q0 + j * kRowThreads, c = q / each, k = q - c * each;
+        piece[j] = part.hi;
+        if (q < n) {
+          const int who = s.chosen[c];
+          piece[j] = part.lo + who % kRowThreads + ((who / kRowThreads) * per + k % per + (k / per) * kSub) * kRowThreads;
+        }
+        v[j] = part.whole_or_nothing(piece[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) look(v[j], piece[j]);
     }
+    const int edge = part.my_edge();
+    if (edge >= 0 && logit_key(top[0]) >= least) look(part.edge(edge), edge);
+    if (SUMS) {
+      tail = block_add(tail, s.tmpf);
+      all = block_add(all, s.tmpf);
+      if (tid == 0) {
+        st_remote(at_rank(&s.tail[rank], 0), tail);
+        st_remote(at_rank(&s.sums[rank], 0), all);
+      }
+    }
+    hand_over(&s.n_list, s.list, kListCap);
   }
-  DF_DEV void put(uint32_t key, int id) {
-    const uint32_t n = add_remote(at_rank(&s.n_list, 0), 1u);
-    if (n < kListCap) st_remote(at_rank(&s.list[n], 0), comp_of(key, id));
+  // What this CTA has put on its own list goes to the first CTA's (which has put its own there).
+  DF_DEV void hand_over(uint32_t* counter, uint64_t* list, uint32_t room) {
+    if (rank == 0) return;
+    __syncthreads();
+    const uint32_t mine = *counter;
+    if (tid == 0) s.found_n = mine ? add_remote(at_rank(counter, 0), mine) : 0;
+    __syncthreads();
+    const uint32_t at = s.found_n;
+    for (uint32_t i = tid; i < mine && at + i < room; i += kRowThreads) st_remote(at_rank(&list[at + i], 0), list[i]);
+    __syncthreads();
+  }
+  // A token for this CTA's list (hand_over() follows).
+  DF_DEV void put(uint32_t* counter, uint64_t* list, uint32_t room, uint32_t key, int id) {
+    const uint32_t n = atomicAdd(counter, 1u);
+    if (n < room) list[n] = comp_of(key, id);
   }
 
-  // One CTA: the list's first n entries in order.
-  DF_DEV void sort_list(int n) {
+  // One CTA: n entries (at most kListCap) in order.  Few: an entry's place is the number of entries
+  // before it.  Else they are dealt into buckets between the largest and the smallest logit first,
+  // and counted in their bucket alone.
+  __device__ __noinline__ void sort_list(uint64_t* list, int n) {
+    constexpr int OWN = kListCap / kRowThreads;
     if (n <= kRowThreads) {
-      // an entry's place is the number of entries before it; several threads count for one
-      int share = 1;
-      while (share < 32 && n * share * 2 <= kRowThreads) share *= 2;
-      const int e = tid / share, part_of = tid % share;
-      uint64_t mine = 0;
-      uint32_t place = 0;
-      if (e < n) {
-        mine = s.list[e];
-        for (int i = part_of; i < n; i += share) place += s.list[i] > mine;
-      }
-      for (int o = share / 2; o > 0; o >>= 1) place += __shfl_xor_sync(0xffffffffu, place, o);
+      const uint64_t e = tid < n ? list[tid] : 0;
+      int at = 0;
+      if (tid < n)
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) at += list[i] > e;
       __syncthreads();
-      if (e < n && part_of == 0) s.list[place] = mine;
+      if (tid < n) list[at] = e;
       __syncthreads();
       return;
     }
-    for (int i = n + tid; i < kListCap; i += kRowThreads) s.list[i] = 0;
-    const int size = n <= 1024 ? 1024 : kListCap;
+    if (tid == 0) s.key_max = 0, s.key_min = 0xFFFFFFFFu;
+    for (int b = tid; b < kBuckets; b += kRowThreads) s.hist[b] = 0;
     __syncthreads();
-    for (int k = 2; k <= size; k <<= 1)
-      for (int j = k >> 1; j > 0; j >>= 1) {
-        for (int i = tid; i < size / 2; i += kRowThreads) {
-          const int a = 2 * i - (i & (j - 1)), b = a + j;
-          const uint64_t x = s.list[a], y = s.list[b];
-          if ((x < y) == ((a & k) == 0)) {
-            s.list[a] = y;
-            s.list[b] = x;
-          }
-        }
-        __syncthreads();
-      }
+    uint32_t big = 0, small = 0xFFFFFFFFu;
+#pragma unroll 1
+    for (int i = tid; i < n; i += kRowThreads) {
+      const uint32_t key = key_of(list[i]);
+      big = max(big, key);
+      small = min(small, key);
+    }
+    big = __reduce_max_sync(0xffffffffu, big);
+    small = __reduce_min_sync(0xffffffffu, small);
+    if ((tid & 31) == 0) {
+      atomicMax(&s.key_max, big);
+      atomicMin(&s.key_min, small);
+    }
+    __syncthreads();
+    const float bigf = key_float(s.key_max), to = (float)kBuckets / (bigf - key_float(s.key_min));
+    uint64_t e[OWN];
+    uint32_t place[OWN];
+#pragma unroll
+    for (int j = 0; j < OWN; ++j) {
+      const int i = tid + j * kRowThreads;
+      if (i >= n) break;
+      e[j] = list[i];
+      const int b = min((int)((bigf - key_float(key_of(e[j]))) * to), kBuckets - 1);   // NaN: 0
+      place[j] = ((uint32_t)b << 16) | atomicAdd(&s.hist[b], 1u);
+    }
+    __syncthreads();
+    constexpr int PER = kBuckets / kRowThreads;
+    uint32_t c[PER], mine = 0, all;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) mine += c[j] = s.hist[tid * PER + j];
+    uint32_t run = block_scan(mine, s.tmp32, &all);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      s.hist[tid * PER + j] = run;
+      run += c[j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < OWN; ++j) {
+      if (tid + j * kRowThreads >= n) break;
+      list[s.hist[place[j] >> 16] + (place[j] & 0xFFFFu)] = e[j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < OWN; ++j) {
+      if (tid + j * kRowThreads >= n) break;
+      const uint32_t b = place[j] >> 16, from = s.hist[b], upto = b + 1 < kBuckets ? s.hist[b + 1] : (uint32_t)n;
+      uint32_t at = from;
+      for (uint32_t i = from; i < upto; ++i) at += list[i] > e[j];
+      place[j] = at;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < OWN; ++j) {
+      if (tid + j * kRowThreads >= n) break;
+      list[place[j]] = e[j];
+    }
+    __syncthreads();
   }
 
   // One CTA, sorted list of n entries behind n_before tokens of mass_before: the border where the
   // tokens reach want_n or the mass reaches `want`.  False: it is not here; *mass_after: behind the list.
-  DF_DEV bool border_in_list(int n, uint32_t n_before, uint64_t mass_before, bool by_count, uint32_t want_n,
-                             uint64_t want, uint64_t* mass_after, Border* found) {
-    constexpr int PER = kListCap / kRowThreads;
-    uint64_t w[PER], mine = 0, all;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int i = tid * PER + j;
-      w[j] = i < n ? mass_of(scale, kPow2.hi, kPow2.lo, key_float(key_of(s.list[i]))) : 0;
-      mine += w[j];
-    }
+  __device__ __noinline__ bool border_in_list(const uint64_t* list, int n, uint32_t n_before, uint64_t mass_before, bool by_count,
+                             uint32_t want_n, uint64_t want, uint64_t* mass_after, Border* found) {
+    const int per = (n + kRowThreads - 1) / kRowThreads, from = tid * per, upto = min(from + per, n);
+    uint64_t mine = 0, all;
+#pragma unroll 1
+    for (int i = from; i < upto; ++i) mine += mass_of(scale, key_float(key_of(list[i])));
     if (tid == 0) s.found = 0;
     uint64_t run = mass_before + block_scan(mine, s.tmp64, &all);
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
+#pragma unroll 1
+    for (int i = from; i < upto; ++i) {
       const uint64_t before = run;
-      run += w[j];
-      const int i = tid * PER + j;
-      if (i < n && (by_count ? n_before + i + 1 == want_n : before < want && run >= want)) {
-        s.found_comp = s.list[i];
+      run += mass_of(scale, key_float(key_of(list[i])));
+      if (by_count ? n_before + i + 1 == want_n : before < want && run >= want) {
+        s.found_comp = list[i];
         s.found_mass = run;
         s.found_n = n_before + i + 1;
         s.found = 1;
@@ -268,67 +478,94 @@ struct RowWork {
 
   // -------------------------------------------------------------------------- all tokens
   DF_DEV void load_table() {
-    for (int i = tid; i < 1024; i += kRowThreads) {
-      s.t_hi[i] = kPow2.hi[i];
-      s.t_lo[i] = kPow2.lo[i];
-    }
-  }
-  DF_DEV void add(MassSum& m, float l) {
-    add_mass(m, scale, s.t_hi, s.t_lo, l);
-    if (m.n == 512) m.fold();
+    for (int i = tid; i < 1024; i += kRowThreads) s.table[i] = make_float2(kPow2.hi[i], kPow2.lo[i]);
   }
   DF_DEV void give_mass(MassSum& m, uint64_t* to) {   // to the first CTA's
     m.fold();
     const uint64_t sum = block_add(m.sum, s.tmp64);
     if (tid == 0 && sum) add_remote(at_rank(to, 0), sum);
   }
-  DF_DEV uint32_t bin_of(float l) const { return min((scale.top - scale.bits(l)) >> 6, (uint32_t)kBins - 1); }
 
-  // First CTA: running sums of the cluster's histograms; weight(b): about a token's mass in bin b.
+  // All CTAs, behind a row_sync: running sums of the cluster's histograms in the first one's bins.
+  // weight(b, n, places): about the mass of a bin's n tokens.
   template <class W>
-  DF_DEV void run_bins(Bins& to, W&& weight) {
-    constexpr int PER = kBins / kRowThreads;
-    uint32_t c[PER] = {}, n = 0, all_n;
-    float w[PER], mine = 0.f, all;
+  DF_DEV void run_bins(W&& weight) {
+    const int share = kBins / ctas;
+    for (int i = tid; i < share; i += kRowThreads) {
+      const int b = rank * share + i;
+      uint32_t h[8], n = 0, places = 0;
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int b = tid * PER + j;
-      for (int r = 0; r < ctas; ++r) c[j] += ld_remote(at_rank(&s.hist[b], r));
-      w[j] = c[j] ? (float)c[j] * weight(b) : 0.f;
-      n += c[j];
-      mine += w[j];
+      for (int r = 0; r < 8; ++r) h[r] = r >= ctas ? 0 : ctas == 1 ? s.hist[b] : ld_remote(at_rank(&s.hist[b], r));
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        n += h[r] & kCountMask;
+        places += h[r] >> 19;
+        if ((h[r] & kCountMask) > 1170) places = 1u << 30;      // their sum does not fit
+      }
+      st_remote(at_rank(&s.bins.count[b], 0), n);
+      st_remote(at_rank(&s.bins.mass[b], 0), n ? weight(b, n, places) : 0.f);
     }
-    uint32_t rn = block_scan(n, s.tmp32, &all_n);
-    float rw = block_scan(mine, s.tmpf, &all);
+    row_sync(ctas);
+    if (rank != 0) return;
+    constexpr int PER = kBins / kRowThreads;
+    uint32_t n = 0, all_n;
+    float m = 0.f, all;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      n += s.bins.count[tid * PER + j];
+      m += s.bins.mass[tid * PER + j];
+    }
+    n = block_scan(n, s.tmp32, &all_n);
+    m = block_scan(m, s.tmpf, &all);
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       const int b = tid * PER + j;
-      rn += c[j]; rw += w[j];
-      to.count[b] = rn;
-      to.mass[b] = rw;
+      s.bins.count[b] = n += s.bins.count[b];
+      s.bins.mass[b] = m += s.bins.mass[b];
     }
     __syncthreads();
   }
+  // Tokens' bins by probability: 1/32 of a power of two; what is added for one (its place in the
+  // bin in eighths goes above the count).
+  static DF_DEV uint32_t bin_of(uint32_t below_top) { return below_top >> 5; }
+  static DF_DEV uint32_t entry_of(uint32_t below_top) { return 1u + ((below_top & 28u) << 17); }
+  static DF_DEV float bin_mass(int b, uint32_t n, uint32_t places) {
+    const float at = places < 1u << 30 ? ((float)places / (float)n + 0.5f) * 0.125f : 0.5f;
+    return (float)n * exp2f(-((float)b + at) * (1.f / 32.f));
+  }
+  bool by_probability;     // the bins are these (else of a range of keys)
 
-  // Sums all masses and counts tokens in bins.  First CTA: *total, *live = tokens above -inf.
-  __device__ __noinline__ void count_all(uint64_t* total, uint32_t* live) {
+  // Counts tokens in bins by probability; SUMS: and sums all masses (first CTA's s.mass).
+  template <bool SUMS>
+  DF_DEV void count_pass() {
     for (int b = tid; b < kBins; b += kRowThreads) s.hist[b] = 0;
-    if (tid == 0) s.mass = 0;
-    load_table();
-    row_sync(ctas);
+    if (SUMS) load_table();
+    __syncthreads();
     MassSum m;
-    for_pieces<4>(part, [&](const float* x, int) {
+    const MassScale c = scale;
+    const RowPart<E> p = part;
+    uint32_t* const hist = s.hist;
+    const float2* const table = s.table;
+    for_pieces<4>(p, [&](const float* x, int, bool) {
+      if (SUMS) m.room(VE);
 #pragma unroll
-      for (int e = 0; e < VE; ++e)
-        if (x[e] > -INFINITY) {
-          add(m, x[e]);
-          atomicAdd(&s.hist[bin_of(x[e])], 1u);
-        }
+      for (int e = 0; e < VE; ++e) {
+        const uint32_t d = c.top - (SUMS ? add_mass(m, c, table, x[e]) : c.bits(x[e]));
+        if (x[e] > -INFINITY) atomicAdd(&hist[bin_of(d)], entry_of(d));
+      }
+      m.n += VE;
     });
-    give_mass(m, &s.mass);
+    if (SUMS) give_mass(m, &s.mass);
+    by_probability = true;
+  }
+  // First CTA: *total, *live = tokens above -inf.
+  __device__ __noinline__ void count_all(uint64_t* total, uint32_t* live) {
+    if (tid == 0) s.mass = 0;
     row_sync(ctas);
+    count_pass<true>();
+    row_sync(ctas);
+    run_bins(bin_mass);
     if (rank == 0) {
-      run_bins(s.bins, [](int b) { return exp2f(-((float)b + 0.5f) * (1.f / 16.f)); });
       *total = s.mass;
       *live = s.bins.count[kBins - 1];
     }
@@ -342,60 +579,76 @@ struct RowWork {
   };
   // First CTA: the bin where the border should be (exactly, for a count), with some around it as
   // far as their tokens fit in the list.  Words 0, 1: first and last bin, 2: their tokens.
-  DF_DEV void choose(const Bins& of, const Window& v, int tries, bool by_count, uint32_t want_n, uint64_t want,
-                     uint32_t* w) {
+  DF_DEV void choose(const Window& v, int tries, bool by_count, uint32_t want_n, uint64_t want,
+                     uint32_t* w, uint32_t room = kListCap, uint32_t around = kAround) {
     constexpr int PER = kBins / kRowThreads;
-    const float e0 = v.first ? of.mass[v.first - 1] : 0.f, e1 = of.mass[v.last];
+    const float e0 = v.first ? s.bins.mass[v.first - 1] : 0.f, e1 = s.bins.mass[v.last];
     const float e = e0 + (float)(want - v.m0) / (float)(v.m1 - v.m0) * (e1 - e0);
     uint32_t at = 0;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       const int b = tid * PER + j;
-      at += by_count ? v.n0 + of.count[b] < want_n : of.mass[b] < e;
+      at += by_count ? v.n0 + s.bins.count[b] < want_n : s.bins.mass[b] < e;
     }
     at = min(max(block_add(at, s.tmp32), v.first), v.last);
     if (!by_count && tries >= 3) at = v.first + (v.last - v.first) / 2;   // the masses mislead
-    const uint32_t upto = of.count[at], before = at ? of.count[at - 1] : 0;
+    const uint32_t upto = s.bins.count[at], before = at ? s.bins.count[at - 1] : 0;
     uint32_t less = 0, more = 0;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-      const uint32_t b = tid * PER + j, c0 = b ? of.count[b - 1] : 0;
-      less += b >= v.first && b < at && before - c0 <= kAround;
-      more += b > at && b <= v.last && of.count[b] - upto <= kAround;
+      const uint32_t b = tid * PER + j, c0 = b ? s.bins.count[b - 1] : 0;
+      less += b >= v.first && b < at && before - c0 <= around;
+      more += b > at && b <= v.last && s.bins.count[b] - upto <= around;
     }
     less = block_add(less, s.tmp32);
     more = block_add(more, s.tmp32);
-    if (by_count || upto - before > kListCap - 2 * kAround) less = more = 0;
+    if (by_count || upto - before > room - 2 * around) less = more = 0;
     w[0] = at - less;
     w[1] = at + more;
-    w[2] = of.count[w[1]] - (w[0] ? of.count[w[0] - 1] : 0);
+    w[2] = s.bins.count[w[1]] - (w[0] ? s.bins.count[w[0] - 1] : 0);
   }
   // All CTAs: mass before the window (s.mass); its tokens on the list if they fit, else their mass
-  // (s.mass_in) and range of keys.  bin(l, key): a logit's bin of this level, above kBins: none.
+  // (s.mass_in) and range of keys.  bin(l, key): a logit's bin of this level, above kBins: none,
+  // not smaller for a smaller logit but above the level.
   template <class B>
   DF_DEV void read_window(B&& bin) {
     const uint32_t b1 = s.word[0], b2 = s.word[1];
     const bool few = s.word[2] <= kListCap;
+    const MassScale c = scale;
+    const RowPart<E> p = part;
+    const float2* const table = s.table;
     MassSum m, in;
     uint32_t kmin = 0xFFFFFFFFu, kmax = 0;
-    for_pieces<4>(part, [&](const float* x, int piece) {
+    for_pieces<4>(p, [&](const float* x, int piece, bool) {
+      float big = x[0];
+#pragma unroll
+      for (int e = 1; e < VE; ++e) big = fmaxf(big, x[e]);
+      const uint32_t first = bin(big, logit_key(big));
+      if (first > b2 && first < kAbove) return;    // all of the piece lies behind the window
+      m.room(VE);
+      in.room(VE);
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
         const uint32_t key = logit_key(x[e]), b = bin(x[e], key);
         if (b > b2) continue;
         if (b < b1) {
-          add(m, x[e]);
+          add_mass(m, c, table, x[e]);
+          ++m.n;
         } else if (few) {
-          put(key, part.id(piece, e));
+          put(&s.n_list, s.list, kListCap, key, p.id(piece, e));
         } else {
-          add(in, x[e]);
+          add_mass(in, c, table, x[e]);
+          ++in.n;
           kmin = min(kmin, key);
           kmax = max(kmax, key);
         }
       }
     });
     give_mass(m, &s.mass);
-    if (few) return;
+    if (few) {
+      hand_over(&s.n_list, s.list, kListCap);
+      return;
+    }
     give_mass(in, &s.mass_in);
     kmin = __reduce_min_sync(0xffffffffu, kmin);
     kmax = __reduce_max_sync(0xffffffffu, kmax);
@@ -410,27 +663,27 @@ struct RowWork {
   // Looks for the border among one level's bins.  `lv`: the level's tokens and masses; on kDeeper
   // those of the bin that holds it (first CTA).
   template <class B>
-  DF_DEV uint32_t search(const Bins& of, Window* lv, bool by_count, uint32_t want_n, uint64_t want, Border* found, B&& bin) {
+  DF_DEV uint32_t search(Window* lv, bool by_count, uint32_t want_n, uint64_t want, Border* found, B&& bin) {
     const uint64_t base = lv->m0;      // mass before the level's bins
     for (int tries = 0; tries < 16; ++tries) {
       uint32_t w[3];
       if (rank == 0) {
-        choose(of, *lv, tries, by_count, want_n, want, w);
+        choose(*lv, tries, by_count, want_n, want, w);
         tell(w, 3);
-        if (tid == 0) { s.mass = s.mass_in = 0; s.n_list = 0; s.key_min = 0xFFFFFFFFu; s.key_max = 0; }
       }
+      if (tid == 0) s.mass = s.mass_in = 0, s.n_list = 0, s.key_min = 0xFFFFFFFFu, s.key_max = 0;
       row_sync(ctas);
       read_window(bin);
       row_sync(ctas);
       if (rank == 0) {
-        const uint32_t n_before = lv->n0 + (w[0] ? of.count[w[0] - 1] : 0);
+        const uint32_t n_before = lv->n0 + (w[0] ? s.bins.count[w[0] - 1] : 0);
         const uint64_t before = base + s.mass;
         uint64_t after = before + s.mass_in;
         uint32_t next = kAgain;
         if (w[2] <= kListCap) {
           const int n = (int)min(s.n_list, (uint32_t)kListCap);
-          sort_list(n);
-          if (border_in_list(n, n_before, before, by_count, want_n, want, &after, found)) next = kFound;
+          sort_list(s.list, n);
+          if (border_in_list(s.list, n, n_before, before, by_count, want_n, want, &after, found)) next = kFound;
         } else if (by_count || (before < want && after >= want)) {
           next = kDeeper;
           *lv = Window{0, kBins - 1, n_before, before, after};
@@ -445,7 +698,7 @@ struct RowWork {
             lv->m0 = after;
           }
         } else if (next == kDeeper) {
-          word[1] = (uint32_t)max(0, 32 - __clz(word[2] - word[3]) - 10);
+          word[1] = (uint32_t)max(0, 32 - __clz(word[2] - word[3]) - kBinBits);
         }
         if (tid < ctas)
           for (int i = 0; i < 4; ++i) st_remote(at_rank(&s.word[3 + i], tid), word[i]);
@@ -461,16 +714,25 @@ struct RowWork {
   __device__ __noinline__ Border locate(bool by_count, uint32_t want_n, uint64_t want, uint64_t total) {
     Border found{0, 0, 0};
     Window lv{0, kBins - 1, 0, 0, total};
-    uint32_t next = search(s.bins, &lv, by_count, want_n, want, &found, [&](float l, uint32_t) {
-      return l > -INFINITY ? bin_of(l) : 0xFFFFFFFFu;
+    const MassScale c = scale;
+    const RowPart<E> p = part;
+    if (!by_probability) {         // the last search left a level's bins
+      row_sync(ctas);
+      count_pass<false>();
+      row_sync(ctas);
+      run_bins(bin_mass);
+    }
+    uint32_t next = search(&lv, by_count, want_n, want, &found, [&](float l, uint32_t) {
+      return l > -INFINITY ? bin_of(c.top - c.bits(l)) : kNone;
     });
-    // Too many tokens in one bin: cut its keys into 1024 bins again, until they fit or one key is left.
+    // Too many tokens in one bin: cut its keys into bins again, until they fit or one key is left.
     for (int level = 0; level < 4 && next == kDeeper; ++level) {
       const uint32_t shift = s.word[4], hi = s.word[5], lo = s.word[6];
       if (hi == lo) break;
+      by_probability = false;
       for (int b = tid; b < kBins; b += kRowThreads) s.hist[b] = 0;
       row_sync(ctas);
-      for_pieces<4>(part, [&](const float* x, int) {
+      for_pieces<4>(p, [&](const float* x, int, bool) {
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
           const uint32_t key = logit_key(x[e]);
@@ -478,13 +740,12 @@ struct RowWork {
         }
       });
       row_sync(ctas);
-      if (rank == 0)
-        run_bins(s.fine, [&](int b) {
-          const uint32_t mid = ((uint32_t)b << shift) + (shift ? 1u << (shift - 1) : 0);
-          return (float)mass_of(scale, kPow2.hi, kPow2.lo, key_float(hi - min(mid, hi - lo)));
-        });
-      next = search(s.fine, &lv, by_count, want_n, want, &found, [&](float, uint32_t key) {
-        return key >= lo && key <= hi ? (hi - key) >> shift : 0xFFFFFFFFu;
+      run_bins([&](int b, uint32_t n, uint32_t) {
+        const uint32_t mid = ((uint32_t)b << shift) + (shift ? 1u << (shift - 1) : 0);
+        return (float)n * (float)mass_of(scale, key_float(hi - min(mid, hi - lo)));
+      });
+      next = search(&lv, by_count, want_n, want, &found, [&](float, uint32_t key) {
+        return key > hi ? kAbove : key >= lo ? (hi - key) >> shift : kNone;
       });
     }
     if (next == kDeeper) one_key(s.word[5], lv, by_count, want_n, want, &found);
@@ -492,10 +753,110 @@ struct RowWork {
     return found;
   }
 
+  // The borders of top-p (p < 1) and of the draw, in one pass over all masses; m_about: about the
+  // row's.  True: *kept and *drawn are right (first CTA); else the row's exact mass is in *total
+  // and bins are counted, for locate().
+  __device__ __noinline__ bool two_borders(float p, float u, uint64_t m_about, uint64_t* total, uint32_t* live, Border* kept,
+                                           Border* drawn) {
+    const MassScale c = scale;
+    const RowPart<E> part_ = part;
+    if (tid == 0) s.mass = s.mass_in = s.mass_2 = 0;
+    load_table();
+    count_pass<false>();
+    row_sync(ctas);
+    run_bins(bin_mass);
+    uint32_t w[6];
+    if (rank == 0) {
+      const Window all{0, kBins - 1, 0, 0, m_about};
+      const uint64_t keep = p < 1.f ? mass_share(p, m_about) : m_about;
+      choose(all, 0, false, 0, keep, w, kHalf, kHalf / 4);
+      choose(all, 0, false, 0, mass_above(u, keep), w + 3, kHalf, kHalf / 4);
+#pragma unroll
+      for (int i = 0; i < 6; i += 3)
+        if (w[i + 2] > kHalf || (i == 0 && p >= 1.f)) w[i] = 1, w[i + 1] = 0;     // not listed
+      tell(w, 6);
+    }
+    if (tid == 0) s.n_list = s.n_list2 = 0;
+    row_sync(ctas);
+    {
+      const uint32_t a1 = s.word[0], a2 = s.word[1], d1 = s.word[3], d2 = s.word[4], last = max(a2, d2);
+      const float2* const table = s.table;
+      MassSum m, ma, md;
+      for_pieces<(VE > 4 ? 2 : 4)>(part_, [&](const float* x, int piece, bool) {
+        uint32_t bin[VE], ta[VE], tb[VE], first = kNone, na = 0, nd = 0;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          bin[e] = bin_of(c.top - mass_terms(c, table, x[e], &ta[e], &tb[e]));
+          first = min(first, bin[e]);
+        }
+        m.room(VE);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) m.a += ta[e], m.b += tb[e];
+        m.n += VE;
+        if (first > last) return;
+        ma.room(VE);
+        md.room(VE);
+        bool in = false;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          const bool ya = bin[e] < a1, yd = bin[e] < d1;
+          ma.a += ya ? ta[e] : 0;
+          ma.b += ya ? tb[e] : 0;
+          na += ya;
+          md.a += yd ? ta[e] : 0;
+          md.b += yd ? tb[e] : 0;
+          nd += yd;
+          in |= (!ya && bin[e] <= a2) || (!yd && bin[e] <= d2);
+        }
+        ma.n += na;
+        md.n += nd;
+        if (in)
+#pragma unroll
+          for (int e = 0; e < VE; ++e)
+            if (x[e] > -INFINITY) {
+              if (bin[e] >= a1 && bin[e] <= a2) put(&s.n_list, s.list, kHalf, logit_key(x[e]), part_.id(piece, e));
+              if (bin[e] >= d1 && bin[e] <= d2) put(&s.n_list2, s.list + kHalf, kHalf, logit_key(x[e]), part_.id(piece, e));
+            }
+      });
+      give_mass(m, &s.mass);
+      give_mass(ma, &s.mass_in);
+      give_mass(md, &s.mass_2);
+      hand_over(&s.n_list, s.list, kHalf);
+      hand_over(&s.n_list2, s.list + kHalf, kHalf);
+    }
+    row_sync(ctas);
+    uint32_t ok = 0;
+    if (rank == 0) {
+      const uint64_t m = s.mass, before_a = s.mass_in, before_d = s.mass_2;
+      *total = m;
+      *live = s.bins.count[kBins - 1];
+      *kept = Border{0, m, *live};
+      uint64_t after;
+      bool yes = true;
+      if (p < 1.f) {
+        const int n = (int)min(s.n_list, (uint32_t)kHalf);
+        yes = w[0] <= w[1];
+        if (yes) {
+          sort_list(s.list, n);
+          yes = border_in_list(s.list, n, w[0] ? s.bins.count[w[0] - 1] : 0, before_a, false, 0, mass_share(p, m), &after, kept);
+        }
+      }
+      if (yes && w[3] <= w[4]) {
+        const int n = (int)min(s.n_list2, (uint32_t)kHalf);
+        sort_list(s.list + kHalf, n);
+        ok = border_in_list(s.list + kHalf, n, w[3] ? s.bins.count[w[3] - 1] : 0, before_d, false, 0,
+                            mass_above(u, kept->mass), &after, drawn);
+      }
+      if (tid < ctas) st_remote(at_rank(&s.word[7], tid), ok);
+    }
+    row_sync(ctas);
+    return s.word[7] != 0;
+  }
+
   // All tokens of the bin have one key: in order of their ids.
   DF_DEV void one_key(uint32_t key, const Window& lv, bool by_count, uint32_t want_n, uint64_t want, Border* found) {
     uint32_t mine = 0;
-    for_pieces<4>(part, [&](const float* x, int) {
+    for_pieces<4>(part, [&](const float* x, int, bool) {
 #pragma unroll
       for (int e = 0; e < VE; ++e) mine += logit_key(x[e]) == key;
     });
@@ -503,7 +864,7 @@ struct RowWork {
     if (tid == 0) st_remote(at_rank(&s.equal[rank], 0), mine);
     row_sync(ctas);
     if (rank == 0) {
-      const uint64_t w = mass_of(scale, kPow2.hi, kPow2.lo, key_float(key));
+      const uint64_t w = mass_of(scale, key_float(key));
       uint64_t r = by_count ? want_n - lv.n0 : w ? (want - lv.m0 + w - 1) / w : 1;
       uint32_t all = 0;
       for (int i = 0; i < ctas; ++i) all += s.equal[i];
@@ -518,10 +879,10 @@ struct RowWork {
     row_sync(ctas);
     if ((uint32_t)rank == s.word[0]) {
       uint32_t left = s.word[1];
-      for (int i0 = part.lo; i0 < part.hi; i0 += kRowThreads) {
+      for (int i0 = part.begin; i0 < part.end; i0 += kRowThreads) {
         const int i = i0 + tid;
         float x[VE];
-        RowOf<E>::unpack(i < part.hi ? part.load(i) : RowPart<E>::nothing(), x);
+        RowOf<E>::unpack(i < part.end ? part.load(i) : part.whole_or_nothing(part.hi), x);
         uint32_t c = 0, all;
 #pragma unroll
         for (int e = 0; e < VE; ++e) c += logit_key(x[e]) == key;
@@ -552,31 +913,8 @@ DF_DEV float least_logit(float largest, float T, float min_p, float* tmp) {
   __syncthreads();
   return *tmp;
 }
-// f * m for f = 0 .. 1, rounded down; *more: it was not a whole number.
-DF_DEV uint64_t part_of(float f, uint64_t m, bool* more) {
-  const uint32_t b = __float_as_uint(f) & 0x7FFFFFFFu, e = b >> 23;
-  const uint64_t mant = e ? (b & 0x7FFFFFu) | 0x800000u : b;
-  const int shift = 150 - (int)max(e, 1u);                     // f = mant / 2^shift
-  const uint64_t lo = m * mant, hi = __umul64hi(m, mant);      // hi < 2^24
-  if (shift >= 64) {
-    const int s = shift - 64;
-    *more = lo != 0 || (s < 64 && (hi & ((1ull << s) - 1)) != 0) || (s >= 64 && hi != 0);
-    return s < 64 ? hi >> s : 0;
-  }
-  *more = (lo & ((1ull << shift) - 1)) != 0;
-  return (hi << (64 - shift)) | (lo >> shift);
-}
-// First mass above u * m, and first mass that reaches p * m.
-DF_DEV uint64_t mass_above(float u, uint64_t m) {
-  bool more;
-  return part_of(u, m, &more) + 1;
-}
-DF_DEV uint64_t mass_share(float p, uint64_t m) {
-  bool more;
-  const uint64_t x = part_of(p, m, &more);
-  return x + more ? x + more : 1;
-}
 DF_DEV float log_share(const MassScale& c, float l, uint64_t w, uint64_t m) {
+  if (w >= m) return 0.f;
   if (2 * w >= m) return log1pf(-((float)(m - w) / (float)m));
   const float x = c.arg(l), t = fmaf(x, c.c_hi, c.shift), g = t - c.shift;
   float r = fmaf(x, c.c_hi, -g);
@@ -586,46 +924,186 @@ DF_DEV float log_share(const MassScale& c, float l, uint64_t w, uint64_t m) {
   return 0.693147180559945f * (y - log2f((float)m * kMassUnit));
 }
 
-// grid: rows x CTAs of a row.  Bound by the row's bytes where the few-token way decides.
+// The first CTA's end of a row whose first n tokens are on the list, in order.  whole: the kept
+// tokens are among them, all that top-k or min-p left; else the others have about the mass `tail`
+// (within 2^-15 of it) and the row has `live` tokens.  True: done; *about: about the row's mass.
+template <class E, class Give>
+DF_DEV bool finish(RowWork<E>& w, int n, bool whole, uint64_t tail, uint32_t live, float p, uint32_t key_low, float u,
+                   bool log, uint64_t* about, Give&& give) {
+  Shared& s = w.s;
+  const int per = (n + kRowThreads - 1) / kRowThreads, from = w.tid * per, upto = min(from + per, n);
+  uint64_t mine = 0, total;
+#pragma unroll 1
+  for (int i = from; i < upto; ++i) mine += s.each_mass[i] = mass_of(w.scale, key_float(key_of(s.list[i])));
+  const uint64_t start = block_scan(mine, s.tmp64, &total);
+  uint64_t m_lo = total, m_hi = total;
+  if (!whole) {
+    m_lo += tail - (tail >> 15);
+    m_hi += tail + (tail >> 15);
+    *about = total + tail;
+  }
+  uint32_t n_kept = whole ? n : live;
+  int room = n;                      // listed tokens that may be drawn
+  if (p < 1.f || key_low) {
+    const uint64_t share_lo = p < 1.f ? mass_share(p, m_lo) : ~0ull, share_hi = p < 1.f ? mass_share(p, m_hi) : ~0ull;
+    uint32_t c = 0;                  // tokens kept at either end of the interval
+    uint64_t before = start;
+    mine = 0;
+#pragma unroll 1
+    for (int i = from; i < upto; ++i) {
+      if (key_of(s.list[i]) >= key_low) {
+        c += (before < share_lo) + ((before < share_hi) << 16);
+        if (before < share_lo) mine += s.each_mass[i];
+      }
+      before += s.each_mass[i];
+    }
+    c = block_add(c, s.tmp32);
+    n_kept = room = c & 0xFFFF;
+    if (!whole && (room != (int)(c >> 16) || room == n)) return false;
+    m_lo = m_hi = block_add(mine, s.tmp64);
+  }
+  const uint64_t want_lo = mass_above(u, m_lo), want_hi = mass_above(u, m_hi);
+  if (w.tid == 0) s.found = 0;
+  __syncthreads();
+  uint64_t at = start;
+#pragma unroll 1
+  for (int i = from; i < min(upto, room); ++i) {
+    const uint64_t before = at, m = s.each_mass[i];
+    at += m;
+    if (before < want_lo && at >= want_hi) {
+      const uint64_t comp = s.list[i];
+      give(id_of(comp), log ? log_share(w.scale, key_float(key_of(comp)), m, (m_lo >> 1) + (m_hi >> 1)) : 0.f, (int32_t)n_kept);
+      s.found = 1;
+    }
+  }
+  __syncthreads();
+  return s.found != 0;
+}
+
+// A row's settings.
+struct Settings {
+  float T, p, low, u;
+  int k;
+  bool ok, by_k, by_min, by_mass;
+
+  DF_DEV Settings(const SampleArgs& a, int r) {
+    const int g = r / a.group;
+    T = a.temperature ? a.temperature[g] : 1.f;
+    k = a.top_k ? a.top_k[g] : 0;
+    p = a.top_p ? a.top_p[g] : 1.f;
+    low = a.min_p ? a.min_p[g] : 0.f;
+    u = a.u[r];
+    ok = T >= 0.f && T <= 0x1p100f && p > 0.f && p <= 1.f && low >= 0.f && low <= 1.f && u >= 0.f && u < 1.f;
+    if (T < 0x1p-126f) {   // the first token
+      T = 1.f;
+      k = 1;
+    }
+    // what the list of the first tokens is for: top-k, min-p alone, or mass (which may need more)
+    by_k = k > 0 && k <= kMaxTop;
+    by_min = k <= 0 && p >= 1.f && low > 0.f;
+    by_mass = k <= 0 && !by_min;
+  }
+};
+
+DF_DEV void give_row(const SampleArgs& a, int r, int32_t token, float lp, int32_t n) {
+  a.token[r] = token;
+  if (a.logprob) a.logprob[r] = lp;
+  if (a.n_kept) a.n_kept[r] = n;
+}
+
+// A row whose kept tokens the list does not hold, or whose borders the sums do not decide.  w.scale
+// is set; about: about the row's mass, 0: not known.
 template <class E>
-__global__ void __launch_bounds__(kRowThreads) sample_kernel(SampleArgs a, int ctas) {
+__device__ __noinline__ void search_row(RowWork<E>& w, const SampleArgs& a, int r, const Settings& st, uint32_t key_low,
+                                        uint64_t about) {
+  Shared& s = w.s;
+  uint64_t total = 0;
+  uint32_t live = 0;
+  Border kept{0, 0, 0}, drawn{0, 0, 0};
+  bool done = false;
+  if (about && st.by_mass && st.low == 0.f)
+    done = w.two_borders(st.p, st.u, about, &total, &live, &kept, &drawn);
+  else
+    w.count_all(&total, &live);
+  if (!done) {
+    kept = Border{0, total, live};
+    if (st.k > 0) {
+      const Border b = w.locate(true, min((uint32_t)st.k, live), 0, total);
+      if (w.rank == 0) kept = b;
+    }
+    if (st.p < 1.f) {
+      const Border b = w.locate(false, 0, mass_share(st.p, kept.mass), total);
+      if (w.rank == 0 && b.n < kept.n) kept = b;
+    }
+    if (st.low > 0.f) {
+      const float from = key_float(key_low);
+      if (w.tid == 0) s.mass = 0, s.n_list = 0;
+      row_sync(w.ctas);
+      MassSum m;
+      uint32_t n = 0;
+      const MassScale sc = w.scale;
+      const float2* const table = s.table;
+      for_pieces<4>(w.part, [&](const float* x, int, bool) {
+        m.room(RowPart<E>::VE);
+#pragma unroll
+        for (int e = 0; e < RowPart<E>::VE; ++e)
+          if (x[e] >= from) {
+            add_mass(m, sc, table, x[e]);
+            ++m.n;
+            ++n;
+          }
+      });
+      w.give_mass(m, &s.mass);
+      n = block_add(n, s.tmp32);
+      if (w.tid == 0) add_remote(at_rank(&s.n_list, 0), n);
+      row_sync(w.ctas);
+      if (w.rank == 0 && s.n_list < kept.n) kept = Border{0, s.mass, s.n_list};
+    }
+    drawn = w.locate(false, 0, mass_above(st.u, kept.mass), total);
+  }
+  if (w.rank == 0 && w.tid == 0) {
+    const float l = key_float(key_of(drawn.comp));
+    give_row(a, r, id_of(drawn.comp), log_share(w.scale, l, mass_of(w.scale, l), kept.mass), (int32_t)kept.n);
+  }
+}
+
+// grid: rows x CTAs of a row.  SEARCH: rows that need it are searched here, else left to
+// search_kernel (a.left).
+template <class E, bool SEARCH>
+__global__ void __launch_bounds__(kRowThreads, 4) sample_kernel(SampleArgs a, int ctas) {
   extern __shared__ __align__(16) unsigned char smem[];
   Shared& s = *reinterpret_cast<Shared*>(smem);
   pdl_wait();
   pdl_trigger();
   const int rank = ctas == 1 ? 0 : (int)cluster_rank(), tid = threadIdx.x;
   const int r = blockIdx.x / ctas;
-  const RowPart<E> part(static_cast<const E*>(a.x.data), a.x.ld, r, a.x.V, rank, ctas);
-  RowWork<E> w(s, part, rank, ctas);
-  const int g = r / a.group;
-  float T = a.temperature ? a.temperature[g] : 1.f;
-  int k = a.top_k ? a.top_k[g] : 0;
-  const float p = a.top_p ? a.top_p[g] : 1.f, low = a.min_p ? a.min_p[g] : 0.f, u = a.u[r];
-  auto give = [&](int32_t token, float lp, int32_t n) {
-    a.token[r] = token;
-    if (a.logprob) a.logprob[r] = lp;
-    if (a.n_kept) a.n_kept[r] = n;
+  const Settings st(a, r);
+  auto leave = [&](uint64_t about, uint32_t largest, uint32_t on) {
+    if (!SEARCH) a.left[r] = SampleLeft{about, largest, on};
   };
-  // the row's settings: the same in every CTA, so all of them leave together
-  if (!(T >= 0.f && T <= 0x1p100f) || !(p > 0.f && p <= 1.f) || !(low >= 0.f && low <= 1.f) || !(u >= 0.f && u < 1.f)) {
+  if (!st.ok) {          // the same in every CTA, so all of them leave together
     if (rank == 0 && tid == 0) {
       set_status(a.status, DF_ERR_ARG, r);
-      give(-1, -INFINITY, 0);
+      give_row(a, r, -1, -INFINITY, 0);
+      leave(0, 0, 0);
     }
     return;
   }
-  if (T < 0x1p-126f) {   // the first token
-    T = 1.f;
-    k = 1;
-  }
-  const bool few = k > 0 && k <= kMaxTop;
-  if (tid == 0) s.n_list = 0;
+  const RowPart<E> part(static_cast<const E*>(a.x.data), a.x.ld, r, a.x.V, rank, ctas);
+  RowWork<E> w(s, part, rank, ctas);
+  const bool count = st.by_mass && st.p >= 1.f && a.n_kept;
+  if (tid == 0) s.n_list = s.live = 0;
   if (ctas > 1) row_sync(ctas);   // every CTA of the cluster runs before its memory is written
-  w.template read_tops<false>(0.f, nullptr, nullptr);
+  const float c = 1.44269504f / st.T;
+  uint32_t live = 0;
+  if (st.by_mass)
+    w.template read_tops<true>(c, count, &live);
+  else
+    w.template read_tops<false>(0.f, false, nullptr);
   row_sync(ctas);
   if (rank == 0) {
     uint32_t big;
-    const uint32_t least = w.threshold(few ? k : 1, &big);
+    const uint32_t least = w.threshold(st.by_k ? st.k : st.by_mass ? kLikely : 1, &big);
     const uint32_t word[2] = {big, least};
     w.tell(word, 2);
   }
@@ -634,111 +1112,95 @@ __global__ void __launch_bounds__(kRowThreads) sample_kernel(SampleArgs a, int c
   if (big <= kNegInfKey || big >= kPosInfKey) {   // nothing to draw from; a NaN or +inf
     if (rank == 0 && tid == 0) {
       if (big >= kPosInfKey) set_status(a.status, DF_ERR_NAN, r);
-      give(-1, -INFINITY, 0);
+      give_row(a, r, -1, -INFINITY, 0);
+      leave(0, 0, 0);
     }
     return;
   }
   const float largest = key_float(big);
-  w.scale.set(T, largest);
-  if (few) {
-    w.list_tops(least);
-    row_sync(ctas);
-    const uint32_t n_list = ctas == 1 ? s.n_list : ld_remote(at_rank(&s.n_list, 0));
-    if (ctas > 1) cluster_arrive();
-    if (n_list <= kListCap) {
-      if (rank == 0) {
-        w.sort_list((int)n_list);
-        const int n_k = min(k, (int)n_list);
-        constexpr int PER = kMaxTop / kRowThreads;
-        uint64_t m[PER], mine = 0, total;
-        uint32_t key[PER];
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-          const int i = tid * PER + j;
-          key[j] = i < n_k ? key_of(s.list[i]) : 0;
-          m[j] = i < n_k ? mass_of(w.scale, kPow2.hi, kPow2.lo, key_float(key[j])) : 0;
-          mine += m[j];
-        }
-        const uint64_t run = block_scan(mine, s.tmp64, &total);
-        uint32_t n = (uint32_t)n_k;
-        if (p < 1.f || low > 0.f) {
-          const uint64_t share = p < 1.f ? mass_share(p, total) : total;
-          const uint32_t key_low = low > 0.f ? logit_key(least_logit(largest, T, low, s.tmpf)) : 0;
-          uint32_t c = 0;
-          uint64_t before = run;
-#pragma unroll
-          for (int j = 0; j < PER; ++j) {
-            c += tid * PER + j < n_k && (before < share || p >= 1.f) && key[j] >= key_low;
-            before += m[j];
-          }
-          n = block_add(c, s.tmp32);
-        }
-        mine = 0;
-#pragma unroll
-        for (int j = 0; j < PER; ++j)
-          if (tid * PER + j >= (int)n) m[j] = 0;
-          else mine += m[j];
-        total = block_add(mine, s.tmp64);
-        const uint64_t want = mass_above(u, total);
-        uint64_t at = run;
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-          const uint64_t before = at;
-          at += m[j];
-          if (before < want && at >= want) {
-            const uint64_t comp = s.list[tid * PER + j];
-            give(id_of(comp), a.logprob ? log_share(w.scale, key_float(key[j]), m[j], total) : 0.f, (int32_t)n);
-          }
-        }
-      }
-      if (ctas > 1) cluster_wait();
-      return;
+  w.scale.set(st.T, largest);
+  const uint32_t key_low = st.low > 0.f ? logit_key(least_logit(largest, st.T, st.low, s.tmpf)) : 0;
+  uint64_t about = 0;
+  bool done = false;
+  if (st.k <= kMaxTop) {
+    if (count) {
+      live = block_add(live, s.tmp32);
+      if (tid == 0) add_remote(at_rank(&s.live, 0), live);
     }
-    if (ctas > 1) cluster_wait();
-  }
-  // any number of tokens
-  uint64_t total = 0;
-  uint32_t live = 0;
-  w.count_all(&total, &live);
-  Border top{0, total, live};
-  if (k > 0) {
-    const Border b = w.locate(true, min((uint32_t)k, live), 0, total);
-    if (rank == 0) top = b;
-  }
-  Border kept = top;
-  if (p < 1.f) {
-    const Border b = w.locate(false, 0, mass_share(p, top.mass), total);
-    if (rank == 0 && b.n < kept.n) kept = b;
-  }
-  if (low > 0.f) {
-    const float from = least_logit(largest, T, low, s.tmpf);
-    if (tid == 0) { s.mass = 0; s.n_list = 0; }
+    if (st.by_mass)
+      w.template list_tops<true>(least, largest, c);
+    else
+      w.template list_tops<false>(st.by_min ? key_low : st.p >= 1.f ? max(least, key_low) : least, 0.f, 0.f);
     row_sync(ctas);
-    MassSum m;
-    uint32_t n = 0;
-    for_pieces<4>(part, [&](const float* x, int) {
-#pragma unroll
-      for (int e = 0; e < RowPart<E>::VE; ++e)
-        if (x[e] >= from) {
-          w.add(m, x[e]);
-          ++n;
+    if (rank == 0) {
+      const int n = (int)s.n_list;
+      if (n <= kListCap) {
+        w.sort_list(s.list, n);
+        uint64_t tail = 0;
+        if (st.by_mass) {
+          float t = 0.f;
+          for (int i = 0; i < ctas; ++i) t += s.tail[i];
+          tail = (uint64_t)(t * (float)mass_of(w.scale, largest));
         }
-    });
-    w.give_mass(m, &s.mass);
-    n = block_add(n, s.tmp32);
-    if (tid == 0) add_remote(at_rank(&s.n_list, 0), n);
-    row_sync(ctas);
-    if (rank == 0 && s.n_list < kept.n) kept = Border{0, s.mass, s.n_list};
+        done = finish(w, st.by_k ? min(st.k, n) : n, !st.by_mass, tail, s.live, st.p, key_low, st.u, a.logprob != nullptr, &about,
+                      [&](int32_t token, float lp, int32_t kept) { give_row(a, r, token, lp, kept); });
+      }
+    }
   }
-  const Border b = w.locate(false, 0, mass_above(u, kept.mass), total);
-  if (rank == 0 && tid == 0) {
-    const float l = key_float(key_of(b.comp));
-    give(id_of(b.comp), log_share(w.scale, l, mass_of(w.scale, kPow2.hi, kPow2.lo, l), kept.mass), (int32_t)kept.n);
+  if (!SEARCH) {
+    if (rank == 0 && tid == 0) leave(about, big, !done);
+    return;
   }
+  if (rank == 0 && tid < ctas) {
+    st_remote(at_rank(&s.word[6], tid), (uint32_t)done);
+    st_remote(at_rank(&s.word[5], tid), (uint32_t)(about != 0));
+  }
+  row_sync(ctas);
+  if (s.word[6]) return;
+  search_row(w, a, r, st, key_low, rank == 0 ? about : (uint64_t)s.word[5]);
+}
+
+// grid: clusters that take the rows left by sample_kernel in turn.
+template <class E>
+__global__ void __launch_bounds__(kRowThreads, 4) search_kernel(SampleArgs a, int ctas) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  Shared& s = *reinterpret_cast<Shared*>(smem);
+  pdl_wait();
+  pdl_trigger();
+  const int rank = ctas == 1 ? 0 : (int)cluster_rank(), tid = threadIdx.x;
+  const int me = blockIdx.x / ctas, all = gridDim.x / ctas;
+  int seen = 0;           // rows left so far, modulo the clusters
+  bool first = true;
+  for (int r0 = 0; r0 < a.x.rows; r0 += kRowThreads) {
+    const bool mine = r0 + tid < a.x.rows && a.left[r0 + tid].on;
+    uint32_t n;
+    const uint32_t at = block_scan((uint32_t)mine, s.tmp32, &n);
+    if (n == 0) continue;
+    __syncthreads();
+    if (mine) s.rows[at] = (uint16_t)tid;
+    __syncthreads();
+    for (int i = ((me - seen) % all + all) % all; i < (int)n; i += all) {
+      row_sync(ctas);     // the last row's memory; every CTA of the cluster runs
+      first = false;
+      const int r = r0 + s.rows[i];
+      const SampleLeft left = a.left[r];
+      const Settings st(a, r);
+      const RowPart<E> part(static_cast<const E*>(a.x.data), a.x.ld, r, a.x.V, rank, ctas);
+      RowWork<E> w(s, part, rank, ctas);
+      const float largest = key_float(left.largest);
+      w.scale.set(st.T, largest);
+      const uint32_t key_low = st.low > 0.f ? logit_key(least_logit(largest, st.T, st.low, s.tmpf)) : 0;
+      search_row(w, a, r, st, key_low, left.about);
+      __syncthreads();
+    }
+    seen = (seen + (int)n) % all;
+  }
+  // no CTA leaves while another of its cluster may read its memory
+  if (!first && ctas > 1) row_sync(ctas);
 }
 
 template <class E>
-__global__ void __launch_bounds__(kRowThreads) top_logits_kernel(TopArgs a, int ctas) {
+__global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a, int ctas) {
   extern __shared__ __align__(16) unsigned char smem[];
   Shared& s = *reinterpret_cast<Shared*>(smem);
   pdl_wait();
@@ -757,9 +1219,9 @@ __global__ void __launch_bounds__(kRowThreads) top_logits_kernel(TopArgs a, int 
   };
   if (tid == 0) s.n_list = 0;
   if (ctas > 1) row_sync(ctas);
-  float rm, rs;
+  uint32_t live;
   const float c = 1.44269504f / a.temperature;
-  w.template read_tops<true>(c, &rm, &rs);
+  w.template read_tops<true>(c, false, &live);
   row_sync(ctas);
   if (rank == 0) {
     uint32_t big;
@@ -780,49 +1242,67 @@ __global__ void __launch_bounds__(kRowThreads) top_logits_kernel(TopArgs a, int 
     return;
   }
   const float largest = key_float(big);
-  // the CTA's share of the log-sum, to the first CTA
-  {
-    const float sum = block_add(rm > -INFINITY ? rs * ex2_approx((rm - largest) * c) : 0.f, s.tmpf);
-    if (tid == 0) st_remote(at_rank(&s.hist[rank], 0), sum);
-  }
-  w.list_tops(least);
+  w.template list_tops<true>(least, largest, c);
   row_sync(ctas);
-  if (rank == 0 && tid == 0 && a.lse) {
-    float sum = 0.f;
-    for (int i = 0; i < ctas; ++i) sum += __uint_as_float(s.hist[i]);
-    a.lse[r] = largest / a.temperature + logf(sum);
-  }
-  const uint32_t n_list = ctas == 1 ? s.n_list : ld_remote(at_rank(&s.n_list, 0));
-  int n_have = (int)min(n_list, (uint32_t)kListCap);
-  if (n_list > kListCap) {   // many equal logits: the K-th token's place decides
-    row_sync(ctas);
-    w.scale.set(1.f, largest);
-    uint64_t total = 0;
-    uint32_t live = 0;
-    w.count_all(&total, &live);
-    const Border b = w.locate(true, min((uint32_t)K, live), 0, total);
-    if (rank == 0) {
-      const uint32_t word[2] = {(uint32_t)(b.comp >> 32), (uint32_t)b.comp};
-      w.tell(word, 2);
-      if (tid == 0) s.n_list = 0;
-    }
-    row_sync(ctas);
-    const uint64_t last = ((uint64_t)s.word[0] << 32) | s.word[1];
-    for_pieces<4>(part, [&](const float* x, int piece) {
-#pragma unroll
-      for (int e = 0; e < RowPart<E>::VE; ++e) {
-        const uint32_t key = logit_key(x[e]);
-        if (comp_of(key, part.id(piece, e)) >= last) w.put(key, part.id(piece, e));
-      }
-    });
-    row_sync(ctas);
-    n_have = (int)min(s.n_list, (uint32_t)kListCap);   // of the first CTA
-  } else if (ctas > 1) {
+  uint32_t n_list = s.n_list;
+  if (ctas > 1) {
+    n_list = ld_remote(at_rank(&s.n_list, 0));
     cluster_arrive();
   }
+  if (n_list <= kListCap) {
+    if (rank == 0) {
+      w.sort_list(s.list, (int)n_list);
+      const int n = min(K, (int)n_list);
+      float sum = 0.f;
+      for (int i = tid; i < (int)n_list; i += kRowThreads) {
+        const uint64_t comp = s.list[i];
+        const float l = key_float(key_of(comp));
+        sum += ex2_approx((l - largest) * c);
+        if (i < n) {
+          id[i] = id_of(comp);
+          val[i] = l;
+        }
+      }
+      fill(n);
+      sum = block_add(sum, s.tmpf);
+      if (tid == 0 && a.lse) {
+        for (int i = 0; i < ctas; ++i) sum += s.tail[i];
+        a.lse[r] = largest / a.temperature + logf(sum);
+      }
+    }
+    if (ctas > 1) cluster_wait();
+    return;
+  }
+  // many equal logits: the K-th token's place decides
+  if (rank == 0 && tid == 0 && a.lse) {
+    float sum = 0.f;
+    for (int i = 0; i < ctas; ++i) sum += s.sums[i];
+    a.lse[r] = largest / a.temperature + logf(sum);
+  }
+  if (ctas > 1) cluster_wait();
+  w.scale.set(1.f, largest);
+  uint64_t total = 0;
+  w.count_all(&total, &live);
+  const Border b = w.locate(true, min((uint32_t)K, live), 0, total);
   if (rank == 0) {
-    w.sort_list(n_have);
-    const int n = min(K, n_have);
+    const uint32_t word[2] = {(uint32_t)(b.comp >> 32), (uint32_t)b.comp};
+    w.tell(word, 2);
+  }
+  if (tid == 0) s.n_list = 0;
+  row_sync(ctas);
+  const uint64_t last = ((uint64_t)s.word[0] << 32) | s.word[1];
+  for_pieces<4>(part, [&](const float* x, int piece, bool) {
+#pragma unroll
+    for (int e = 0; e < RowPart<E>::VE; ++e) {
+      const uint32_t key = logit_key(x[e]);
+      if (comp_of(key, part.id(piece, e)) >= last) w.put(&s.n_list, s.list, kListCap, key, part.id(piece, e));
+    }
+  });
+  w.hand_over(&s.n_list, s.list, kListCap);
+  row_sync(ctas);
+  if (rank == 0) {
+    const int n = min(K, (int)min(s.n_list, (uint32_t)kListCap));
+    w.sort_list(s.list, n);
     for (int i = tid; i < n; i += kRowThreads) {
       const uint64_t comp = s.list[i];
       id[i] = id_of(comp);
@@ -830,26 +1310,34 @@ __global__ void __launch_bounds__(kRowThreads) top_logits_kernel(TopArgs a, int 
     }
     fill(n);
   }
-  if (n_list <= kListCap && ctas > 1) cluster_wait();
 }
 
 template <class A, class F>
-int launch_rows(F f32, F b16, const A& a, const df_rows& x, const char* tag, cudaStream_t st) {
-  const int ctas = row_ctas(x.rows, x.V);
-  F f = x.dtype == DF_F32 ? f32 : b16;
-  if (ensure_dynamic_smem(f, sizeof(Shared)) != cudaSuccess) return DF_ERR_CUDA;
+int launch_rows(F f, const A& a, int clusters, int ctas, const char* tag, cudaStream_t st) {
+  if (ensure_dynamic_smem(f, sizeof(Shared)) != cudaSuccess || prefer_shared(f) != cudaSuccess) return DF_ERR_CUDA;
   DF_TRACE(tag, st);
-  if (launch_cluster(f, (unsigned)x.rows * ctas, ctas, sizeof(Shared), st, a, ctas) != cudaSuccess) return DF_ERR_CUDA;
+  if (launch_cluster(f, (unsigned)clusters * ctas, ctas, sizeof(Shared), st, a, ctas) != cudaSuccess) return DF_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? DF_OK : DF_ERR_CUDA;
 }
 
 }  // namespace
 
 int launch_sample(const SampleArgs& a, cudaStream_t st) {
-  return launch_rows(sample_kernel<float>, sample_kernel<uint16_t>, a, a.x, "sample", st);
+  const int rows = a.x.rows, ctas = row_ctas(rows, a.x.V);
+  const bool f32 = a.x.dtype == DF_F32;
+  // Few rows have all the CTAs that a search wants from the start; among many, rows to be searched
+  // get them from a second launch.
+  const int most = row_ctas(1, a.x.V);
+  if (ctas == most)
+    return launch_rows(f32 ? sample_kernel<float, true> : sample_kernel<uint16_t, true>, a, rows, ctas, "sample", st);
+  const int rc = launch_rows(f32 ? sample_kernel<float, false> : sample_kernel<uint16_t, false>, a, rows, ctas, "sample", st);
+  if (rc != DF_OK) return rc;
+  return launch_rows(f32 ? search_kernel<float> : search_kernel<uint16_t>, a, std::min(rows, 4 * num_sms() / most), most,
+                     "sample_search", st);
 }
 int launch_top_logits(const TopArgs& a, cudaStream_t st) {
-  return launch_rows(top_logits_kernel<float>, top_logits_kernel<uint16_t>, a, a.x, "top_logits", st);
+  return launch_rows(a.x.dtype == DF_F32 ? top_logits_kernel<float> : top_logits_kernel<uint16_t>, a, a.x.rows,
+                     row_ctas(a.x.rows, a.x.V), "top_logits", st);
 }
 
 int row_ctas(int rows, int V) {

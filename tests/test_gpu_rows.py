@@ -2,7 +2,8 @@
 
 Whole numbers (tokens, counts, ids) have to be the oracle's: a border is missed where two masses that it compares lie
 within 2^-34 of each other, about once in 10^7 rows here.  Tolerances of the rest:
-  logprob   log1p(x) with x off by 3 * 2^-24 of itself, or a difference of log2's: 2^-24 (4 |lp| + 24) + 2^-23
+  logprob   log1p(x) with x off by 3 * 2^-24 of itself, or a difference of log2's: 2^-24 (4 |lp| + 24) + 2^-23; where
+            nothing is cut the mass of the tokens behind the list is an fp32 sum: the lse's bound on top of it
   lse       a term is off by 2^-22 (ex2.approx) and by its exponent's rounding, 2^-23 |y| at a weight of 2^-y (|y| 2^-y <
             0.54); a thread adds up to V / 512 terms one after the other, then 2^5 sums: 2^-24 (V / 512 + 48) in all,
             and the result is rounded (2^-23 of it)
@@ -79,7 +80,9 @@ def check_sample(x, u, settings=None, group=1):
         if token < 0:
             assert got[1][r] == -INF
         else:
-            assert abs(got[1][r] - lp) <= 2.0 ** -24 * (4 * abs(lp) + 24) + 2.0 ** -23, (r, s, got[1][r], lp)
+            open_ = s[1] <= 0 and p == 1 and low == 0
+            assert abs(got[1][r] - lp) <= 2.0 ** -24 * (4 * abs(lp) + 24) + 2.0 ** -23 + open_ * lse_tol(0, rows.shape[1]), \
+                (r, s, got[1][r], lp)
     assert got[3] == 0
     return got
 
@@ -106,7 +109,7 @@ def test_sample_does_not_depend_on_how_many_ctas_share_a_row(rows):
     s = [SETTINGS[2], SETTINGS[3], SETTINGS[7], SETTINGS[8]] * 5
     got = check_sample(x, u, (s * (rows // 20 + 1))[:rows], 1)
     for r in range(20, rows):
-        assert all(got[i][r] == got[i][r % 20] for i in range(3))
+        assert all(got[i][r] == got[i][r % 20] for i in (0, 2))
 
 
 @pytest.mark.parametrize("kind", ["constant", "two", "whole", "flat", "steps"])
@@ -198,7 +201,7 @@ def test_sample_optional_outputs_and_empty_call():
 
 def test_sample_captured_and_on_another_stream():
     x, u = held(logits(6, 32, 50000), "bf16"), f32(np.random.default_rng(1).random(32))
-    ws, token = _lib.Workspace(256), i32([0] * 32)
+    ws, token = _lib.Workspace(_lib.sample_workspace_size(32, 50000)), i32([0] * 32)
     T, p = f32([0.9]), f32([0.9])
     call = lambda: _lib.sample(x, u, token, ws, temperature=T, top_p=p, group=32)  # noqa: E731
     call()
@@ -499,7 +502,7 @@ def test_draw_then_teach():
     token, _, _, _ = run_sample(x, np.random.default_rng(2).random(T), [(0.6, 20, 0.95, 0.0)], T)
     ids = torch.zeros(T, K, dtype=torch.int32, device=DEV)
     vals, lse = torch.zeros(T, K, device=DEV), torch.zeros(T, device=DEV)
-    ws = _lib.Workspace(256)
+    ws = _lib.Workspace(_lib.distill_workspace_size(T, V))
     _lib.top_logits(x, 1.0, ids, vals, lse, ws)
     assert all(token[r] in ids[r].tolist() for r in range(T))
     path = [0, 4, 9, 30]

@@ -12,22 +12,22 @@ def rows(data=A, dtype=0, n=4, V=100, ld=None):
     return _lib.RowsStruct(data, dtype, n, V, V if ld is None else ld)
 
 
-def sample(x=None, group=1, u=A, token=A, ws=A, ws_bytes=256):
+def sample(x=None, group=1, u=A, token=A, ws=A, ws_bytes=512):
     x = rows() if x is None else x
     return _lib.load().dflash_sample(C.addressof(x), group, None, None, None, None, u, token, None, None, ws, ws_bytes, None)
 
 
-def top(x=None, K=5, T=1.0, id=A, val=A, ws=A, ws_bytes=256):
+def top(x=None, K=5, T=1.0, id=A, val=A, ws=A, ws_bytes=512):
     x = rows() if x is None else x
     return _lib.load().dflash_top_logits(C.addressof(x), K, T, id, val, None, ws, ws_bytes, None)
 
 
-def distill(x=None, K=5, lists=4, id=A, val=A, row=None, T=1.0, loss=A, stats=A, grad=None, ld=100, ws=A, ws_bytes=256):
+def distill(x=None, K=5, lists=4, id=A, val=A, row=None, T=1.0, loss=A, stats=A, grad=None, ld=100, ws=A, ws_bytes=512):
     x = rows() if x is None else x
     return _lib.load().dflash_distill(C.addressof(x), K, lists, id, val, None, row, T, None, loss, stats, grad, ld, ws, ws_bytes, None)
 
 
-def backward(x=None, K=5, lists=4, id=A, val=A, row=None, T=1.0, stats=A, grad=2 * A, ld=100, ws=A, ws_bytes=256):
+def backward(x=None, K=5, lists=4, id=A, val=A, row=None, T=1.0, stats=A, grad=2 * A, ld=100, ws=A, ws_bytes=512):
     x = rows() if x is None else x
     return _lib.load().dflash_distill_backward(C.addressof(x), K, lists, id, val, None, row, T, None, stats, None, grad, ld, ws, ws_bytes, None)
 
