@@ -30,12 +30,13 @@ namespace {
 constexpr int kListCap = 2048;     // tokens that one CTA sorts
 constexpr int kHalf = kListCap / 2;
 constexpr int kMaxTop = 1024;      // top-k and K that the list of the first tokens is used for
-constexpr int kLikely = 128;       // tokens listed (at least) where mass alone decides
+constexpr int kFewTop = 64;        // up to this many, every CTA finds its own part's first ones
+constexpr int kLikely = 128;       // tokens listed (about) where mass alone decides
 constexpr int kBuckets = 512;      // of threshold() and sort_list()
 constexpr int kBins = 2048;
 constexpr int kBinBits = 11;
 constexpr uint32_t kCountMask = (1u << 19) - 1;   // a bin's tokens; above it the sum of their places in the bin
-constexpr int kSub = 8;            // groups of a thread times CTAs of a row
+constexpr int kSub = 8;            // groups of a thread
 constexpr uint32_t kNone = 1u << 20, kAbove = 1u << 21;   // no bin of a level: below it, above it
 constexpr uint32_t kAround = 512;  // tokens listed on either side of the bin where a border should be
 
@@ -47,7 +48,7 @@ struct Bins {          // running sums over bins: tokens, and about their mass
 };
 struct Shared {
   union {
-    uint32_t group_key[kSub * kRowThreads];  // of the whole row, in the first CTA
+    uint32_t group_key[kSub * kRowThreads];  // of the whole row, in the first CTA (from several CTAs: of larger groups)
     uint64_t list[kListCap];                 // the first CTA's is the row's
   };
   union {
@@ -64,7 +65,8 @@ struct Shared {
   // collected in the first CTA
   uint64_t mass, mass_in, mass_2;
   uint32_t n_list, n_list2, key_min, key_max, equal[8], at_id, live;
-  float tail[8], sums[8];
+  float tail[8], sums[8];                    // of each CTA's part
+  uint32_t part_max[8], part_least[8];
   // one CTA's own
   uint64_t tmp64[kRowWarps];
   uint32_t tmp32[kRowWarps];
@@ -82,13 +84,15 @@ DF_DEV int id_of(uint64_t comp) { return (int)~(uint32_t)comp; }
 struct GlobalTable {
   DF_DEV float2 operator[](uint32_t j) const { return make_float2(kPow2.hi[j], kPow2.lo[j]); }
 };
-DF_DEV uint64_t mass_of(const MassScale& c, float l) {
+template <class Table>
+DF_DEV uint64_t mass_of(const MassScale& c, const Table& table, float l) {
   MassSum m;
-  add_mass(m, c, GlobalTable{}, l);
+  add_mass(m, c, table, l);
   m.n = 1;
   m.fold();
   return m.sum;
 }
+DF_DEV uint64_t mass_of(const MassScale& c, float l) { return mass_of(c, GlobalTable{}, l); }
 
 // A border in the order: its token, the tokens up to it and their mass.
 struct Border {
@@ -200,23 +204,66 @@ struct RowWork {
       m[0] = max_nan(m[0], l);
       if (SUMS) add(&v, 1, l, sum);
     }
-    const int sub = kSub / ctas;
 #pragma unroll
     for (int j = 0; j < kSub; ++j) top[j] = m[j];
+    if (SUMS) *live = n_live;
+  }
+  static DF_DEV uint32_t top_key(float l) { return l == l ? logit_key(l) : 0xFFFFFFFFu; }
+
+  // The groups' keys to the first CTA, those of several CTAs as the largest of `ctas` groups each.
+  DF_DEV void post_groups() {
+    float m[kSub];
+#pragma unroll
+    for (int j = 0; j < kSub; ++j) m[j] = top[j];
+    const int sub = kSub / ctas;
 #pragma unroll
     for (int n = kSub / 2; n > 0; n >>= 1)
       if (sub <= n)
 #pragma unroll
-        for (int j = 0; j < n; ++j) {
-          top[j] = max_nan(top[2 * j], top[2 * j + 1]);
-          if (SUMS) sum[j] = sum[2 * j] + sum[2 * j + 1];
-        }
+        for (int j = 0; j < n; ++j) m[j] = max_nan(m[2 * j], m[2 * j + 1]);
 #pragma unroll
     for (int g = 0; g < kSub; ++g)
-      if (g < sub)
-        st_remote(at_rank(&s.group_key[(rank * sub + g) * kRowThreads + tid], 0),
-                  top[g] == top[g] ? logit_key(top[g]) : 0xFFFFFFFFu);
-    if (SUMS) *live = n_live;
+      if (g < sub) st_remote(at_rank(&s.group_key[(rank * sub + g) * kRowThreads + tid], 0), top_key(m[g]));
+  }
+
+  // This CTA's largest key (*largest), and a key that at least k of its threads reach, or all that
+  // have a token: the upper 16 bits of the k-th largest of the threads' keys.  Every warp finds it.
+  DF_DEV uint32_t part_threshold(int k, uint32_t* largest) {
+    float m = top[0];
+#pragma unroll
+    for (int j = 1; j < kSub; ++j) m = max_nan(m, top[j]);
+    s.hist[tid] = top_key(m);
+    __syncthreads();
+    uint32_t key[kRowWarps], big = 0, n = 0;
+#pragma unroll
+    for (int j = 0; j < kRowWarps; ++j) {
+      key[j] = s.hist[(tid & 31) + 32 * j];
+      big = max(big, key[j]);
+      n += key[j] > kNegInfKey;
+    }
+    *largest = __reduce_max_sync(0xffffffffu, big);
+    uint32_t least = 0;
+    if ((int)__reduce_add_sync(0xffffffffu, n) >= k)
+#pragma unroll 1
+      for (uint32_t bit = 1u << 31; bit > 1u << 15; bit >>= 1) {
+        uint32_t c = 0;
+#pragma unroll
+        for (int j = 0; j < kRowWarps; ++j) c += key[j] >= (least | bit);
+        if ((int)__reduce_add_sync(0xffffffffu, c) >= k) least |= bit;
+      }
+    return max(least, kNegInfKey + 1);
+  }
+  // Lists what of this CTA's part reaches the key that k of its threads reach.  In the first CTA:
+  // part_max and part_least; with SUMS tail and sums relative to the part's largest logit.
+  template <bool SUMS>
+  DF_DEV void list_part(int k, float c) {
+    uint32_t big;
+    const uint32_t least = part_threshold(k, &big);
+    if (tid == 0) {
+      st_remote(at_rank(&s.part_max[rank], 0), big);
+      st_remote(at_rank(&s.part_least[rank], 0), least);
+    }
+    list_tops<SUMS>(least, key_float(big), c);
   }
 
   // First CTA, behind a row_sync: the largest key, and for k > 1 a key above -inf's that at least k
@@ -278,16 +325,16 @@ struct RowWork {
   // again, by all threads.  Every CTA lists its own and hands them to the first one.  SUMS: the sum
   // of the others, relative to the largest logit, goes to the first CTA's tail: of the groups not
   // read again from the first pass, of those that are from this one, so that no large term that is
-  // on the list has left its rounding there.  Its sums: of all groups.
+  // on the list has left its rounding there.  Its sums: of all groups.  (A group's pieces are
+  // lo + who, lo + who + kSub * kRowThreads, ..., who = the thread + its group * kRowThreads.)
   template <bool SUMS>
   DF_DEV void list_tops(uint32_t least, float largest, float c) {
-    const int lane = tid & 31, sub = kSub / ctas, per = ctas;
+    const int lane = tid & 31;
     float tail = 0.f, all = 0.f;
     if (tid == 0) s.n_chosen = 0;
     __syncthreads();
 #pragma unroll
     for (int g = 0; g < kSub; ++g) {
-      if (g >= sub) break;
       const bool yes = logit_key(top[g]) >= least;
       if (SUMS) {
         all += sum[g];
@@ -321,7 +368,7 @@ struct RowWork {
         }
       }
     };
-    const int each = (part.hi - part.lo + kSub * kRowThreads - 1) / (kSub * kRowThreads) * per;   // pieces of a group
+    const int each = (part.hi - part.lo + kSub * kRowThreads - 1) / (kSub * kRowThreads);   // pieces of a group
     const int n = (int)s.n_chosen * each;
     for (int q0 = tid; q0 < n; q0 += 4 * kRowThreads) {
       uint4 v[4];
@@ -332,7 +379,7 @@ struct RowWork {
         piece[j] = part.hi;
         if (q < n) {
           const int who = s.chosen[c];
-          piece[j] = part.lo + who % kRowThreads + ((who / kRowThreads) * per + k % per + (k / per) * kSub) * kRowThreads;
+          piece[j] = part.lo + who + k * kSub * kRowThreads;
         }
         v[j] = part.whole_or_nothing(piece[j]);
       }
@@ -454,13 +501,13 @@ struct RowWork {
     const int per = (n + kRowThreads - 1) / kRowThreads, from = tid * per, upto = min(from + per, n);
     uint64_t mine = 0, all;
 #pragma unroll 1
-    for (int i = from; i < upto; ++i) mine += mass_of(scale, key_float(key_of(list[i])));
+    for (int i = from; i < upto; ++i) mine += mass_of(scale, s.table, key_float(key_of(list[i])));
     if (tid == 0) s.found = 0;
     uint64_t run = mass_before + block_scan(mine, s.tmp64, &all);
 #pragma unroll 1
     for (int i = from; i < upto; ++i) {
       const uint64_t before = run;
-      run += mass_of(scale, key_float(key_of(list[i])));
+      run += mass_of(scale, s.table, key_float(key_of(list[i])));
       if (by_count ? n_before + i + 1 == want_n : before < want && run >= want) {
         s.found_comp = list[i];
         s.found_mass = run;
@@ -753,13 +800,60 @@ struct RowWork {
     return found;
   }
 
+  // All CTAs: all masses (s.mass) and those before two windows of bins, words 0 and 1 (s.mass_in),
+  // words 3 and 4 (s.mass_2); the windows' tokens on the list's halves.
+  __device__ __noinline__ void sum_and_list() {
+    const MassScale c = scale;
+    const RowPart<E> p = part;
+    const uint32_t a1 = s.word[0], a2 = s.word[1], d1 = s.word[3], d2 = s.word[4], last = max(a2, d2);
+    const float2* const table = s.table;
+    MassSum m, ma, md;
+    for_pieces<2>(p, [&](const float* x, int piece, bool) {
+      float big = x[0];
+#pragma unroll
+      for (int e = 1; e < VE; ++e) big = fmaxf(big, x[e]);
+      m.room(VE);
+      m.n += VE;
+      if (bin_of(c.top - c.bits(big)) > last) {      // the piece lies behind both windows
+#pragma unroll
+        for (int e = 0; e < VE; ++e) add_mass(m, c, table, x[e]);
+        return;
+      }
+      ma.room(VE);
+      md.room(VE);
+      uint32_t in = 0;
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        uint32_t ta, tb;
+        const uint32_t bin = bin_of(c.top - mass_terms(c, table, x[e], &ta, &tb));
+        m.a += ta;
+        m.b += tb;
+        if (bin < a1) ma.a += ta, ma.b += tb, ++ma.n;
+        else if (bin <= a2) in |= 1u << e;
+        if (bin < d1) md.a += ta, md.b += tb, ++md.n;
+        else if (bin <= d2) in |= 256u << e;
+      }
+      if (in)
+#pragma unroll
+        for (int e = 0; e < VE; ++e)
+          if ((in >> e & 257u) && x[e] > -INFINITY) {
+            const uint32_t key = logit_key(x[e]);
+            const int id = p.id(piece, e);
+            if (in >> e & 1u) put(&s.n_list, s.list, kHalf, key, id);
+            if (in >> e & 256u) put(&s.n_list2, s.list + kHalf, kHalf, key, id);
+          }
+    });
+    give_mass(m, &s.mass);
+    give_mass(ma, &s.mass_in);
+    give_mass(md, &s.mass_2);
+    hand_over(&s.n_list, s.list, kHalf);
+    hand_over(&s.n_list2, s.list + kHalf, kHalf);
+  }
   // The borders of top-p (p < 1) and of the draw, in one pass over all masses; m_about: about the
   // row's.  True: *kept and *drawn are right (first CTA); else the row's exact mass is in *total
   // and bins are counted, for locate().
   __device__ __noinline__ bool two_borders(float p, float u, uint64_t m_about, uint64_t* total, uint32_t* live, Border* kept,
                                            Border* drawn) {
-    const MassScale c = scale;
-    const RowPart<E> part_ = part;
     if (tid == 0) s.mass = s.mass_in = s.mass_2 = 0;
     load_table();
     count_pass<false>();
@@ -769,8 +863,8 @@ struct RowWork {
     if (rank == 0) {
       const Window all{0, kBins - 1, 0, 0, m_about};
       const uint64_t keep = p < 1.f ? mass_share(p, m_about) : m_about;
-      choose(all, 0, false, 0, keep, w, kHalf, kHalf / 4);
-      choose(all, 0, false, 0, mass_above(u, keep), w + 3, kHalf, kHalf / 4);
+      choose(all, 0, false, 0, keep, w, kHalf, kHalf / 8);
+      choose(all, 0, false, 0, mass_above(u, keep), w + 3, kHalf, kHalf / 8);
 #pragma unroll
       for (int i = 0; i < 6; i += 3)
         if (w[i + 2] > kHalf || (i == 0 && p >= 1.f)) w[i] = 1, w[i + 1] = 0;     // not listed
@@ -778,52 +872,7 @@ struct RowWork {
     }
     if (tid == 0) s.n_list = s.n_list2 = 0;
     row_sync(ctas);
-    {
-      const uint32_t a1 = s.word[0], a2 = s.word[1], d1 = s.word[3], d2 = s.word[4], last = max(a2, d2);
-      const float2* const table = s.table;
-      MassSum m, ma, md;
-      for_pieces<(VE > 4 ? 2 : 4)>(part_, [&](const float* x, int piece, bool) {
-        uint32_t bin[VE], ta[VE], tb[VE], first = kNone, na = 0, nd = 0;
-#pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          bin[e] = bin_of(c.top - mass_terms(c, table, x[e], &ta[e], &tb[e]));
-          first = min(first, bin[e]);
-        }
-        m.room(VE);
-#pragma unroll
-        for (int e = 0; e < VE; ++e) m.a += ta[e], m.b += tb[e];
-        m.n += VE;
-        if (first > last) return;
-        ma.room(VE);
-        md.room(VE);
-        bool in = false;
-#pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          const bool ya = bin[e] < a1, yd = bin[e] < d1;
-          ma.a += ya ? ta[e] : 0;
-          ma.b += ya ? tb[e] : 0;
-          na += ya;
-          md.a += yd ? ta[e] : 0;
-          md.b += yd ? tb[e] : 0;
-          nd += yd;
-          in |= (!ya && bin[e] <= a2) || (!yd && bin[e] <= d2);
-        }
-        ma.n += na;
-        md.n += nd;
-        if (in)
-#pragma unroll
-          for (int e = 0; e < VE; ++e)
-            if (x[e] > -INFINITY) {
-              if (bin[e] >= a1 && bin[e] <= a2) put(&s.n_list, s.list, kHalf, logit_key(x[e]), part_.id(piece, e));
-              if (bin[e] >= d1 && bin[e] <= d2) put(&s.n_list2, s.list + kHalf, kHalf, logit_key(x[e]), part_.id(piece, e));
-            }
-      });
-      give_mass(m, &s.mass);
-      give_mass(ma, &s.mass_in);
-      give_mass(md, &s.mass_2);
-      hand_over(&s.n_list, s.list, kHalf);
-      hand_over(&s.n_list2, s.list + kHalf, kHalf);
-    }
+    sum_and_list();
     row_sync(ctas);
     uint32_t ok = 0;
     if (rank == 0) {
@@ -980,6 +1029,51 @@ DF_DEV bool finish(RowWork<E>& w, int n, bool whole, uint64_t tail, uint32_t liv
   return s.found != 0;
 }
 
+// The same for at most 64 tokens, by the first warp alone.
+template <class E, class Give>
+DF_DEV bool finish_few(RowWork<E>& w, int n, bool whole, uint64_t tail, uint32_t live, float p, uint32_t key_low, float u,
+                       bool log, uint64_t* about, Give&& give) {
+  Shared& s = w.s;
+  const int lane = w.tid & 31;
+  const uint64_t e0 = 2 * lane < n ? s.list[2 * lane] : 0, e1 = 2 * lane + 1 < n ? s.list[2 * lane + 1] : 0;
+  const uint64_t m0 = 2 * lane < n ? mass_of(w.scale, key_float(key_of(e0))) : 0;
+  const uint64_t m1 = 2 * lane + 1 < n ? mass_of(w.scale, key_float(key_of(e1))) : 0;
+  uint64_t incl = m0 + m1;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  const uint64_t start = incl - m0 - m1, total = __shfl_sync(0xffffffffu, incl, 31);
+  uint64_t m_lo = total, m_hi = total;
+  if (!whole) {
+    m_lo += tail - (tail >> 15);
+    m_hi += tail + (tail >> 15);
+    *about = total + tail;
+  }
+  uint32_t n_kept = whole ? n : live;
+  int room = n;
+  if (p < 1.f || key_low) {
+    const uint64_t share_lo = p < 1.f ? mass_share(p, m_lo) : ~0ull, share_hi = p < 1.f ? mass_share(p, m_hi) : ~0ull;
+    const bool k0 = 2 * lane < n && key_of(e0) >= key_low, k1 = 2 * lane + 1 < n && key_of(e1) >= key_low;
+    const bool y0 = k0 && start < share_lo, y1 = k1 && start + m0 < share_lo;
+    const uint32_t c = (uint32_t)y0 + y1 + (((uint32_t)(k0 && start < share_hi) + (k1 && start + m0 < share_hi)) << 16);
+    const uint32_t both = __reduce_add_sync(0xffffffffu, c);
+    n_kept = room = both & 0xFFFF;
+    if (!whole && (room != (int)(both >> 16) || room == n)) return false;
+    m_lo = m_hi = warp_add((y0 ? m0 : 0) + (y1 ? m1 : 0));
+  }
+  const uint64_t want_lo = mass_above(u, m_lo), want_hi = mass_above(u, m_hi);
+  const bool at0 = 2 * lane < room && start < want_lo && start + m0 >= want_hi;
+  const bool at1 = 2 * lane + 1 < room && start + m0 < want_lo && incl >= want_hi;
+  if (at0 || at1) {
+    const uint64_t comp = at0 ? e0 : e1;
+    give(id_of(comp), log ? log_share(w.scale, key_float(key_of(comp)), at0 ? m0 : m1, (m_lo >> 1) + (m_hi >> 1)) : 0.f,
+         (int32_t)n_kept);
+  }
+  return __any_sync(0xffffffffu, at0 || at1);
+}
+
 // A row's settings.
 struct Settings {
   float T, p, low, u;
@@ -1070,7 +1164,7 @@ __device__ __noinline__ void search_row(RowWork<E>& w, const SampleArgs& a, int 
 // grid: rows x CTAs of a row.  SEARCH: rows that need it are searched here, else left to
 // search_kernel (a.left).
 template <class E, bool SEARCH>
-__global__ void __launch_bounds__(kRowThreads, 4) sample_kernel(SampleArgs a, int ctas) {
+__global__ void __launch_bounds__(kRowThreads, SEARCH ? 2 : 4) sample_kernel(SampleArgs a, int ctas) {
   extern __shared__ __align__(16) unsigned char smem[];
   Shared& s = *reinterpret_cast<Shared*>(smem);
   pdl_wait();
@@ -1092,72 +1186,105 @@ __global__ void __launch_bounds__(kRowThreads, 4) sample_kernel(SampleArgs a, in
   const RowPart<E> part(static_cast<const E*>(a.x.data), a.x.ld, r, a.x.V, rank, ctas);
   RowWork<E> w(s, part, rank, ctas);
   const bool count = st.by_mass && st.p >= 1.f && a.n_kept;
+  // Every CTA finds the first tokens of its own part, if they are few; else the row's are found together.
+  const bool parts = st.by_mass || (st.by_k && st.k <= kFewTop);
   if (tid == 0) s.n_list = s.live = 0;
   if (ctas > 1) row_sync(ctas);   // every CTA of the cluster runs before its memory is written
   const float c = 1.44269504f / st.T;
-  uint32_t live = 0;
-  if (st.by_mass)
+  uint32_t big = 0, key_low = 0;
+  if (st.by_mass) {
+    uint32_t live;
     w.template read_tops<true>(c, count, &live);
-  else
-    w.template read_tops<false>(0.f, false, nullptr);
-  row_sync(ctas);
-  if (rank == 0) {
-    uint32_t big;
-    const uint32_t least = w.threshold(st.by_k ? st.k : st.by_mass ? kLikely : 1, &big);
-    const uint32_t word[2] = {big, least};
-    w.tell(word, 2);
-  }
-  row_sync(ctas);
-  const uint32_t big = s.word[0], least = s.word[1];
-  if (big <= kNegInfKey || big >= kPosInfKey) {   // nothing to draw from; a NaN or +inf
-    if (rank == 0 && tid == 0) {
-      if (big >= kPosInfKey) set_status(a.status, DF_ERR_NAN, r);
-      give_row(a, r, -1, -INFINITY, 0);
-      leave(0, 0, 0);
-    }
-    return;
-  }
-  const float largest = key_float(big);
-  w.scale.set(st.T, largest);
-  const uint32_t key_low = st.low > 0.f ? logit_key(least_logit(largest, st.T, st.low, s.tmpf)) : 0;
-  uint64_t about = 0;
-  bool done = false;
-  if (st.k <= kMaxTop) {
+    w.template list_part<true>(kLikely / ctas + 8, c);
     if (count) {
       live = block_add(live, s.tmp32);
       if (tid == 0) add_remote(at_rank(&s.live, 0), live);
     }
-    if (st.by_mass)
-      w.template list_tops<true>(least, largest, c);
-    else
-      w.template list_tops<false>(st.by_min ? key_low : st.p >= 1.f ? max(least, key_low) : least, 0.f, 0.f);
-    row_sync(ctas);
-    if (rank == 0) {
-      const int n = (int)s.n_list;
-      if (n <= kListCap) {
-        w.sort_list(s.list, n);
-        uint64_t tail = 0;
-        if (st.by_mass) {
-          float t = 0.f;
-          for (int i = 0; i < ctas; ++i) t += s.tail[i];
-          tail = (uint64_t)(t * (float)mass_of(w.scale, largest));
-        }
-        done = finish(w, st.by_k ? min(st.k, n) : n, !st.by_mass, tail, s.live, st.p, key_low, st.u, a.logprob != nullptr, &about,
-                      [&](int32_t token, float lp, int32_t kept) { give_row(a, r, token, lp, kept); });
+  } else {
+    w.template read_tops<false>(0.f, false, nullptr);
+    if (parts) {
+      w.template list_part<false>(st.k, 0.f);
+    } else {
+      w.post_groups();
+      row_sync(ctas);
+      if (rank == 0) {
+        const uint32_t least = w.threshold(st.by_k ? st.k : 1, &big);
+        const uint32_t word[2] = {big, least};
+        w.tell(word, 2);
       }
+      row_sync(ctas);
+      big = s.word[0];
+      uint32_t least = s.word[1];
+      if (big > kNegInfKey && big < kPosInfKey && st.k <= kMaxTop) {
+        if (st.low > 0.f) key_low = logit_key(least_logit(key_float(big), st.T, st.low, s.tmpf));
+        if (st.p >= 1.f) least = st.by_min ? key_low : max(least, key_low);
+        w.template list_tops<false>(least, 0.f, 0.f);
+      }
+    }
+  }
+  row_sync(ctas);
+  uint64_t about = 0;
+  bool done = false;
+  if (rank == 0) {
+    uint32_t cut = 0;              // above it the list is complete
+    if (parts)
+      for (int i = 0; i < ctas; ++i) {
+        big = max(big, s.part_max[i]);
+        cut = max(cut, s.part_least[i]);
+      }
+    if (big <= kNegInfKey || big >= kPosInfKey) {   // nothing to draw from; a NaN or +inf
+      if (tid == 0) {
+        if (big >= kPosInfKey) set_status(a.status, DF_ERR_NAN, r);
+        give_row(a, r, -1, -INFINITY, 0);
+      }
+      done = true;
+    } else if (st.k <= kMaxTop && s.n_list <= kListCap) {
+      const float largest = key_float(big);
+      w.scale.set(st.T, largest);
+      if (st.low > 0.f && !key_low) key_low = logit_key(least_logit(largest, st.T, st.low, s.tmpf));
+      int n = (int)s.n_list;
+      w.sort_list(s.list, n);
+      uint64_t tail = 0;
+      if (st.by_mass) {
+        float t = 0.f;
+        int above = 0;
+        for (int i = tid; i < n; i += kRowThreads) {
+          const uint32_t key = key_of(s.list[i]);
+          if (key >= cut) ++above;
+          else t += ex2_approx((key_float(key) - largest) * c);
+        }
+        n = block_add(above, (int*)s.tmp32);
+        t = block_add(t, s.tmpf);
+        for (int i = 0; i < ctas; ++i)
+          if (s.part_max[i] > kNegInfKey) t += s.tail[i] * ex2_approx((key_float(s.part_max[i]) - largest) * c);
+        tail = (uint64_t)(t * (float)mass_of(w.scale, largest));
+      }
+      if (st.by_k) n = min(st.k, n);
+      auto give = [&](int32_t token, float lp, int32_t kept) { give_row(a, r, token, lp, kept); };
+      if (n > 64)
+        done = finish(w, n, !st.by_mass, tail, s.live, st.p, key_low, st.u, a.logprob != nullptr, &about, give);
+      else if (tid < 32)
+        done = finish_few(w, n, !st.by_mass, tail, s.live, st.p, key_low, st.u, a.logprob != nullptr, &about, give);
     }
   }
   if (!SEARCH) {
     if (rank == 0 && tid == 0) leave(about, big, !done);
     return;
   }
-  if (rank == 0 && tid < ctas) {
-    st_remote(at_rank(&s.word[6], tid), (uint32_t)done);
+  if (rank == 0 && tid < ctas) {     // of the first warp
+    st_remote(at_rank(&s.word[4], tid), big);
     st_remote(at_rank(&s.word[5], tid), (uint32_t)(about != 0));
+    st_remote(at_rank(&s.word[6], tid), (uint32_t)done);
   }
+  if (rank == 0 && tid == 0) s.mass_2 = about;
   row_sync(ctas);
   if (s.word[6]) return;
-  search_row(w, a, r, st, key_low, rank == 0 ? about : (uint64_t)s.word[5]);
+  const float largest = key_float(s.word[4]);
+  about = rank == 0 ? s.mass_2 : s.word[5];
+  __syncthreads();
+  w.scale.set(st.T, largest);
+  if (st.low > 0.f) key_low = logit_key(least_logit(largest, st.T, st.low, s.tmpf));
+  search_row(w, a, r, st, key_low, about);
 }
 
 // grid: clusters that take the rows left by sample_kernel in turn.
@@ -1219,67 +1346,72 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a, i
   };
   if (tid == 0) s.n_list = 0;
   if (ctas > 1) row_sync(ctas);
-  uint32_t live;
+  uint32_t live, big = 0;
   const float c = 1.44269504f / a.temperature;
+  const bool parts = K <= kFewTop;
   w.template read_tops<true>(c, false, &live);
-  row_sync(ctas);
-  if (rank == 0) {
-    uint32_t big;
-    const uint32_t least = w.threshold(K, &big);
-    const uint32_t word[2] = {big, least};
-    w.tell(word, 2);
+  if (parts) {
+    w.template list_part<true>(K, c);
+  } else {
+    w.post_groups();
+    row_sync(ctas);
+    if (rank == 0) {
+      const uint32_t least = w.threshold(K, &big);
+      const uint32_t word[2] = {big, least};
+      w.tell(word, 2);
+      if (tid < ctas) s.part_max[tid] = big;
+    }
+    row_sync(ctas);
+    big = s.word[0];
+    if (big > kNegInfKey && big < kPosInfKey) w.template list_tops<true>(s.word[1], key_float(big), c);
   }
   row_sync(ctas);
-  const uint32_t big = s.word[0], least = s.word[1];
-  if (big <= kNegInfKey || big >= kPosInfKey) {
-    if (rank == 0) {
+  bool many = false;
+  float largest = 0.f;
+  if (rank == 0) {
+    for (int i = 0; i < ctas; ++i) big = max(big, s.part_max[i]);
+    largest = key_float(big);
+    const int n_list = (int)s.n_list;
+    if (big <= kNegInfKey || big >= kPosInfKey) {
       fill(0);
       if (tid == 0) {
         if (big >= kPosInfKey) set_status(a.status, DF_ERR_NAN, r);
         if (a.lse) a.lse[r] = big >= kPosInfKey ? NAN : -INFINITY;
       }
-    }
-    return;
-  }
-  const float largest = key_float(big);
-  w.template list_tops<true>(least, largest, c);
-  row_sync(ctas);
-  uint32_t n_list = s.n_list;
-  if (ctas > 1) {
-    n_list = ld_remote(at_rank(&s.n_list, 0));
-    cluster_arrive();
-  }
-  if (n_list <= kListCap) {
-    if (rank == 0) {
-      w.sort_list(s.list, (int)n_list);
-      const int n = min(K, (int)n_list);
+    } else {
+      many = n_list > kListCap;
       float sum = 0.f;
-      for (int i = tid; i < (int)n_list; i += kRowThreads) {
-        const uint64_t comp = s.list[i];
-        const float l = key_float(key_of(comp));
-        sum += ex2_approx((l - largest) * c);
-        if (i < n) {
-          id[i] = id_of(comp);
-          val[i] = l;
+      if (!many) {
+        w.sort_list(s.list, n_list);
+        const int n = min(K, n_list);
+        for (int i = tid; i < n_list; i += kRowThreads) {
+          const uint64_t comp = s.list[i];
+          const float l = key_float(key_of(comp));
+          sum += ex2_approx((l - largest) * c);
+          if (i < n) {
+            id[i] = id_of(comp);
+            val[i] = l;
+          }
         }
+        fill(n);
+        sum = block_add(sum, s.tmpf);
       }
-      fill(n);
-      sum = block_add(sum, s.tmpf);
       if (tid == 0 && a.lse) {
-        for (int i = 0; i < ctas; ++i) sum += s.tail[i];
+        for (int i = 0; i < ctas; ++i)
+          if (s.part_max[i] > kNegInfKey)
+            sum += (many ? s.sums[i] : s.tail[i]) * ex2_approx((key_float(s.part_max[i]) - largest) * c);
         a.lse[r] = largest / a.temperature + logf(sum);
       }
     }
-    if (ctas > 1) cluster_wait();
-    return;
+    if (tid < ctas) {
+      st_remote(at_rank(&s.word[6], tid), (uint32_t)many);
+      st_remote(at_rank(&s.word[4], tid), big);
+    }
   }
+  row_sync(ctas);
+  if (!s.word[6]) return;
   // many equal logits: the K-th token's place decides
-  if (rank == 0 && tid == 0 && a.lse) {
-    float sum = 0.f;
-    for (int i = 0; i < ctas; ++i) sum += s.sums[i];
-    a.lse[r] = largest / a.temperature + logf(sum);
-  }
-  if (ctas > 1) cluster_wait();
+  largest = key_float(s.word[4]);
   w.scale.set(1.f, largest);
   uint64_t total = 0;
   w.count_all(&total, &live);
