@@ -253,10 +253,11 @@ struct RowWork {
       }
     return max(least, kNegInfKey + 1);
   }
-  // Lists what of this CTA's part reaches the key that k of its threads reach.  In the first CTA:
-  // part_max and part_least; with SUMS tail and sums relative to the part's largest logit.
+  // Lists what of this CTA's part reaches the key that k of its threads reach; the part's largest
+  // key.  In the first CTA:
+  // part_max and part_least; with SUMS tail, relative to the part's largest logit.
   template <bool SUMS>
-  DF_DEV void list_part(int k, float c) {
+  DF_DEV uint32_t list_part(int k, float c) {
     uint32_t big;
     const uint32_t least = part_threshold(k, &big);
     if (tid == 0) {
@@ -264,6 +265,7 @@ struct RowWork {
       st_remote(at_rank(&s.part_least[rank], 0), least);
     }
     list_tops<SUMS>(least, key_float(big), c);
+    return big;
   }
 
   // First CTA, behind a row_sync: the largest key, and for k > 1 a key above -inf's that at least k
@@ -325,21 +327,18 @@ struct RowWork {
   // again, by all threads.  Every CTA lists its own and hands them to the first one.  SUMS: the sum
   // of the others, relative to the largest logit, goes to the first CTA's tail: of the groups not
   // read again from the first pass, of those that are from this one, so that no large term that is
-  // on the list has left its rounding there.  Its sums: of all groups.  (A group's pieces are
-  // lo + who, lo + who + kSub * kRowThreads, ..., who = the thread + its group * kRowThreads.)
+  // on the list has left its rounding there.  (A group's pieces are lo + who, lo + who + kSub *
+  // kRowThreads, ..., who = the thread + its group * kRowThreads.)
   template <bool SUMS>
   DF_DEV void list_tops(uint32_t least, float largest, float c) {
     const int lane = tid & 31;
-    float tail = 0.f, all = 0.f;
+    float tail = 0.f;
     if (tid == 0) s.n_chosen = 0;
     __syncthreads();
 #pragma unroll
     for (int g = 0; g < kSub; ++g) {
       const bool yes = logit_key(top[g]) >= least;
-      if (SUMS) {
-        all += sum[g];
-        if (!yes) tail += sum[g];
-      }
+      if (SUMS && !yes) tail += sum[g];
       const uint32_t who = __ballot_sync(0xffffffffu, yes);
       if (who == 0) continue;
       uint32_t at = 0;
@@ -347,26 +346,25 @@ struct RowWork {
       at = __shfl_sync(0xffffffffu, at, 0);
       if (yes) s.chosen[at + __popc(who & ((1u << lane) - 1))] = (uint16_t)(g * kRowThreads + tid);
     }
-    if (SUMS) {
-      const float f = ref > -INFINITY ? ex2_approx((ref - largest) * c) : 0.f;
-      tail *= f;
-      all *= f;
-    }
+    if (SUMS) tail *= ref > -INFINITY ? ex2_approx((ref - largest) * c) : 0.f;
     __syncthreads();
     auto look = [&](const uint4& v, int piece) {
-      if (!SUMS && !(logit_key(RowOf<E>::largest(v)) >= least)) return;
+      const bool any = logit_key(RowOf<E>::largest(v)) >= least;
+      if (!SUMS && !any) return;
       float x[VE];
       RowOf<E>::unpack(v, x);
+      float t = 0.f;
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
-        const uint32_t key = logit_key(x[e]);
-        if (key >= least) {
-          const uint32_t at = atomicAdd(&s.n_list, 1u);
-          if (at < kListCap) s.list[at] = comp_of(key, part.id(piece, e));
-        } else if (SUMS) {
-          tail += ex2_approx((x[e] - largest) * c);
+        bool listed = false;
+        if (any) {
+          const uint32_t key = logit_key(x[e]);
+          listed = key >= least;
+          if (listed) put(&s.n_list, s.list, kListCap, key, part.id(piece, e));
         }
+        if (SUMS && !listed) t += ex2_approx((x[e] - largest) * c);
       }
+      if (SUMS) tail += t;
     };
     const int each = (part.hi - part.lo + kSub * kRowThreads - 1) / (kSub * kRowThreads);   // pieces of a group
     const int n = (int)s.n_chosen * each;
@@ -390,13 +388,17 @@ struct RowWork {
     if (edge >= 0 && logit_key(top[0]) >= least) look(part.edge(edge), edge);
     if (SUMS) {
       tail = block_add(tail, s.tmpf);
-      all = block_add(all, s.tmpf);
-      if (tid == 0) {
-        st_remote(at_rank(&s.tail[rank], 0), tail);
-        st_remote(at_rank(&s.sums[rank], 0), all);
-      }
+      if (tid == 0) st_remote(at_rank(&s.tail[rank], 0), tail);
     }
     hand_over(&s.n_list, s.list, kListCap);
+  }
+  // The part's sum relative to its largest logit, in the first CTA: sums.
+  DF_DEV void give_sum(float largest, float c) {
+    float all = 0.f;
+#pragma unroll
+    for (int g = 0; g < kSub; ++g) all += sum[g];
+    all = block_add(ref > -INFINITY ? all * ex2_approx((ref - largest) * c) : 0.f, s.tmpf);
+    if (tid == 0) st_remote(at_rank(&s.sums[rank], 0), all);
   }
   // What this CTA has put on its own list goes to the first CTA's (which has put its own there).
   DF_DEV void hand_over(uint32_t* counter, uint64_t* list, uint32_t room) {
@@ -1351,7 +1353,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a, i
   const bool parts = K <= kFewTop;
   w.template read_tops<true>(c, false, &live);
   if (parts) {
-    w.template list_part<true>(K, c);
+    w.give_sum(key_float(w.template list_part<false>(K, 0.f)), c);
   } else {
     w.post_groups();
     row_sync(ctas);
@@ -1363,7 +1365,10 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a, i
     }
     row_sync(ctas);
     big = s.word[0];
-    if (big > kNegInfKey && big < kPosInfKey) w.template list_tops<true>(s.word[1], key_float(big), c);
+    if (big > kNegInfKey && big < kPosInfKey) {
+      w.template list_tops<false>(s.word[1], 0.f, 0.f);
+      w.give_sum(key_float(big), c);
+    }
   }
   row_sync(ctas);
   bool many = false;
@@ -1380,26 +1385,20 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a, i
       }
     } else {
       many = n_list > kListCap;
-      float sum = 0.f;
       if (!many) {
         w.sort_list(s.list, n_list);
         const int n = min(K, n_list);
-        for (int i = tid; i < n_list; i += kRowThreads) {
+        for (int i = tid; i < n; i += kRowThreads) {
           const uint64_t comp = s.list[i];
-          const float l = key_float(key_of(comp));
-          sum += ex2_approx((l - largest) * c);
-          if (i < n) {
-            id[i] = id_of(comp);
-            val[i] = l;
-          }
+          id[i] = id_of(comp);
+          val[i] = key_float(key_of(comp));
         }
         fill(n);
-        sum = block_add(sum, s.tmpf);
       }
       if (tid == 0 && a.lse) {
+        float sum = 0.f;
         for (int i = 0; i < ctas; ++i)
-          if (s.part_max[i] > kNegInfKey)
-            sum += (many ? s.sums[i] : s.tail[i]) * ex2_approx((key_float(s.part_max[i]) - largest) * c);
+          if (s.part_max[i] > kNegInfKey) sum += s.sums[i] * ex2_approx((key_float(s.part_max[i]) - largest) * c);
         a.lse[r] = largest / a.temperature + logf(sum);
       }
     }
