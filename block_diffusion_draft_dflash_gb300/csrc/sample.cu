@@ -144,8 +144,8 @@ struct RowWork {
 
   // -------------------------------------------------------------------------- the first tokens
   float top[kSub];     // largest logits of this thread's groups (the first kSub / ctas)
-  float sum[kSub];     // with SUMS: their sums of 2^((l - ref) c)
-  float ref;           // a logit of the thread at most 8 / c below its largest
+  float sum[kSub];     // with SUMS: their sums of 2^(l c - ref)
+  float ref;           // an exponent at most 8 below that of the thread's largest logit
 
   // Reads the row.  SUMS: also the groups' sums, and with `count` the number of logits above -inf.
   template <bool SUMS>
@@ -157,11 +157,12 @@ struct RowWork {
     for (int j = 0; j < kSub; ++j) m[j] = -INFINITY, sum[j] = 0.f;
     // four groups' pieces, largest logit `big`
     auto add = [&](const uint4* v, int n, float big, float* to) {
-      if ((big - ref) * c > 8.f) {      // also the first time
-        const float f = ref > -INFINITY ? ex2_approx((ref - big) * c) : 0.f;
+      const float y = big * c;
+      if (y > ref + 8.f) {              // also the first time
+        const float f = ref > -INFINITY ? ex2_approx(ref - y) : 0.f;
 #pragma unroll
         for (int j = 0; j < kSub; ++j) sum[j] *= f;
-        ref = big;
+        ref = y;
       }
       if (!(ref > -INFINITY)) return;
 #pragma unroll
@@ -172,7 +173,7 @@ struct RowWork {
 #pragma unroll
           for (int e = 0; e < VE; ++e) n_live += x[e] > -INFINITY;
 #pragma unroll
-        for (int e = 0; e < VE; ++e) x[e] = ex2_approx((x[e] - ref) * c);
+        for (int e = 0; e < VE; ++e) x[e] = ex2_approx(fmaf(x[e], c, -ref));
 #pragma unroll
         for (int w = VE / 2; w > 0; w >>= 1)
 #pragma unroll
@@ -346,7 +347,7 @@ struct RowWork {
       at = __shfl_sync(0xffffffffu, at, 0);
       if (yes) s.chosen[at + __popc(who & ((1u << lane) - 1))] = (uint16_t)(g * kRowThreads + tid);
     }
-    if (SUMS) tail *= ref > -INFINITY ? ex2_approx((ref - largest) * c) : 0.f;
+    if (SUMS) tail *= over_largest(largest, c);
     __syncthreads();
     auto look = [&](const uint4& v, int piece) {
       const bool any = logit_key(RowOf<E>::largest(v)) >= least;
@@ -392,12 +393,16 @@ struct RowWork {
     }
     hand_over(&s.n_list, s.list, kListCap);
   }
+  // 2^(ref - largest c): ref is a float, l c - ref in the sums is rounded once, and so is this.
+  DF_DEV float over_largest(float largest, float c) const {
+    return ref > -INFINITY ? ex2_approx(fmaf(-largest, c, ref)) : 0.f;
+  }
   // The part's sum relative to its largest logit, in the first CTA: sums.
   DF_DEV void give_sum(float largest, float c) {
     float all = 0.f;
 #pragma unroll
     for (int g = 0; g < kSub; ++g) all += sum[g];
-    all = block_add(ref > -INFINITY ? all * ex2_approx((ref - largest) * c) : 0.f, s.tmpf);
+    all = block_add(all * over_largest(largest, c), s.tmpf);
     if (tid == 0) st_remote(at_rank(&s.sums[rank], 0), all);
   }
   // What this CTA has put on its own list goes to the first CTA's (which has put its own there).
@@ -421,8 +426,7 @@ struct RowWork {
   // before it.  Else they are dealt into buckets between the largest and the smallest logit first,
   // and counted in their bucket alone.
   __device__ __noinline__ void sort_list(uint64_t* list, int n) {
-    constexpr int OWN = kListCap / kRowThreads;
-    if (n <= kRowThreads) {
+    if (n <= kRowThreads / 2) {
       const uint64_t e = tid < n ? list[tid] : 0;
       int at = 0;
       if (tid < n)
@@ -433,6 +437,13 @@ struct RowWork {
       __syncthreads();
       return;
     }
+    if (n <= 2 * kRowThreads)
+      deal<2>(list, n);
+    else
+      deal<kListCap / kRowThreads>(list, n);
+  }
+  template <int OWN>     // entries of a thread
+  DF_DEV void deal(uint64_t* list, int n) {
     if (tid == 0) s.key_max = 0, s.key_min = 0xFFFFFFFFu;
     for (int b = tid; b < kBuckets; b += kRowThreads) s.hist[b] = 0;
     __syncthreads();
