@@ -78,6 +78,11 @@ _SIGS = {
     "dflash_target_tree_forward_sampled": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_int] + [C.c_void_p] * 5 +
                                            [C.c_int, C.c_void_p, C.c_float, C.c_ulonglong] + [C.c_void_p] * 3 +
                                            [C.c_size_t, C.c_void_p]),
+    "dflash_target_tree_forward_filtered_workspace_size": (C.c_size_t, [C.c_void_p, C.c_int, C.c_int]),
+    "dflash_target_tree_forward_filtered": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_int] + [C.c_void_p] * 5 +
+                                            [C.c_int] + [C.c_void_p] * 5 + [C.c_ulonglong, C.c_int, C.c_float] +
+                                            [C.c_void_p] * 6 + [C.c_size_t, C.c_void_p]),
+    "dflash_path_rows": (C.c_int, [C.c_int] * 3 + [C.c_void_p] * 2 + [C.c_int] + [C.c_void_p] * 3),
     "dflash_target_expert_counts": (C.c_int, [C.c_void_p, C.c_int, C.c_int, C.c_void_p, C.c_size_t, C.c_void_p,
                                               C.c_void_p]),
     "dflash_linear_workspace_size": (C.c_size_t, []),
@@ -298,6 +303,47 @@ def target_tree_forward(cfg: ModelCfg, weights: ModelWeights, tok, depth, anc, k
     _check("dflash_target_tree_forward", load().dflash_target_tree_forward(
         C.byref(cfg), C.byref(weights), b, T, _p(tok), _p(depth), _p(anc), _p(k_cache), _p(v_cache), cap,
         _p(cache_len), _p(choice), _p(tree_feat), ws.ptr, ws.nbytes, _stream()))
+
+
+def target_tree_forward_filtered_workspace_size(cfg: ModelCfg, b, n_tree):
+    return load().dflash_target_tree_forward_filtered_workspace_size(C.byref(cfg), b, n_tree)
+
+
+def target_tree_forward_filtered(cfg: ModelCfg, weights: ModelWeights, tok, depth, anc, k_cache, v_cache, cache_len,
+                                 choice, tree_feat, ws: Workspace, temperature=None, top_k=None, top_p=None, min_p=None,
+                                 seed: int = 0, top_id=None, top_val=None, top_lse=None, top_temperature: float = 1.0):
+    """The choice per node drawn under its sequence's settings (fp32 and int32 [b], or None; keyed to seed, sequence and
+    position); top_id, top_val [b][n_tree][K] and top_lse [b][n_tree] (optional) take every node's first K tokens."""
+    b, T = tok.shape
+    for t, name in ((temperature, "temperature"), (top_p, "top_p"), (min_p, "min_p"), (top_val, "top_val"),
+                    (top_lse, "top_lse")):
+        _dev(t, torch.float32, name)
+    for t, name in ((top_k, "top_k"), (top_id, "top_id"), (choice, "choice")):
+        _dev(t, torch.int32, name)
+    for t, name in ((temperature, "temperature"), (top_k, "top_k"), (top_p, "top_p"), (min_p, "min_p")):
+        if t is not None and tuple(t.shape) != (b,):
+            raise ValueError(f"{name} must have one entry for each of {b} sequences")
+    K = 0 if top_id is None else top_id.shape[-1]
+    if K and (tuple(top_id.shape) != (b, T, K) or top_val is None or tuple(top_val.shape) != (b, T, K) or
+              (top_lse is not None and tuple(top_lse.shape) != (b, T))):
+        raise ValueError(f"top_id and top_val must be [{b}][{T}][K], top_lse [{b}][{T}]")
+    _check("dflash_target_tree_forward_filtered", load().dflash_target_tree_forward_filtered(
+        C.byref(cfg), C.byref(weights), b, T, _p(tok), _p(depth), _p(anc), _p(k_cache), _p(v_cache), k_cache.shape[3],
+        _p(cache_len), _p(temperature), _p(top_k), _p(top_p), _p(min_p), seed & 0xFFFFFFFFFFFFFFFF, K,
+        float(top_temperature), _p(top_id), _p(top_val), _p(top_lse), _p(choice), _p(tree_feat), ws.ptr, ws.nbytes,
+        _stream()))
+
+
+def path_rows(n_new, src_slot, cache_len, n_tree, teacher_row):
+    """teacher_row [b][D]: the nodes of the accepted path (n_new, src_slot, cache_len as accept_and_compact left them)
+    whose logits stand for draft positions 1 .. D; -1 behind the path."""
+    for t, name in ((n_new, "n_new"), (src_slot, "src_slot"), (cache_len, "cache_len"), (teacher_row, "teacher_row")):
+        _dev(t, torch.int32, name)
+    b, D = teacher_row.shape
+    if n_new.shape != (b,) or cache_len.shape != (b,) or src_slot.dim() != 2 or src_slot.shape[0] != b:
+        raise ValueError(f"n_new, cache_len [{b}] and src_slot [{b}][max] are wanted")
+    _check("dflash_path_rows", load().dflash_path_rows(
+        b, D, n_tree, _p(n_new), _p(src_slot), src_slot.shape[1], _p(cache_len), _p(teacher_row), _stream()))
 
 
 def target_expert_counts(cfg: ModelCfg, b, n_tree, ws: Workspace, counts):

@@ -12,6 +12,7 @@
 #include "layers.h"
 #include "moe.h"
 #include "nvtx.h"
+#include "rows.h"
 #include "workspace.h"
 
 namespace df {
@@ -161,6 +162,31 @@ struct TargetWs {
   LayerBufs B;
   unsigned long long* amax;
   uint32_t* draw_key;  // per-row keys of the LM head's temperature draw
+};
+// What the filtered forward has behind it: logits of a block of rows, and rows that draws leave.
+constexpr int kLogitRows = 1024;
+struct FilterWs {
+  float* logits;
+  SampleLeft* left;
+};
+size_t filter_ws(const df_model_cfg* c, size_t rows, size_t from, void* base, FilterWs* out) {
+  Carver cv(base);
+  cv.off = from;
+  const size_t block = std::min(rows, (size_t)kLogitRows);
+  FilterWs w{};
+  w.logits = cv.take<float>(block * c->vocab);
+  w.left = cv.take<SampleLeft>(block);
+  if (out) *out = w;
+  return cv.off;
+}
+// Settings and outputs of the filtered forward.
+struct Filter {
+  const float *temperature, *top_p, *min_p;
+  const int32_t* top_k;
+  int K;
+  float top_temperature;
+  int32_t* top_id;
+  float *top_val, *top_lse;
 };
 size_t target_ws(const df_model_cfg* c, int b, int n_tree, void* base, TargetWs* out) {
   const int d = c->d_model, Hq = c->n_q_heads, Hkv = c->n_kv_heads, F = c->d_ff;
@@ -450,11 +476,13 @@ int dflash_target_expert_counts(const df_model_cfg* c, int b, int n_tree, const 
 }
 
 // The target's forward over the flattened tree; the choice per node is the argmax
-// (temperature 0) or a temperature draw keyed to (seed, sequence, position).
+// (temperature 0) or a temperature draw keyed to (seed, sequence, position), or with `filter` a draw
+// of dflash_sample with a number keyed so.
 static int target_forward_run(const df_model_cfg* c, const df_model_weights* w, int b, int n_tree, const int32_t* tok,
                               const int32_t* depth, const uint32_t* anc, df_bf16* k_cache, df_bf16* v_cache, int cap,
                               const int32_t* cache_len, int32_t* choice, df_bf16* tree_feat, void* ws,
-                              size_t ws_bytes, float temperature, uint64_t seed, cudaStream_t st) {
+                              size_t ws_bytes, float temperature, uint64_t seed, const Filter* filter,
+                              cudaStream_t st) {
   if (!cfg_ok(c)) return DF_ERR_SHAPE;
   if (!w || !w->layers || !w->embed || !w->final_norm || b < 0 || n_tree < 1 || cap <= 0) return DF_ERR_ARG;
   DF_TRY(layers_ok(c, w));
@@ -463,9 +491,11 @@ static int target_forward_run(const df_model_cfg* c, const df_model_weights* w, 
   if (!tok || !k_cache || !v_cache || !cache_len || !choice) return DF_ERR_ARG;
   if ((depth == nullptr) != (anc == nullptr)) return DF_ERR_ARG;  // both NULL: a causal chain
   if (!al16(k_cache) || !al16(v_cache) || (anc && !al16(anc)) || (tree_feat && !al16(tree_feat))) return DF_ERR_ALIGN;
-  if (!ws || ws_bytes < dflash_target_tree_forward_workspace_size(c, b, n_tree)) return DF_ERR_WORKSPACE;
+  if (!ws || ws_bytes < (filter ? dflash_target_tree_forward_filtered_workspace_size(c, b, n_tree)
+                                : dflash_target_tree_forward_workspace_size(c, b, n_tree)))
+    return DF_ERR_WORKSPACE;
   TargetWs W;
-  target_ws(c, b, n_tree, ws, &W);
+  const size_t used = target_ws(c, b, n_tree, ws, &W);
   int* status = status_of(ws);
   const int d = c->d_model, R = b * n_tree, nf = c->n_feat_layers, Hkv = c->n_kv_heads;
   const size_t plane = (size_t)b * Hkv * cap * 128;
@@ -505,6 +535,32 @@ static int target_forward_run(const df_model_cfg* c, const df_model_weights* w, 
     o.ld_capture = nf * d;
     DF_TRY(run_layer(L, W.B, st));
   }
+  if (filter) {
+    FilterWs F;
+    filter_ws(c, (size_t)R, used, ws, &F);
+    DF_TRY(launch_draw_keys(R, seed, nullptr, nullptr, n_tree, cache_len, depth, W.draw_key, st));
+    for (int r0 = 0; r0 < R; r0 += kLogitRows) {
+      const int n = std::min(kLogitRows, R - r0);
+      GemmDesc g{};
+      g.X = W.B.x + (size_t)r0 * d; g.W = w->embed; g.M = n; g.N = c->vocab; g.K = d; g.ldx = d; g.ldw = d;
+      g.mode = kGemmStore; g.out = F.logits; g.ldo = c->vocab; g.status = status;
+      DF_TRY(launch_gemm(g, st));
+      SampleArgs sa{};
+      sa.x = df_rows{F.logits, DF_F32, n, c->vocab, c->vocab};
+      sa.group = n_tree; sa.row0 = r0; sa.temperature = filter->temperature; sa.top_k = filter->top_k;
+      sa.top_p = filter->top_p; sa.min_p = filter->min_p; sa.draw_key = W.draw_key + r0; sa.token = choice + r0;
+      sa.left = F.left; sa.status = status;
+      DF_TRY(launch_sample(sa, st));
+      if (filter->K > 0) {
+        TopArgs ta{};
+        ta.x = sa.x; ta.K = filter->K; ta.temperature = filter->top_temperature;
+        ta.id = filter->top_id + (size_t)r0 * ta.K; ta.val = filter->top_val + (size_t)r0 * ta.K;
+        ta.lse = filter->top_lse ? filter->top_lse + r0 : nullptr; ta.status = status;
+        DF_TRY(launch_top_logits(ta, st));
+      }
+    }
+    return DF_OK;
+  }
   GemmDesc g{};
   g.X = W.B.x; g.W = w->embed; g.M = R; g.N = c->vocab; g.K = d; g.ldx = d; g.ldw = d;
   g.mode = kGemmArgmax; g.amax = W.amax; g.status = status;
@@ -523,7 +579,7 @@ int dflash_target_tree_forward(const df_model_cfg* c, const df_model_weights* w,
                                size_t ws_bytes, df_stream stream) {
   DF_NVTX("dflash_target_tree_forward");
   return target_forward_run(c, w, b, n_tree, tok, depth, anc, k_cache, v_cache, cap, cache_len, choice, tree_feat, ws,
-                            ws_bytes, 0.f, 0, (cudaStream_t)stream);
+                            ws_bytes, 0.f, 0, nullptr, (cudaStream_t)stream);
 }
 
 int dflash_target_tree_forward_sampled(const df_model_cfg* c, const df_model_weights* w, int b, int n_tree,
@@ -534,7 +590,28 @@ int dflash_target_tree_forward_sampled(const df_model_cfg* c, const df_model_wei
   DF_NVTX("dflash_target_tree_forward_sampled");
   if (!(temperature > 0.f) || !std::isfinite(temperature)) return DF_ERR_ARG;
   return target_forward_run(c, w, b, n_tree, tok, depth, anc, k_cache, v_cache, cap, cache_len, choice, tree_feat, ws,
-                            ws_bytes, temperature, seed, (cudaStream_t)stream);
+                            ws_bytes, temperature, seed, nullptr, (cudaStream_t)stream);
+}
+
+size_t dflash_target_tree_forward_filtered_workspace_size(const df_model_cfg* tcfg, int b, int n_tree) {
+  if (!cfg_ok(tcfg) || b <= 0 || n_tree <= 0) return kAlign;
+  return filter_ws(tcfg, (size_t)b * n_tree, dflash_target_tree_forward_workspace_size(tcfg, b, n_tree), nullptr, nullptr);
+}
+
+int dflash_target_tree_forward_filtered(const df_model_cfg* c, const df_model_weights* w, int b, int n_tree,
+                                        const int32_t* tok, const int32_t* depth, const uint32_t* anc,
+                                        df_bf16* k_cache, df_bf16* v_cache, int cap, const int32_t* cache_len,
+                                        const float* temperature, const int32_t* top_k, const float* top_p,
+                                        const float* min_p, uint64_t seed, int K, float top_temperature,
+                                        int32_t* top_id, float* top_val, float* top_lse, int32_t* choice,
+                                        df_bf16* tree_feat, void* ws, size_t ws_bytes, df_stream stream) {
+  DF_NVTX("dflash_target_tree_forward_filtered");
+  if (K < 0 || (K > 0 && (!(top_temperature >= 0x1p-100f && top_temperature <= 0x1p100f) || !top_id || !top_val)))
+    return DF_ERR_ARG;
+  if (K > 1024 || (c && c->vocab > 1 << 20)) return DF_ERR_SHAPE;
+  const Filter f{temperature, top_p, min_p, top_k, K, top_temperature, top_id, top_val, top_lse};
+  return target_forward_run(c, w, b, n_tree, tok, depth, anc, k_cache, v_cache, cap, cache_len, choice, tree_feat, ws,
+                            ws_bytes, 0.f, seed, &f, (cudaStream_t)stream);
 }
 
 // ------------------------------------------------------------------------ draft block

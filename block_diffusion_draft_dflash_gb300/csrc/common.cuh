@@ -336,9 +336,12 @@ DF_HD uint32_t draw_key(uint64_t seed, int s, int n) {
 // g_v of token v for the draw keyed by k; u = (23 random bits + 1/2) / 2^23, exact in fp32
 // and inside [2^-24, 1 - 2^-24].  The inner logarithm is the accurate one: for u near 1,
 // -log u is tiny and an approximate logarithm's absolute error would dominate it.
-DF_DEV float draw_noise(uint32_t k, int v) {
+DF_DEV float draw_uniform(uint32_t k, int v) {
   const uint32_t h = fmix32(k ^ ((uint32_t)v * 0x27D4EB2Fu));
-  const float u = ((float)(h >> 9) + 0.5f) * (1.f / 8388608.f);
+  return ((float)(h >> 9) + 0.5f) * (1.f / 8388608.f);
+}
+DF_DEV float draw_noise(uint32_t k, int v) {
+  const float u = draw_uniform(k, v);
   return -__logf(-logf(u));
 }
 

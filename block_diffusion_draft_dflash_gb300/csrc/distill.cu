@@ -352,6 +352,20 @@ __global__ void __launch_bounds__(kRowThreads) distill_backward_kernel(DistillAr
   write_gradient(part, grad, en, z, mine, st.x, T.c, scale, expf(-st.y), st.z > -INFINITY ? rho * expf(-st.z) : 0.f);
 }
 
+__global__ void __launch_bounds__(256) path_rows_kernel(int b, int D, int n_tree, const int32_t* __restrict__ n_new,
+                                                        const int32_t* __restrict__ src_slot, int max_src,
+                                                        const int32_t* __restrict__ cache_len, int32_t* __restrict__ row) {
+  pdl_wait();
+  pdl_trigger();
+  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= (long long)b * D) return;
+  const int s = (int)(i / D), d = (int)(i % D);
+  int node = -1;
+  if (d < n_new[s]) node = d == 0 ? 0 : src_slot[(size_t)s * max_src + d - 1] - (cache_len[s] - n_new[s]);
+  if (node >= n_tree || node < (d > 0)) node = -1;
+  row[i] = node < 0 ? -1 : s * n_tree + node;
+}
+
 int done(cudaError_t e) { return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? DF_OK : DF_ERR_CUDA; }
 
 }  // namespace
@@ -369,6 +383,14 @@ int launch_distill_backward(const DistillArgs& a, cudaStream_t st) {
   const auto f = a.x.dtype == DF_F32 ? distill_backward_kernel<float> : distill_backward_kernel<uint16_t>;
   DF_TRACE("distill_backward", st);
   return done(launch_k(f, dim3((unsigned)a.x.rows * ctas), dim3(kRowThreads), 0, st, a, ctas));
+}
+
+int launch_path_rows(int b, int D, int n_tree, const int32_t* n_new, const int32_t* src_slot, int max_src,
+                     const int32_t* cache_len, int32_t* teacher_row, cudaStream_t st) {
+  DF_TRACE("path_rows", st);
+  const unsigned blocks = (unsigned)(((long long)b * D + 255) / 256);
+  return done(launch_k(path_rows_kernel, dim3(blocks), dim3(256), 0, st, b, D, n_tree, n_new, src_slot, max_src, cache_len,
+                       teacher_row));
 }
 
 }  // namespace df

@@ -13,10 +13,11 @@ struct SampleLeft {               // a row that one pass did not decide
 };
 struct SampleArgs {
   df_rows x;
-  int group;                      // rows r of one setting: r / group
+  int group, row0;                // row r's setting: (row0 + r) / group
   const float *temperature, *top_p, *min_p;   // [rows / group], each may be null
   const int32_t* top_k;
-  const float* u;                 // [rows]
+  const float* u;                 // [rows], or null:
+  const uint32_t* draw_key;       // [rows] keys of the draws
   int32_t* token;                 // [rows]
   float* logprob;                 // [rows], may be null
   int32_t* n_kept;                // [rows], may be null
@@ -50,6 +51,10 @@ struct DistillArgs {
 };
 int launch_distill(const DistillArgs& a, cudaStream_t st);
 int launch_distill_backward(const DistillArgs& a, cudaStream_t st);
+
+// dflash_path_rows
+int launch_path_rows(int b, int D, int n_tree, const int32_t* n_new, const int32_t* src_slot, int max_src,
+                     const int32_t* cache_len, int32_t* teacher_row, cudaStream_t st);
 
 // CTAs that share a row of V logits, for this many rows: a power of two up to 8 (one cluster).
 int row_ctas(int rows, int V);

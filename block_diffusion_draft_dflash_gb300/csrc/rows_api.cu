@@ -125,4 +125,14 @@ int dflash_distill_backward(const df_rows* x, int K, int n_teacher, const int32_
   return launch_distill_backward(a, (cudaStream_t)stream);
 }
 
+int dflash_path_rows(int b, int D, int n_tree, const int32_t* n_new, const int32_t* src_slot, int max_src,
+                     const int32_t* cache_len, int32_t* teacher_row, df_stream stream) {
+  DF_NVTX("dflash_path_rows");
+  if (b < 0 || D < 1 || n_tree < 1 || max_src < 0 || max_src < D - 1) return DF_ERR_ARG;
+  if ((long long)b * D > (1 << 27) || (long long)b * n_tree > 2147483647LL) return DF_ERR_SHAPE;
+  if (b == 0) return DF_OK;
+  if (!n_new || !cache_len || !teacher_row || (D > 1 && !src_slot)) return DF_ERR_ARG;
+  return launch_path_rows(b, D, n_tree, n_new, src_slot, max_src, cache_len, teacher_row, (cudaStream_t)stream);
+}
+
 }  // extern "C"

@@ -1094,12 +1094,12 @@ struct Settings {
   bool ok, by_k, by_min, by_mass;
 
   DF_DEV Settings(const SampleArgs& a, int r) {
-    const int g = r / a.group;
+    const int g = (a.row0 + r) / a.group;
     T = a.temperature ? a.temperature[g] : 1.f;
     k = a.top_k ? a.top_k[g] : 0;
     p = a.top_p ? a.top_p[g] : 1.f;
     low = a.min_p ? a.min_p[g] : 0.f;
-    u = a.u[r];
+    u = a.u ? a.u[r] : draw_uniform(a.draw_key[r], 0);
     ok = T >= 0.f && T <= 0x1p100f && p > 0.f && p <= 1.f && low >= 0.f && low <= 1.f && u >= 0.f && u < 1.f;
     if (T < 0x1p-126f) {   // the first token
       T = 1.f;

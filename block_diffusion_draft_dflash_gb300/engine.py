@@ -127,12 +127,20 @@ class SpecDecoder:
     temperature 0: greedy verification; > 0: the target draws its token after every node at
     that temperature (keyed to seed, sequence and position; see dflash.h), and the walk
     follows the drawn tokens.
+    top_k, top_p, min_p: the draws are cut to likely tokens (dflash_target_tree_forward_filtered);
+    `settings` holds them and the temperature for every sequence and may be changed between steps,
+    replayed ones too.
+    teach K: every verification also gives its nodes' first K tokens, and distill() the loss of
+    the step's draft against them, at the accepted path's nodes, with its gradient by `logprobs`.
     """
 
     def __init__(self, target: DeviceModel, drafter: DeviceModel, b: int, B: int, cap: int, prompt_len: int = 0,
-                 device="cuda", mode: str = "tree", temperature: float = 0.0, seed: int = 0):
+                 device="cuda", mode: str = "tree", temperature: float = 0.0, seed: int = 0, top_k: int = 0,
+                 top_p: float = 1.0, min_p: float = 0.0, teach: int = 0, teach_temperature: float = 1.0):
         assert mode in ("tree", "chain")
         assert temperature >= 0.0
+        assert 0.0 < top_p <= 1.0 and 0.0 <= min_p <= 1.0 and teach >= 0
+        self.filtered = top_k > 0 or top_p < 1.0 or min_p > 0.0 or teach > 0
         self.temperature, self.seed = float(temperature), int(seed)
         ts, ds = target.shape, drafter.shape
         self.t, self.d = target, drafter
@@ -171,17 +179,37 @@ class SpecDecoder:
         self.ws_draft = _lib.Workspace(_lib.draft_block_workspace_size(drafter.cfg, b, self.max_new), device)
         self.ws_tree = _lib.Workspace(_lib.chain_build_workspace_size(b, self.D) if mode == "chain" else
                                       _lib.ddtree_build_workspace_size(b, self.D, ds.vocab, B), device)
-        self.ws_verify = _lib.Workspace(_lib.target_tree_forward_workspace_size(target.cfg, b, T), device)
+        verify_size = _lib.target_tree_forward_filtered_workspace_size if self.filtered else \
+            _lib.target_tree_forward_workspace_size
+        self.ws_verify = _lib.Workspace(verify_size(target.cfg, b, T), device)
+        if self.filtered:
+            full = lambda v, dt: torch.full((b,), v, dtype=dt, **dev)
+            self.settings = dict(temperature=full(self.temperature, torch.float32), top_k=full(top_k, torch.int32),
+                                 top_p=full(top_p, torch.float32), min_p=full(min_p, torch.float32))
+        self.teach, self.teach_temperature = int(teach), float(teach_temperature)
+        if teach:
+            zf = lambda *s: torch.zeros(s, dtype=torch.float32, **dev)
+            self.top = dict(top_id=zi(b, T, teach), top_val=zf(b, T, teach), top_lse=zf(b, T))
+            self.teacher_row = zi(b, self.D)
+            self.loss, self.stats, self.grad = zf(b, self.D), zf(b, self.D, 4), torch.zeros_like(self.logprobs)
+            self.ws_distill = _lib.Workspace(_lib.distill_workspace_size(b * self.D, ds.vocab), device)
         self.ws_accept = _lib.Workspace(_lib.accept_and_compact_workspace_size(b, T), device)
         self.prompt_len = prompt_len
         if prompt_len:
             self.prompt_feat = z16(b, prompt_len, self.feat_dim)
-            self.ws_prefill = _lib.Workspace(_lib.target_tree_forward_workspace_size(target.cfg, b, prompt_len), device)
+            self.ws_prefill = _lib.Workspace(verify_size(target.cfg, b, prompt_len), device)
             self.ws_draft0 = _lib.Workspace(_lib.draft_block_workspace_size(drafter.cfg, b, prompt_len), device)
         self.first = False
         self.plant = None  # optional callable(logprobs) run between draft and tree build (harness only)
 
     # ------------------------------------------------------------------ phases
+    def _target(self, tok, depth, anc, choice, feat, ws, **top):
+        args = (self.t.cfg, self.t.weights, tok, depth, anc, self.k_cache, self.v_cache, self.cache_len, choice, feat, ws)
+        if self.filtered:
+            _lib.target_tree_forward_filtered(*args, seed=self.seed, **self.settings, **top)
+        else:
+            _lib.target_tree_forward(*args, self.temperature, self.seed)
+
     def prefill(self, prompt: torch.Tensor):
         """Prompt pass through the target (chain tree at N = 0); sets the first bonus token."""
         b, P = prompt.shape
@@ -190,9 +218,7 @@ class SpecDecoder:
         self.cache_len.zero_()
         self.ctx_len.zero_()
         # depth and ancestor rows omitted: the library runs the rows as a causal chain
-        _lib.target_tree_forward(self.t.cfg, self.t.weights, prompt.to(torch.int32).contiguous(), None, None,
-                                 self.k_cache, self.v_cache, self.cache_len, choice, self.prompt_feat, self.ws_prefill,
-                                 self.temperature, self.seed)
+        self._target(prompt.to(torch.int32).contiguous(), None, None, choice, self.prompt_feat, self.ws_prefill)
         self.cache_len.fill_(P)
         self.bonus.copy_(choice[:, -1])
         self.n_new.fill_(P)
@@ -215,13 +241,24 @@ class SpecDecoder:
             _lib.ddtree_build(self.logprobs, self.B, self.tree, self.ws_tree, root_tok=self.bonus)
 
     def verify(self):
-        _lib.target_tree_forward(self.t.cfg, self.t.weights, self.tree["tok"], self.tree["depth"], self.tree["anc"],
-                                 self.k_cache, self.v_cache, self.cache_len, self.choice, self.tree_feat,
-                                 self.ws_verify, self.temperature, self.seed)
+        top = dict(self.top, top_temperature=self.teach_temperature) if self.teach else {}
+        self._target(self.tree["tok"], self.tree["depth"], self.tree["anc"], self.choice, self.tree_feat, self.ws_verify, **top)
 
     def accept(self):
         _lib.accept_and_compact(self.choice, self.tree["tok"], self.tree["parent"], self.k_cache, self.v_cache,
                                 self.cache_len, self.tree_feat, self.new_feat, self.acc, self.ws_accept)
+
+    def distill(self, weight=None):
+        """After a step: loss [b][D] of its drafted distributions against the target's at the accepted path (weight [b][D]
+        fp32, optional: early positions may count more), and in `grad` the gradient of their sum by `logprobs`."""
+        b, D, V = self.logprobs.shape
+        _lib.path_rows(self.n_new, self.acc["src_slot"], self.cache_len, self.T, self.teacher_row)
+        flat = lambda t: None if t is None else t.view(b * D, *t.shape[2:])
+        K = self.teach
+        _lib.distill(flat(self.logprobs), self.top["top_id"].view(-1, K), self.top["top_val"].view(-1, K),
+                     self.top["top_lse"].view(-1), self.teach_temperature, flat(self.loss), flat(self.stats),
+                     self.ws_distill, teacher_row=flat(self.teacher_row), weight=flat(weight), grad=flat(self.grad))
+        return self.loss
 
     def step(self):
         self.draft()
@@ -250,7 +287,7 @@ class SpecDecoder:
 
     def status(self):
         """First device-side error of any call (0 if none); synchronises the stream."""
-        for ws in (self.ws_draft, self.ws_tree, self.ws_verify, self.ws_accept):
+        for ws in (self.ws_draft, self.ws_tree, self.ws_verify, self.ws_accept) + ((self.ws_distill,) if self.teach else ()):
             s = ws.status()
             if s:
                 return s

@@ -10,6 +10,8 @@
  *                              (_sampled: the target's temperature draw per node)
  *   tree_verify_attention      ancestor-only attention of tree rows over the KV cache
  *   accept_and_compact         greedy longest-path walk and KV-cache compaction
+ *   dflash_sample, dflash_top_logits, dflash_distill   rows of logits: draws under top-k, top-p and
+ *                              min-p, what a target teaches, and the drafter's loss with its gradient
  *
  * Sources (page title, section):
  *   [DFlash]  "DFlash: Block Diffusion for Flash Speculative Decoding 논문 정리"
@@ -559,6 +561,36 @@ int dflash_distill_backward(const df_rows* student, int K, int n_teacher, const 
                             const float* lse, const int32_t* teacher_row, float temperature, const float* weight,
                             const float* stats, const float* grad_loss, void* grad, int64_t ld_grad, void* ws,
                             size_t ws_bytes, df_stream stream);
+
+/* dflash_target_tree_forward_filtered -- as dflash_target_tree_forward, with the choice after
+ * every node drawn under a temperature, top-k, top-p and min-p of its sequence (dflash_sample over
+ * the node's logits), and on request the first K tokens of every node (dflash_top_logits): what
+ * the accepted path's nodes teach the drafter.
+ *
+ * Sequence s draws at position n with u = (23 bits + 1/2) / 2^23, the number that the sampled
+ * forward gives token 0 there, so speculative decoding emits the tokens plain decoding emits under
+ * the same seed and settings.  Logits (fp32) are made and used in blocks of at most 1024 nodes.
+ *   temperature, top_k, top_p, min_p   [b] (device) or NULL, as in dflash_sample; a setting outside
+ *             its range is recorded and its sequence's choices are -1
+ *   K         0: no lists; else 1 .. 1024 with top_temperature (2^-100 .. 2^100),
+ *             top_id, top_val [b][n_tree][K] and top_lse [b][n_tree] (may be NULL) out
+ *   Every other argument is that of dflash_target_tree_forward; depth and anc may be NULL. */
+size_t dflash_target_tree_forward_filtered_workspace_size(const df_model_cfg* tcfg, int b, int n_tree);
+int dflash_target_tree_forward_filtered(const df_model_cfg* tcfg, const df_model_weights* tw, int b, int n_tree,
+                                        const int32_t* tok, const int32_t* depth, const uint32_t* anc,
+                                        df_bf16* k_cache, df_bf16* v_cache, int cap, const int32_t* cache_len,
+                                        const float* temperature, const int32_t* top_k, const float* top_p,
+                                        const float* min_p, uint64_t seed, int K, float top_temperature,
+                                        int32_t* top_id, float* top_val, float* top_lse, int32_t* choice,
+                                        df_bf16* tree_feat, void* ws, size_t ws_bytes, df_stream stream);
+
+/* dflash_path_rows -- the nodes of a step's accepted path, as dflash_distill's teacher_row: the
+ * node whose logits stand for draft position d + 1 of sequence s is the path's node of depth d.
+ *   n_new, src_slot [b][max_src], cache_len   as accept_and_compact left them
+ *   teacher_row  [b][D] int32 out: s * n_tree + node for d < n_new[s] (the root, then the path), else
+ *                -1, as where an entry is not a node of the tree.  max_src >= D - 1 */
+int dflash_path_rows(int b, int D, int n_tree, const int32_t* n_new, const int32_t* src_slot, int max_src,
+                     const int32_t* cache_len, int32_t* teacher_row, df_stream stream);
 
 /* ------------------------------------------------------------------------------------
  * dflash_linear -- building block: out (+)= X . W^T on the tensor cores.

@@ -76,3 +76,29 @@ def test_distill(call):
 
 def test_outputs():
     assert distill(loss=None) == -1 and backward(grad=None) == -1
+
+
+def test_path_rows():
+    lib = _lib.load()
+    call = lambda b=2, D=4, n=9, new=A, src=A, ms=4, cl=A, out=A: lib.dflash_path_rows(b, D, n, new, src, ms, cl, out, None)  # noqa: E731
+    assert call(b=-1) == -1 and call(D=0) == -1 and call(n=0) == -1 and call(ms=2) == -1 and call(ms=-1) == -1
+    assert call(new=None) == -1 and call(src=None) == -1 and call(cl=None) == -1 and call(out=None) == -1
+    assert call(b=1 << 28) == -2 and call(b=0, new=None) == 0
+
+
+def test_filtered_forward():
+    import synth
+    from block_diffusion_draft_dflash_gb300 import engine
+
+    m = engine.DeviceModel.from_host(synth.target_weights(synth.ModelShape(1, 128, 2, 1, 128, 128, 64), 1), "cpu")
+    lib = _lib.load()
+    size = lib.dflash_target_tree_forward_filtered_workspace_size(C.byref(m.cfg), 1, 3)
+    assert size > lib.dflash_target_tree_forward_workspace_size(C.byref(m.cfg), 1, 3)
+
+    def call(K=0, T=1.0, ids=A, vals=A, ws_bytes=size, ws=A):
+        return lib.dflash_target_tree_forward_filtered(
+            C.byref(m.cfg), C.byref(m.weights), 1, 3, A, None, None, A, A, 64, A, None, None, None, None, 0, K, T, ids, vals, None,
+            A, None, ws, ws_bytes, None)
+    assert call(K=-1) == -1 and call(K=1025) == -2 and call(K=4, ids=None) == -1 and call(K=4, vals=None) == -1
+    assert call(K=4, T=0.0) == -1 and call(K=4, T=float("nan")) == -1
+    assert call(ws=None) == -9 and call(ws_bytes=size - 256) == -9
