@@ -557,44 +557,45 @@ def kv4_evict(cache: Kv4Cache, score, cache_len, budget, n_sink, n_recent, to: K
 
 # ------------------------------------------------------------------------- rows of logits
 _ROW_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
-class _Rows:
-    """A call's rows [rows][V] (fp32 or bf16, any row stride) and its other arguments, all on one device, which
-    has to be the current one."""
+def _rows(t, ws, name):
+    """(df_rows, device, rows, V, workspace and stream) of a call's rows [rows][V] (fp32 or bf16, any row stride), which
+    have to lie on the current device, like its other arguments."""
+    dtype, index = _ROW_TYPES.get(t.dtype), t.get_device()
+    if dtype is None or index < 0 or t.dim() != 2:
+        raise ValueError(f"{name} must be a CUDA tensor [rows][V], fp32 or bf16")
+    n, V = t.shape
+    ld, step = t.stride()
+    if step != 1 and V > 1:
+        raise ValueError(f"{name} must have a row's values next to each other")
+    buf = ws.buf
+    if _current_device() != index or buf.get_device() != index:
+        raise ValueError(f"the current device and the workspace's have to be that of {name}")
+    return (RowsStruct(t.data_ptr(), dtype, n, V, ld if n > 1 else V), index, n, V,
+            (buf.data_ptr(), ws.nbytes, _current_stream(index)))
 
-    def __init__(self, t, ws, name):
-        dt = _ROW_TYPES.get(t.dtype)
-        if dt is None or not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-            raise ValueError(f"{name} must be a CUDA tensor [rows][V], fp32 or bf16, with values next to each other")
-        self.index, (self.rows, self.V) = t.get_device(), t.shape
-        if torch._C._cuda_getDevice() != self.index or ws.buf.get_device() != self.index:
-            raise ValueError(f"the current device and the workspace's have to be that of {name}")
-        self.ws = (ws.buf.data_ptr(), ws.nbytes, torch._C._cuda_getCurrentRawStream(self.index))
-        self.struct = RowsStruct(t.data_ptr(), dt, self.rows, self.V, self.stride(t))
-        self.ref = C.addressof(self.struct)
 
-    @staticmethod
-    def stride(t):
-        return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _at(t, dtype, index, shape, name):
+    """Address of an argument that lies on device `index` (None: 0)."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or t.get_device() != index or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on the rows' device")
+    return t.data_ptr()
 
-    def arg(self, t, dtype, shape, name):
-        """Address of an argument (None: 0)."""
-        if t is None:
-            return 0
-        if t.dtype is not dtype or t.get_device() != self.index or t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on the rows' device")
-        return t.data_ptr()
 
-    def like(self, t, dtype, name):
-        """Address and row stride of an output shaped like the rows."""
-        if t is None:
-            return 0, 0
-        if t.dtype is not dtype or t.get_device() != self.index or t.shape != (self.rows, self.V) or \
-                (self.V > 1 and t.stride(1) != 1):
-            raise ValueError(f"{name} must be a {dtype} tensor [{self.rows}][{self.V}] on the rows' device, with values "
-                             "next to each other")
-        return t.data_ptr(), self.stride(t)
+def _rows_out(t, dtype, index, n, V, name):
+    """Address and row stride of an output shaped like the rows (None: 0)."""
+    if t is None:
+        return 0, 0
+    if t.dtype is not dtype or t.get_device() != index or t.shape != (n, V):
+        raise ValueError(f"{name} must be a {dtype} tensor [{n}][{V}] on the rows' device")
+    ld, step = t.stride()
+    if step != 1 and V > 1:
+        raise ValueError(f"{name} must have a row's values next to each other")
+    return t.data_ptr(), ld if n > 1 else V
 
 
 def sample_workspace_size(rows, V):
@@ -605,15 +606,14 @@ def sample(logits, u, token, ws: Workspace, temperature=None, top_k=None, top_p=
            n_kept=None):
     """token[r] = the token of row r of logits [rows][V] (fp32 or bf16) drawn with u[r] under temperature, top-k, top-p
     and min-p (see dflash.h); settings [rows / group] (row r: r / group) or None: 1, 0, 1, 0."""
-    x = _Rows(logits, ws, "logits")
-    arg, f32, i32, n = x.arg, torch.float32, torch.int32, (x.rows,)
-    if group < 1 or x.rows % group:
-        raise ValueError(f"{x.rows} rows are not groups of {group}")
-    s = (x.rows // group,)
+    x, dev, rows, _, where = _rows(logits, ws, "logits")
+    if group < 1 or rows % group:
+        raise ValueError(f"{rows} rows are not groups of {group}")
+    f32, i32, n, each = torch.float32, torch.int32, (rows,), (rows // group,)
     _check("dflash_sample", load().dflash_sample(
-        x.ref, group, arg(temperature, f32, s, "temperature"), arg(top_k, i32, s, "top_k"), arg(top_p, f32, s, "top_p"),
-        arg(min_p, f32, s, "min_p"), arg(u, f32, n, "u"), arg(token, i32, n, "token"), arg(logprob, f32, n, "logprob"),
-        arg(n_kept, i32, n, "n_kept"), *x.ws))
+        C.addressof(x), group, _at(temperature, f32, dev, each, "temperature"), _at(top_k, i32, dev, each, "top_k"),
+        _at(top_p, f32, dev, each, "top_p"), _at(min_p, f32, dev, each, "min_p"), _at(u, f32, dev, n, "u"),
+        _at(token, i32, dev, n, "token"), _at(logprob, f32, dev, n, "logprob"), _at(n_kept, i32, dev, n, "n_kept"), *where))
 
 
 def top_logits_workspace_size(rows, V):
@@ -623,43 +623,41 @@ def top_logits_workspace_size(rows, V):
 def top_logits(logits, temperature, id, val, lse, ws: Workspace):
     """The K first tokens of every row of logits [rows][V] (id, val [rows][K] int32, fp32) and, at the temperature, the
     log-sum of all of it (lse [rows] fp32, may be None)."""
-    x = _Rows(logits, ws, "logits")
-    shape = (x.rows, id.shape[1])
+    x, dev, rows, _, where = _rows(logits, ws, "logits")
+    shape = (rows, id.shape[1])
     _check("dflash_top_logits", load().dflash_top_logits(
-        x.ref, shape[1], temperature, x.arg(id, torch.int32, shape, "id"), x.arg(val, torch.float32, shape, "val"),
-        x.arg(lse, torch.float32, shape[:1], "lse"), *x.ws))
+        C.addressof(x), shape[1], temperature, _at(id, torch.int32, dev, shape, "id"), _at(val, torch.float32, dev, shape, "val"),
+        _at(lse, torch.float32, dev, shape[:1], "lse"), *where))
 
 
 def distill_workspace_size(rows, V):
     return load().dflash_distill_workspace_size(rows, V)
 
 
-def _distill_args(student, id, val, lse, temperature, ws, teacher_row, weight):
-    x = _Rows(student, ws, "student")
-    arg, f32, i32, n = x.arg, torch.float32, torch.int32, (x.rows,)
-    lists, K = shape = tuple(id.shape)
-    return x, (x.ref, K, lists, arg(id, i32, shape, "id"), arg(val, f32, shape, "val"), arg(lse, f32, shape[:1], "lse"),
-               arg(teacher_row, i32, n, "teacher_row"), temperature, arg(weight, f32, n, "weight"))
-
-
 def distill(student, id, val, lse, temperature, loss, stats, ws: Workspace, teacher_row=None, weight=None, grad=None):
     """loss [rows] of student rows [rows][V] (fp32 or bf16) against a teacher's lists id, val [lists][K] and lse [lists]
     (None: the lists are all there is), with stats [rows][4] for distill_backward and, where grad is given (like student, or
     student itself), the gradient of the losses' sum.  teacher_row [rows]: each row's list, -1: none."""
-    x, args = _distill_args(student, id, val, lse, temperature, ws, teacher_row, weight)
+    x, dev, rows, V, where = _rows(student, ws, "student")
+    f32, i32, n, shape = torch.float32, torch.int32, (rows,), id.shape
     _check("dflash_distill", load().dflash_distill(
-        *args, x.arg(loss, torch.float32, (x.rows,), "loss"), x.arg(stats, torch.float32, (x.rows, 4), "stats"),
-        *x.like(grad, student.dtype, "grad"), *x.ws))
+        C.addressof(x), shape[1], shape[0], _at(id, i32, dev, shape, "id"), _at(val, f32, dev, shape, "val"),
+        _at(lse, f32, dev, shape[:1], "lse"), _at(teacher_row, i32, dev, n, "teacher_row"), temperature,
+        _at(weight, f32, dev, n, "weight"), _at(loss, f32, dev, n, "loss"), _at(stats, f32, dev, (rows, 4), "stats"),
+        *_rows_out(grad, student.dtype, dev, rows, V, "grad"), *where))
 
 
 def distill_backward(student, id, val, lse, temperature, stats, grad, ws: Workspace, grad_loss=None, teacher_row=None,
                      weight=None):
     """grad (like student, or student itself) = the gradient of sum grad_loss loss by the student's rows, from the arguments
     and the stats of distill."""
-    x, args = _distill_args(student, id, val, lse, temperature, ws, teacher_row, weight)
+    x, dev, rows, V, where = _rows(student, ws, "student")
+    f32, i32, n, shape = torch.float32, torch.int32, (rows,), id.shape
     _check("dflash_distill_backward", load().dflash_distill_backward(
-        *args, x.arg(stats, torch.float32, (x.rows, 4), "stats"), x.arg(grad_loss, torch.float32, (x.rows,), "grad_loss"),
-        *x.like(grad, student.dtype, "grad"), *x.ws))
+        C.addressof(x), shape[1], shape[0], _at(id, i32, dev, shape, "id"), _at(val, f32, dev, shape, "val"),
+        _at(lse, f32, dev, shape[:1], "lse"), _at(teacher_row, i32, dev, n, "teacher_row"), temperature,
+        _at(weight, f32, dev, n, "weight"), _at(stats, f32, dev, (rows, 4), "stats"), _at(grad_loss, f32, dev, n, "grad_loss"),
+        *_rows_out(grad, student.dtype, dev, rows, V, "grad"), *where))
 
 
 def plant_logprobs(logprobs, ref, pos, rate, bias, seed, miss_bias=0.0):

@@ -56,19 +56,26 @@ struct Entries {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int i = (int)threadIdx.x + j * kRowThreads;
-      id[j] = i < a.K ? a.id[(size_t)list * a.K + i] : -1;
-      float v = -INFINITY;
+      id[j] = -1;
+      ln_t[j] = -INFINITY;
+      if (i < a.K) {
+        id[j] = a.id[(size_t)list * a.K + i];
+        ln_t[j] = a.val[(size_t)list * a.K + i];
+      }
+    }
+    if (a.lse) lse = a.lse[list];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
       if (id[j] < -1 || id[j] >= V) {
         bad |= 2;
         id[j] = -1;
-      } else if (id[j] >= 0) {
-        v = a.val[(size_t)list * a.K + i];
-        if (!(v < INFINITY)) bad |= 1;
       }
-      ln_t[j] = v;
+      if (id[j] < 0)
+        ln_t[j] = -INFINITY;
+      else if (!(ln_t[j] < INFINITY))
+        bad |= 1;
     }
     if (a.lse) {
-      lse = a.lse[list];
       if (!(fabsf(lse) < INFINITY)) bad |= 1;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) ln_t[j] = ln_t[j] > -INFINITY ? T.over(ln_t[j], lse) : -INFINITY;
@@ -208,7 +215,12 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a, int
   const int n_words = ((part.end - part.begin) * VE + 31) / 32;
   for (int i = tid; i < n_words; i += kRowThreads) bits[i] = 0;
   if (tid == 0) s.flags = 0;
-  if (ctas > 1) row_sync(ctas);     // every CTA of the cluster runs
+  if (ctas > 1) {
+    cluster_arrive();
+    // few rows: theirs are on the way while the list is read
+    for (int i = part.lo + tid * 8; i < part.hi; i += 8 * kRowThreads)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(part.pieces + i));
+  }
   Entries en;
   en.load(a, T, list, s.tmp);       // with barriers behind the zeros
   float z[kPer];
@@ -272,6 +284,7 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a, int
   in = block_add(in, s.tmp);
   cross = block_add(cross, s.tmp);
   tsum = block_add(tsum, s.tmp);
+  if (ctas > 1) cluster_wait();     // every CTA of the cluster runs before its memory is written
   if (tid < ctas) {
     const float w[6] = {big, rest, in, cross, tsum, __uint_as_float(s.flags)};
     for (int i = 0; i < 6; ++i) st_remote(at_rank(&s.post[rank][i], tid), w[i]);
@@ -370,21 +383,26 @@ int done(cudaError_t e) { return e == cudaSuccess && cudaGetLastError() == cudaS
 
 }  // namespace
 
-int launch_distill(const DistillArgs& a, cudaStream_t st) {
-  const int ctas = row_ctas(a.x.rows, a.x.V);
-  const auto f = a.x.dtype == DF_F32 ? distill_kernel<float> : distill_kernel<uint16_t>;
+template <void (*KERNEL)(DistillArgs, int)>
+static int launch_loss(const DistillArgs& a, int ctas, cudaStream_t st) {
+  static std::atomic<unsigned long long> done_{0};
+  // one bit for each element of a CTA's part; a part is at most 2^18 elements and a piece or two
   const size_t smem = sizeof(Shared) + ((size_t)(a.x.V + 16) / ctas + 64) / 8 + 16;
-  if (ensure_dynamic_smem(f, smem) != cudaSuccess || prefer_shared(f) != cudaSuccess) return DF_ERR_CUDA;
+  if (prepare_kernel(reinterpret_cast<const void*>(KERNEL), sizeof(Shared) + (1 << 15) + 64, done_) != cudaSuccess)
+    return DF_ERR_CUDA;
   DF_TRACE("distill", st);
-  return done(launch_cluster(f, (unsigned)a.x.rows * ctas, ctas, smem, st, a, ctas));
+  return done(launch_cluster(KERNEL, (unsigned)a.x.rows * ctas, ctas, smem, st, a, ctas));
+}
+int launch_distill(const DistillArgs& a, cudaStream_t st) {
+  const int ctas = row_ctas(a.x.rows, a.x.V, num_sms());
+  return a.x.dtype == DF_F32 ? launch_loss<distill_kernel<float>>(a, ctas, st) : launch_loss<distill_kernel<uint16_t>>(a, ctas, st);
 }
 int launch_distill_backward(const DistillArgs& a, cudaStream_t st) {
-  const int ctas = row_ctas(a.x.rows, a.x.V);
+  const int ctas = row_ctas(a.x.rows, a.x.V, num_sms());
   const auto f = a.x.dtype == DF_F32 ? distill_backward_kernel<float> : distill_backward_kernel<uint16_t>;
   DF_TRACE("distill_backward", st);
   return done(launch_k(f, dim3((unsigned)a.x.rows * ctas), dim3(kRowThreads), 0, st, a, ctas));
 }
-
 int launch_path_rows(int b, int D, int n_tree, const int32_t* n_new, const int32_t* src_slot, int max_src,
                      const int32_t* cache_len, int32_t* teacher_row, cudaStream_t st) {
   DF_TRACE("path_rows", st);

@@ -56,7 +56,8 @@ int launch_distill_backward(const DistillArgs& a, cudaStream_t st);
 int launch_path_rows(int b, int D, int n_tree, const int32_t* n_new, const int32_t* src_slot, int max_src,
                      const int32_t* cache_len, int32_t* teacher_row, cudaStream_t st);
 
-// CTAs that share a row of V logits, for this many rows: a power of two up to 8 (one cluster).
-int row_ctas(int rows, int V);
+// CTAs that share a row of V logits, for this many rows on a GPU of so many SMs: a power of two up
+// to 8 (one cluster).
+int row_ctas(int rows, int V, int sms);
 
 }  // namespace df

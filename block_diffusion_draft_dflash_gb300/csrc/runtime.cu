@@ -1,7 +1,6 @@
 // Per-device host state (see runtime.h).
 #include <map>
 #include <mutex>
-#include <set>
 #include <utility>
 
 #include "runtime.h"
@@ -11,7 +10,6 @@ namespace {
 std::mutex mu;
 std::map<int, int> sm_count;                                // device -> SMs
 std::map<std::pair<int, const void*>, size_t> smem_set;     // (device, kernel) -> bytes allowed
-std::set<std::pair<int, const void*>> shared_preferred;     // (device, kernel) told prefer_shared
 
 int current_device() {
   int dev = 0;
@@ -44,13 +42,15 @@ cudaError_t ensure_dynamic_smem(const void* func, size_t bytes) {
   return e;
 }
 
-cudaError_t prefer_shared(const void* func) {
+cudaError_t prepare_kernel(const void* func, size_t bytes, std::atomic<unsigned long long>& done) {
   const int dev = current_device();
   if (dev < 0) return cudaErrorInvalidDevice;
-  std::lock_guard<std::mutex> g(mu);
-  if (shared_preferred.count({dev, func})) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(func, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-  if (e == cudaSuccess) shared_preferred.insert({dev, func});
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  cudaError_t e = ensure_dynamic_smem(func, bytes);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(func, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
   return e;
 }
 

@@ -6,6 +6,8 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 namespace df {
 
 // SM count of the current device (cached per device).
@@ -22,13 +24,9 @@ cudaError_t ensure_dynamic_smem(F* func, size_t bytes) {
   return ensure_dynamic_smem(reinterpret_cast<const void*>(func), bytes);
 }
 
-// Asks for the largest shared-memory part of the SM's memory for `func` (once per device and
-// kernel): without it the split that is chosen may hold one CTA where the registers allow more.
-cudaError_t prefer_shared(const void* func);
-
-template <typename F>
-cudaError_t prefer_shared(F* func) {
-  return prefer_shared(reinterpret_cast<const void*>(func));
-}
+// Both for a kernel whose dynamic shared memory does not grow: the opt-in for `bytes`, and the
+// largest shared-memory part of the SM's memory (without it the split that is chosen may hold one
+// CTA where the registers allow more).  `done` keeps a bit for each device that has them.
+cudaError_t prepare_kernel(const void* func, size_t bytes, std::atomic<unsigned long long>& done);
 
 }  // namespace df

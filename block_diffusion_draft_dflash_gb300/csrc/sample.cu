@@ -1202,12 +1202,13 @@ __global__ void __launch_bounds__(kRowThreads, SEARCH ? 2 : 4) sample_kernel(Sam
   // Every CTA finds the first tokens of its own part, if they are few; else the row's are found together.
   const bool parts = st.by_mass || (st.by_k && st.k <= kFewTop);
   if (tid == 0) s.n_list = s.live = 0;
-  if (ctas > 1) row_sync(ctas);   // every CTA of the cluster runs before its memory is written
+  if (ctas > 1) cluster_arrive();
   const float c = 1.44269504f / st.T;
   uint32_t big = 0, key_low = 0;
   if (st.by_mass) {
     uint32_t live;
     w.template read_tops<true>(c, count, &live);
+    if (ctas > 1) cluster_wait();   // every CTA of the cluster runs before its memory is written
     w.template list_part<true>(kLikely / ctas + 8, c);
     if (count) {
       live = block_add(live, s.tmp32);
@@ -1215,6 +1216,7 @@ __global__ void __launch_bounds__(kRowThreads, SEARCH ? 2 : 4) sample_kernel(Sam
     }
   } else {
     w.template read_tops<false>(0.f, false, nullptr);
+    if (ctas > 1) cluster_wait();
     if (parts) {
       w.template list_part<false>(st.k, 0.f);
     } else {
@@ -1358,11 +1360,12 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a, i
     }
   };
   if (tid == 0) s.n_list = 0;
-  if (ctas > 1) row_sync(ctas);
+  if (ctas > 1) cluster_arrive();
   uint32_t live, big = 0;
   const float c = 1.44269504f / a.temperature;
   const bool parts = K <= kFewTop;
   w.template read_tops<true>(c, false, &live);
+  if (ctas > 1) cluster_wait();     // every CTA of the cluster runs before its memory is written
   if (parts) {
     w.give_sum(key_float(w.template list_part<false>(K, 0.f)), c);
   } else {
@@ -1454,37 +1457,40 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a, i
   }
 }
 
-template <class A, class F>
-int launch_rows(F f, const A& a, int clusters, int ctas, const char* tag, cudaStream_t st) {
-  if (ensure_dynamic_smem(f, sizeof(Shared)) != cudaSuccess || prefer_shared(f) != cudaSuccess) return DF_ERR_CUDA;
+template <class A, void (*KERNEL)(A, int)>
+int launch_rows(const A& a, int clusters, int ctas, const char* tag, cudaStream_t st) {
+  static std::atomic<unsigned long long> done{0};
+  if (prepare_kernel(reinterpret_cast<const void*>(KERNEL), sizeof(Shared), done) != cudaSuccess) return DF_ERR_CUDA;
   DF_TRACE(tag, st);
-  if (launch_cluster(f, (unsigned)clusters * ctas, ctas, sizeof(Shared), st, a, ctas) != cudaSuccess) return DF_ERR_CUDA;
+  if (launch_cluster(KERNEL, (unsigned)clusters * ctas, ctas, sizeof(Shared), st, a, ctas) != cudaSuccess) return DF_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? DF_OK : DF_ERR_CUDA;
+}
+
+template <class E>
+int launch_draws(const SampleArgs& a, cudaStream_t st) {
+  const int rows = a.x.rows, sms = num_sms(), ctas = row_ctas(rows, a.x.V, sms), most = row_ctas(1, a.x.V, sms);
+  // Few rows have all the CTAs that a search wants from the start; among many, rows to be searched
+  // get them from a second launch.
+  if (ctas == most) return launch_rows<SampleArgs, sample_kernel<E, true>>(a, rows, ctas, "sample", st);
+  const int rc = launch_rows<SampleArgs, sample_kernel<E, false>>(a, rows, ctas, "sample", st);
+  if (rc != DF_OK) return rc;
+  return launch_rows<SampleArgs, search_kernel<E>>(a, std::min(rows, 4 * sms / most), most, "sample_search", st);
 }
 
 }  // namespace
 
 int launch_sample(const SampleArgs& a, cudaStream_t st) {
-  const int rows = a.x.rows, ctas = row_ctas(rows, a.x.V);
-  const bool f32 = a.x.dtype == DF_F32;
-  // Few rows have all the CTAs that a search wants from the start; among many, rows to be searched
-  // get them from a second launch.
-  const int most = row_ctas(1, a.x.V);
-  if (ctas == most)
-    return launch_rows(f32 ? sample_kernel<float, true> : sample_kernel<uint16_t, true>, a, rows, ctas, "sample", st);
-  const int rc = launch_rows(f32 ? sample_kernel<float, false> : sample_kernel<uint16_t, false>, a, rows, ctas, "sample", st);
-  if (rc != DF_OK) return rc;
-  return launch_rows(f32 ? search_kernel<float> : search_kernel<uint16_t>, a, std::min(rows, 4 * num_sms() / most), most,
-                     "sample_search", st);
+  return a.x.dtype == DF_F32 ? launch_draws<float>(a, st) : launch_draws<uint16_t>(a, st);
 }
 int launch_top_logits(const TopArgs& a, cudaStream_t st) {
-  return launch_rows(a.x.dtype == DF_F32 ? top_logits_kernel<float> : top_logits_kernel<uint16_t>, a, a.x.rows,
-                     row_ctas(a.x.rows, a.x.V), "top_logits", st);
+  const int ctas = row_ctas(a.x.rows, a.x.V, num_sms());
+  return a.x.dtype == DF_F32 ? launch_rows<TopArgs, top_logits_kernel<float>>(a, a.x.rows, ctas, "top_logits", st)
+                             : launch_rows<TopArgs, top_logits_kernel<uint16_t>>(a, a.x.rows, ctas, "top_logits", st);
 }
 
-int row_ctas(int rows, int V) {
+int row_ctas(int rows, int V, int sms) {
   int c = 1;
-  while (c < 8 && (long long)rows * c < 2LL * num_sms() && V >= 4096 * c) c *= 2;
+  while (c < 8 && (long long)rows * c < 2LL * sms && V >= 4096 * c) c *= 2;
   while (c < 8 && V > (1 << 18) * c) c *= 2;   // a thread's sums and a CTA's bitmap are made for 2^18 elements
   return c;
 }
