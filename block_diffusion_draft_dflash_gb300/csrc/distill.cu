@@ -393,12 +393,20 @@ static int launch_loss(const DistillArgs& a, int ctas, cudaStream_t st) {
   DF_TRACE("distill", st);
   return done(launch_cluster(KERNEL, (unsigned)a.x.rows * ctas, ctas, smem, st, a, ctas));
 }
+// CTAs of all rows that are one wave, or hardly more.
+static int one_wave() { return 2 * num_sms() + num_sms() / 8; }
+
 int launch_distill(const DistillArgs& a, cudaStream_t st) {
-  const int ctas = row_ctas(a.x.rows, a.x.V, num_sms());
+  int ctas = row_ctas(a.x.rows, a.x.V, one_wave());
+  // With the gradient a row is read twice, the second time from L2 if the rows under way fit there:
+  // a CTA has at most about 160 KB of a row (960 rows of 151936 bf16: 2 CTAs 133 us, 1 160; 400 rows
+  // of fp32: 4 CTAs 111 us, 2 135, 1 145).
+  if (a.grad)
+    while (ctas < 8 && (size_t)a.x.V * (a.x.dtype == DF_F32 ? 4 : 2) > ((size_t)160 << 10) * ctas) ctas *= 2;
   return a.x.dtype == DF_F32 ? launch_loss<distill_kernel<float>>(a, ctas, st) : launch_loss<distill_kernel<uint16_t>>(a, ctas, st);
 }
 int launch_distill_backward(const DistillArgs& a, cudaStream_t st) {
-  const int ctas = row_ctas(a.x.rows, a.x.V, num_sms());
+  const int ctas = row_ctas(a.x.rows, a.x.V, one_wave());
   const auto f = a.x.dtype == DF_F32 ? distill_backward_kernel<float> : distill_backward_kernel<uint16_t>;
   DF_TRACE("distill_backward", st);
   return done(launch_k(f, dim3((unsigned)a.x.rows * ctas), dim3(kRowThreads), 0, st, a, ctas));

@@ -56,8 +56,10 @@ int launch_distill_backward(const DistillArgs& a, cudaStream_t st);
 int launch_path_rows(int b, int D, int n_tree, const int32_t* n_new, const int32_t* src_slot, int max_src,
                      const int32_t* cache_len, int32_t* teacher_row, cudaStream_t st);
 
-// CTAs that share a row of V logits, for this many rows on a GPU of so many SMs: a power of two up
-// to 8 (one cluster).
-int row_ctas(int rows, int V, int sms);
+// CTAs that share a row of V logits (one cluster): a power of two up to 8 with which all rows have at
+// most `most` of them, and at least 2048 elements each.  One wave of CTAs that share rows beats a
+// second wave by far (draws of 40 rows of 151936: 4 CTAs each 16 us, 8 of them 27; of 80 rows: 2 CTAs
+// 21 us, 8 of them 41), and more CTAs on a row beat idle SMs (of 20 rows: 1 CTA 18 us, 8 of them 14).
+int row_ctas(int rows, int V, int most);
 
 }  // namespace df

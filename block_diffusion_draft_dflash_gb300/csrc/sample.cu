@@ -1468,7 +1468,7 @@ int launch_rows(const A& a, int clusters, int ctas, const char* tag, cudaStream_
 
 template <class E>
 int launch_draws(const SampleArgs& a, cudaStream_t st) {
-  const int rows = a.x.rows, sms = num_sms(), ctas = row_ctas(rows, a.x.V, sms), most = row_ctas(1, a.x.V, sms);
+  const int rows = a.x.rows, sms = num_sms(), ctas = row_ctas(rows, a.x.V, 2 * sms), most = row_ctas(1, a.x.V, 2 * sms);
   // Few rows have all the CTAs that a search wants from the start; among many, rows to be searched
   // get them from a second launch.
   if (ctas == most) return launch_rows<SampleArgs, sample_kernel<E, true>>(a, rows, ctas, "sample", st);
@@ -1483,14 +1483,14 @@ int launch_sample(const SampleArgs& a, cudaStream_t st) {
   return a.x.dtype == DF_F32 ? launch_draws<float>(a, st) : launch_draws<uint16_t>(a, st);
 }
 int launch_top_logits(const TopArgs& a, cudaStream_t st) {
-  const int ctas = row_ctas(a.x.rows, a.x.V, num_sms());
+  const int ctas = row_ctas(a.x.rows, a.x.V, 2 * num_sms());
   return a.x.dtype == DF_F32 ? launch_rows<TopArgs, top_logits_kernel<float>>(a, a.x.rows, ctas, "top_logits", st)
                              : launch_rows<TopArgs, top_logits_kernel<uint16_t>>(a, a.x.rows, ctas, "top_logits", st);
 }
 
-int row_ctas(int rows, int V, int sms) {
+int row_ctas(int rows, int V, int most) {
   int c = 1;
-  while (c < 8 && (long long)rows * c < 2LL * sms && V >= 4096 * c) c *= 2;
+  while (c < 8 && (long long)rows * c * 2 <= most && V >= 4096 * c) c *= 2;
   while (c < 8 && V > (1 << 18) * c) c *= 2;   // a thread's sums and a CTA's bitmap are made for 2^18 elements
   return c;
 }
