@@ -31,7 +31,7 @@ constexpr int kListCap = 2048;     // tokens that one CTA sorts
 constexpr int kHalf = kListCap / 2;
 constexpr int kMaxTop = 1024;      // top-k and K that the list of the first tokens is used for
 constexpr int kFewTop = 64;        // up to this many, every CTA finds its own part's first ones
-constexpr int kLikely = 128;       // tokens listed (about) where mass alone decides
+constexpr int kLikely = 64;        // tokens listed (about) where mass alone decides
 constexpr int kBuckets = 512;      // of threshold() and sort_list()
 constexpr int kBins = 2048;
 constexpr int kBinBits = 11;
@@ -72,7 +72,7 @@ struct Shared {
   uint32_t tmp32[kRowWarps];
   float tmpf[kRowWarps];
   uint64_t found_comp, found_mass;
-  uint32_t found_n, found, n_chosen;
+  uint32_t found_n, found, n_chosen, window[6];
   uint16_t rows[kRowThreads];
 };
 
@@ -567,21 +567,28 @@ struct RowWork {
     }
     row_sync(ctas);
     if (rank != 0) return;
-    constexpr int PER = kBins / kRowThreads;
+    constexpr int PER = kBins / kRowThreads / 4;
+    uint4* const counts = reinterpret_cast<uint4*>(s.bins.count) + tid * PER;
+    float4* const masses = reinterpret_cast<float4*>(s.bins.mass) + tid * PER;
     uint32_t n = 0, all_n;
     float m = 0.f, all;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-      n += s.bins.count[tid * PER + j];
-      m += s.bins.mass[tid * PER + j];
+      const uint4 c = counts[j];
+      const float4 e = masses[j];
+      n += (c.x + c.y) + (c.z + c.w);
+      m += (e.x + e.y) + (e.z + e.w);
     }
     n = block_scan(n, s.tmp32, &all_n);
     m = block_scan(m, s.tmpf, &all);
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-      const int b = tid * PER + j;
-      s.bins.count[b] = n += s.bins.count[b];
-      s.bins.mass[b] = m += s.bins.mass[b];
+      uint4 c = counts[j];
+      float4 e = masses[j];
+      n = c.w = (c.z = (c.y = (c.x += n) + c.y) + c.z) + c.w;
+      m = e.w = (e.z = (e.y = (e.x += m) + e.y) + e.z) + e.w;
+      counts[j] = c;
+      masses[j] = e;
     }
     __syncthreads();
   }
@@ -637,35 +644,42 @@ struct RowWork {
     uint32_t first, last, n0;
     uint64_t m0, m1;
   };
-  // First CTA: the bin where the border should be (exactly, for a count), with some around it as
-  // far as their tokens fit in the list.  Words 0, 1: first and last bin, 2: their tokens.
-  DF_DEV void choose(const Window& v, int tries, bool by_count, uint32_t want_n, uint64_t want,
-                     uint32_t* w, uint32_t room = kListCap, uint32_t around = kAround) {
-    constexpr int PER = kBins / kRowThreads;
-    const float e0 = v.first ? s.bins.mass[v.first - 1] : 0.f, e1 = s.bins.mass[v.last];
-    const float e = e0 + (float)(want - v.m0) / (float)(v.m1 - v.m0) * (e1 - e0);
-    uint32_t at = 0;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int b = tid * PER + j;
-      at += by_count ? v.n0 + s.bins.count[b] < want_n : s.bins.mass[b] < e;
+  // The number of bins whose running sum is below `upto`.
+  template <class V>
+  static DF_DEV uint32_t bins_below(const V* sum, V upto) {
+    uint32_t n = 0;
+#pragma unroll 1
+    for (uint32_t step = kBins; step; step >>= 1)
+      if (n + step <= kBins && sum[n + step - 1] < upto) n += step;
+    return n;
+  }
+  // A thread of the first CTA: the bin where the border should be (exactly, for a count), with some
+  // around it as far as their tokens fit in `room`.  w: first and last bin, their tokens.
+  DF_DEV void choose(const Window& v, int tries, bool by_count, uint32_t want_n, uint64_t want, uint32_t* w,
+                     uint32_t room = kListCap, uint32_t around = kAround) {
+    const uint32_t* const count = s.bins.count;
+    uint32_t at;
+    if (by_count) {
+      at = bins_below(count, want_n - v.n0);
+    } else {
+      const float e0 = v.first ? s.bins.mass[v.first - 1] : 0.f, e1 = s.bins.mass[v.last];
+      at = bins_below((const float*)s.bins.mass, e0 + (float)(want - v.m0) / (float)(v.m1 - v.m0) * (e1 - e0));
+      if (tries >= 3) at = v.first + (v.last - v.first) / 2;   // the masses mislead
     }
-    at = min(max(block_add(at, s.tmp32), v.first), v.last);
-    if (!by_count && tries >= 3) at = v.first + (v.last - v.first) / 2;   // the masses mislead
-    const uint32_t upto = s.bins.count[at], before = at ? s.bins.count[at - 1] : 0;
-    uint32_t less = 0, more = 0;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const uint32_t b = tid * PER + j, c0 = b ? s.bins.count[b - 1] : 0;
-      less += b >= v.first && b < at && before - c0 <= around;
-      more += b > at && b <= v.last && s.bins.count[b] - upto <= around;
+    at = min(max(at, v.first), v.last);
+    const uint32_t upto = count[at], before = at ? count[at - 1] : 0;
+    uint32_t lo = at, hi = at;
+    if (!by_count && upto - before <= room - 2 * around) {
+      // bins from which at most `around` tokens lie before `at`, and up to which behind it
+      lo = before > around ? bins_below(count, before - around) + 1 : 0;
+      hi = bins_below(count, upto + around + 1);
+      lo = min(max(lo, v.first), at);
+      hi = max(min(hi, kBins) - (hi > 0), at);
+      hi = min(hi, v.last);
     }
-    less = block_add(less, s.tmp32);
-    more = block_add(more, s.tmp32);
-    if (by_count || upto - before > room - 2 * around) less = more = 0;
-    w[0] = at - less;
-    w[1] = at + more;
-    w[2] = s.bins.count[w[1]] - (w[0] ? s.bins.count[w[0] - 1] : 0);
+    w[0] = lo;
+    w[1] = hi;
+    w[2] = count[hi] - (lo ? count[lo - 1] : 0);
   }
   // All CTAs: mass before the window (s.mass); its tokens on the list if they fit, else their mass
   // (s.mass_in) and range of keys.  bin(l, key): a logit's bin of this level, above kBins: none,
@@ -728,7 +742,9 @@ struct RowWork {
     for (int tries = 0; tries < 16; ++tries) {
       uint32_t w[3];
       if (rank == 0) {
-        choose(*lv, tries, by_count, want_n, want, w);
+        if (tid == 0) choose(*lv, tries, by_count, want_n, want, s.window);
+        __syncthreads();
+        for (int i = 0; i < 3; ++i) w[i] = s.window[i];
         tell(w, 3);
       }
       if (tid == 0) s.mass = s.mass_in = 0, s.n_list = 0, s.key_min = 0xFFFFFFFFu, s.key_max = 0;
@@ -876,8 +892,9 @@ struct RowWork {
     if (rank == 0) {
       const Window all{0, kBins - 1, 0, 0, m_about};
       const uint64_t keep = p < 1.f ? mass_share(p, m_about) : m_about;
-      choose(all, 0, false, 0, keep, w, kHalf, kHalf / 8);
-      choose(all, 0, false, 0, mass_above(u, keep), w + 3, kHalf, kHalf / 8);
+      if (tid < 2) choose(all, 0, false, 0, tid == 0 ? keep : mass_above(u, keep), s.window + 3 * tid, kHalf, kHalf / 8);
+      __syncthreads();
+      for (int i = 0; i < 6; ++i) w[i] = s.window[i];
 #pragma unroll
       for (int i = 0; i < 6; i += 3)
         if (w[i + 2] > kHalf || (i == 0 && p >= 1.f)) w[i] = 1, w[i + 1] = 0;     // not listed
