@@ -669,7 +669,8 @@ struct RowWork {
     at = min(max(at, v.first), v.last);
     const uint32_t upto = count[at], before = at ? count[at - 1] : 0;
     uint32_t lo = at, hi = at;
-    if (!by_count && upto - before <= room - 2 * around) {
+    if (!by_count && upto - before < room) {
+      around = min(around, (room - (upto - before)) / 2);
       // bins from which at most `around` tokens lie before `at`, and up to which behind it
       lo = before > around ? bins_below(count, before - around) + 1 : 0;
       hi = bins_below(count, upto + around + 1);
@@ -892,7 +893,7 @@ struct RowWork {
     if (rank == 0) {
       const Window all{0, kBins - 1, 0, 0, m_about};
       const uint64_t keep = p < 1.f ? mass_share(p, m_about) : m_about;
-      if (tid < 2) choose(all, 0, false, 0, tid == 0 ? keep : mass_above(u, keep), s.window + 3 * tid, kHalf, kHalf / 8);
+      if (tid < 2) choose(all, 0, false, 0, tid == 0 ? keep : mass_above(u, keep), s.window + 3 * tid, kHalf, kHalf);
       __syncthreads();
       for (int i = 0; i < 6; ++i) w[i] = s.window[i];
 #pragma unroll
@@ -1321,7 +1322,7 @@ __global__ void __launch_bounds__(kRowThreads, SEARCH ? 2 : 4) sample_kernel(Sam
 
 // grid: clusters that take the rows left by sample_kernel in turn.
 template <class E>
-__global__ void __launch_bounds__(kRowThreads, 4) search_kernel(SampleArgs a, int ctas) {
+__global__ void __launch_bounds__(kRowThreads, 2) search_kernel(SampleArgs a, int ctas) {
   extern __shared__ __align__(16) unsigned char smem[];
   Shared& s = *reinterpret_cast<Shared*>(smem);
   pdl_wait();
@@ -1491,7 +1492,11 @@ int launch_draws(const SampleArgs& a, cudaStream_t st) {
   if (ctas == most) return launch_rows<SampleArgs, sample_kernel<E, true>>(a, rows, ctas, "sample", st);
   const int rc = launch_rows<SampleArgs, sample_kernel<E, false>>(a, rows, ctas, "sample", st);
   if (rc != DF_OK) return rc;
-  return launch_rows<SampleArgs, search_kernel<E>>(a, std::min(rows, 4 * sms / most), most, "sample_search", st);
+  // Clusters of 4, as many as are resident at two CTAs to an SM (of 8 and at four CTAs, the last
+  // clusters began when others were through: 73 rows of 151936, 190 us against 173; 114 of 2064,
+  // 222 against 187).
+  const int search = std::min(most, 4);
+  return launch_rows<SampleArgs, search_kernel<E>>(a, std::min(rows, 2 * sms / search), search, "sample_search", st);
 }
 
 }  // namespace
