@@ -880,9 +880,9 @@ struct RowWork {
     hand_over(&s.n_list2, s.list + kHalf, kHalf);
   }
   // The borders of top-p (p < 1) and of the draw, in one pass over all masses; m_about: about the
-  // row's.  True: *kept and *drawn are right (first CTA); else the row's exact mass is in *total
-  // and bins are counted, for locate().
-  __device__ __noinline__ bool two_borders(float p, float u, uint64_t m_about, uint64_t* total, uint32_t* live, Border* kept,
+  // row's.  Bit 0: *kept is right, bit 1: *drawn too (first CTA); for what is not, the row's exact
+  // mass is in *total and bins are counted, for locate().
+  __device__ __noinline__ uint32_t two_borders(float p, float u, uint64_t m_about, uint64_t* total, uint32_t* live, Border* kept,
                                            Border* drawn) {
     if (tid == 0) s.mass = s.mass_in = s.mass_2 = 0;
     load_table();
@@ -921,16 +921,18 @@ struct RowWork {
           yes = border_in_list(s.list, n, w[0] ? s.bins.count[w[0] - 1] : 0, before_a, false, 0, mass_share(p, m), &after, kept);
         }
       }
+      ok = yes;
       if (yes && w[3] <= w[4]) {
         const int n = (int)min(s.n_list2, (uint32_t)kHalf);
         sort_list(s.list + kHalf, n);
-        ok = border_in_list(s.list + kHalf, n, w[3] ? s.bins.count[w[3] - 1] : 0, before_d, false, 0,
-                            mass_above(u, kept->mass), &after, drawn);
+        if (border_in_list(s.list + kHalf, n, w[3] ? s.bins.count[w[3] - 1] : 0, before_d, false, 0,
+                           mass_above(u, kept->mass), &after, drawn))
+          ok = 3;
       }
       if (tid < ctas) st_remote(at_rank(&s.word[7], tid), ok);
     }
     row_sync(ctas);
-    return s.word[7] != 0;
+    return s.word[7];
   }
 
   // All tokens of the bin have one key: in order of their ids.
@@ -1145,12 +1147,12 @@ __device__ __noinline__ void search_row(RowWork<E>& w, const SampleArgs& a, int 
   uint64_t total = 0;
   uint32_t live = 0;
   Border kept{0, 0, 0}, drawn{0, 0, 0};
-  bool done = false;
+  uint32_t done = 0;
   if (about && st.by_mass && st.low == 0.f)
     done = w.two_borders(st.p, st.u, about, &total, &live, &kept, &drawn);
   else
     w.count_all(&total, &live);
-  if (!done) {
+  if (done == 0) {
     kept = Border{0, total, live};
     if (st.k > 0) {
       const Border b = w.locate(true, min((uint32_t)st.k, live), 0, total);
@@ -1184,8 +1186,8 @@ __device__ __noinline__ void search_row(RowWork<E>& w, const SampleArgs& a, int 
       row_sync(w.ctas);
       if (w.rank == 0 && s.n_list < kept.n) kept = Border{0, s.mass, s.n_list};
     }
-    drawn = w.locate(false, 0, mass_above(st.u, kept.mass), total);
   }
+  if (done < 3) drawn = w.locate(false, 0, mass_above(st.u, kept.mass), total);
   if (w.rank == 0 && w.tid == 0) {
     const float l = key_float(key_of(drawn.comp));
     give_row(a, r, id_of(drawn.comp), log_share(w.scale, l, mass_of(w.scale, l), kept.mass), (int32_t)kept.n);
