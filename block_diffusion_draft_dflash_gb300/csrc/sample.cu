@@ -72,7 +72,7 @@ struct Shared {
   uint32_t tmp32[kRowWarps];
   float tmpf[kRowWarps];
   uint64_t found_comp, found_mass;
-  uint32_t found_n, found, n_chosen, window[6];
+  uint32_t found_n, found, n_chosen[kRowWarps], window[6];
   uint16_t rows[kRowThreads];
 };
 
@@ -145,7 +145,8 @@ struct RowWork {
   // -------------------------------------------------------------------------- the first tokens
   float top[kSub];     // largest logits of this thread's groups (the first kSub / ctas)
   float sum[kSub];     // with SUMS: their sums of 2^(l c - ref)
-  float ref;           // an exponent at most 8 below that of the thread's largest logit
+  float ref;           // an exponent at most 8 below that of the thread's largest logit; inf: that of `far`
+  float far;
 
   // Reads the row.  SUMS: also the groups' sums, and with `count` the number of logits above -inf.
   template <bool SUMS>
@@ -161,10 +162,20 @@ struct RowWork {
       if (y > ref + 8.f) {              // also the first time
         const float f = ref > -INFINITY ? ex2_approx(ref - y) : 0.f;
 #pragma unroll
-        for (int j = 0; j < kSub; ++j) sum[j] *= f;
+        for (int j = 0; j < kSub; ++j) sum[j] = f > 0.f ? sum[j] * f : 0.f;     // a sum may be infinite, see sum_far
         ref = y;
       }
-      if (!(ref > -INFINITY)) return;
+      if (!(ref > -INFINITY)) {         // nothing, or l c overflows
+        if (count && big > -INFINITY)
+#pragma unroll
+          for (int j = 0; j < n; ++j) {
+            float x[VE];
+            RowOf<E>::unpack(v[j], x);
+#pragma unroll
+            for (int e = 0; e < VE; ++e) n_live += x[e] > -INFINITY;
+          }
+        return;
+      }
 #pragma unroll
       for (int j = 0; j < n; ++j) {
         float x[VE];
@@ -208,6 +219,31 @@ struct RowWork {
 #pragma unroll
     for (int j = 0; j < kSub; ++j) top[j] = m[j];
     if (SUMS) *live = n_live;
+    if (SUMS && !(fabsf(ref) < 0x1p24f)) sum_far(c);     // also a thread without logits
+  }
+  // The sums of a thread for which l c is too large a number: as a float it is off by so much that
+  // 2^(l c - ref) may overflow, or it overflows itself.  Relative to the thread's largest logit.
+  __device__ __noinline__ void sum_far(float c) {
+    float m = -INFINITY;
+    for (int g = 0; g < kSub; ++g) m = fmaxf(m, top[g]);
+    ref = -INFINITY;
+    if (!(m > -INFINITY)) return;
+    ref = INFINITY;
+    far = m;
+    auto add = [&](const uint4& v, float* to) {
+      float x[VE];
+      RowOf<E>::unpack(v, x);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) *to += ex2_approx((x[e] - m) * c);
+    };
+#pragma unroll 1
+    for (int g = 0; g < kSub; ++g) {
+      sum[g] = 0.f;
+#pragma unroll 1
+      for (int i = part.lo + tid + g * kRowThreads; i < part.hi; i += kSub * kRowThreads) add(part.pieces[i], &sum[g]);
+    }
+    const int edge = part.my_edge();
+    if (edge >= 0) add(part.edge(edge), &sum[0]);
   }
   static DF_DEV uint32_t top_key(float l) { return l == l ? logit_key(l) : 0xFFFFFFFFu; }
 
@@ -332,22 +368,31 @@ struct RowWork {
   // kRowThreads, ..., who = the thread + its group * kRowThreads.)
   template <bool SUMS>
   DF_DEV void list_tops(uint32_t least, float largest, float c) {
-    const int lane = tid & 31;
+    const int lane = tid & 31, warp = tid / 32;
     float tail = 0.f;
-    if (tid == 0) s.n_chosen = 0;
-    __syncthreads();
+    uint32_t who[kSub], at = 0;
 #pragma unroll
     for (int g = 0; g < kSub; ++g) {
       const bool yes = logit_key(top[g]) >= least;
       if (SUMS && !yes) tail += sum[g];
-      const uint32_t who = __ballot_sync(0xffffffffu, yes);
-      if (who == 0) continue;
-      uint32_t at = 0;
-      if (lane == 0) at = atomicAdd(&s.n_chosen, (uint32_t)__popc(who));
-      at = __shfl_sync(0xffffffffu, at, 0);
-      if (yes) s.chosen[at + __popc(who & ((1u << lane) - 1))] = (uint16_t)(g * kRowThreads + tid);
+      who[g] = __ballot_sync(0xffffffffu, yes);
+      at += __popc(who[g]);
     }
+    // in a fixed order, on which the rounding of the threads' sums depends
+    if (lane == 0) s.n_chosen[warp] = at;
     if (SUMS) tail *= over_largest(largest, c);
+    __syncthreads();
+    uint32_t n_chosen = 0;
+#pragma unroll
+    for (int w = 0; w < kRowWarps; ++w) {
+      if (w == warp) at = n_chosen;
+      n_chosen += s.n_chosen[w];
+    }
+#pragma unroll
+    for (int g = 0; g < kSub; ++g) {
+      if (who[g] >> lane & 1u) s.chosen[at + __popc(who[g] & ((1u << lane) - 1))] = (uint16_t)(g * kRowThreads + tid);
+      at += __popc(who[g]);
+    }
     __syncthreads();
     auto look = [&](const uint4& v, int piece) {
       const bool any = logit_key(RowOf<E>::largest(v)) >= least;
@@ -368,7 +413,7 @@ struct RowWork {
       if (SUMS) tail += t;
     };
     const int each = (part.hi - part.lo + kSub * kRowThreads - 1) / (kSub * kRowThreads);   // pieces of a group
-    const int n = (int)s.n_chosen * each;
+    const int n = (int)n_chosen * each;
     for (int q0 = tid; q0 < n; q0 += 4 * kRowThreads) {
       uint4 v[4];
       int piece[4];
@@ -395,6 +440,7 @@ struct RowWork {
   }
   // 2^(ref - largest c): ref is a float, l c - ref in the sums is rounded once, and so is this.
   DF_DEV float over_largest(float largest, float c) const {
+    if (ref == INFINITY) return ex2_approx((far - largest) * c);
     return ref > -INFINITY ? ex2_approx(fmaf(-largest, c, ref)) : 0.f;
   }
   // The part's sum relative to its largest logit, in the first CTA: sums.
