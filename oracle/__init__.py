@@ -42,6 +42,11 @@ Parity pins (see tests/test_oracle_*.py):
   kv4 (KV cache held in 4 bits; no counterpart in the pages) rounding against every
                           candidate and torch's e4m3, attention against torch's, weights
                           sum to the rows, eviction by brute force over subsets.  PINNED
+  rows (draws under top-k, top-p and min-p, largest logits, distillation; no counterpart in
+                          the pages) filters by their definitions token by token, draw
+                          frequencies = kept probabilities, torch's sort and log-sum,
+                          gradient by differences and by torch's autograd, a student equal
+                          to its teacher has loss and gradient 0.      PINNED
   model.layer_forward     pinned only through the invariants above: the pages
                           print no layer equations or values (a Qwen3-style
                           pre-norm layer is the stated reading).
