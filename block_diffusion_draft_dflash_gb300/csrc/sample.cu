@@ -85,7 +85,8 @@ struct Shared {
   float tmpf[kRowWarps];
   uint64_t found_comp, found_mass;
   uint32_t found_n, found, n_chosen[kRowWarps], window[6];
-  uint16_t rows[kRowThreads];
+  uint32_t n_rows;
+  int rows[kRowThreads];
 };
 
 DF_DEV uint32_t logit_key(float l) { return float_key(l + 0.f); }   // -0 as +0
@@ -1389,20 +1390,33 @@ __global__ void __launch_bounds__(kRowThreads, 2) search_kernel(SampleArgs a, in
   pdl_trigger();
   const int rank = ctas == 1 ? 0 : (int)cluster_rank(), tid = threadIdx.x;
   const int me = blockIdx.x / ctas, all = gridDim.x / ctas;
-  int seen = 0;           // rows left so far, modulo the clusters
+  uint32_t mine = 0, n;
+#pragma unroll 4
+  for (int r = tid; r < a.x.rows; r += kRowThreads) mine += a.left[r].on;
+  const uint32_t before = block_scan(mine, s.tmp32, &n);
   bool first = true;
-  for (int r0 = 0; r0 < a.x.rows; r0 += kRowThreads) {
-    const bool mine = r0 + tid < a.x.rows && a.left[r0 + tid].on;
-    uint32_t n;
-    const uint32_t at = block_scan((uint32_t)mine, s.tmp32, &n);
-    if (n == 0) continue;
+  // this cluster's rows: of all that are left, in the threads' order, me, me + all, ...
+  for (uint32_t from = 0; from < n; from += (uint32_t)all * kRowThreads) {
     __syncthreads();
-    if (mine) s.rows[at] = (uint16_t)tid;
+    if (tid == 0) s.n_rows = 0;
     __syncthreads();
-    for (int i = ((me - seen) % all + all) % all; i < (int)n; i += all) {
+    if (mine) {
+      uint32_t at = before;
+      for (int r = tid; r < a.x.rows; r += kRowThreads) {
+        if (!a.left[r].on) continue;
+        const uint32_t q = at++ - from;       // wraps around below `from`
+        if (q < (uint32_t)all * kRowThreads && q % all == (uint32_t)me) {
+          s.rows[q / all] = r;
+          atomicAdd(&s.n_rows, 1u);
+        }
+      }
+    }
+    __syncthreads();
+    const int k = (int)s.n_rows;
+    for (int i = 0; i < k; ++i) {
       row_sync(ctas);     // the last row's memory; every CTA of the cluster runs
       first = false;
-      const int r = r0 + s.rows[i];
+      const int r = s.rows[i];
       const SampleLeft left = a.left[r];
       const Settings st(a, r);
       const RowPart<E> part(static_cast<const E*>(a.x.data), a.x.ld, r, a.x.V, rank, ctas);
@@ -1413,7 +1427,6 @@ __global__ void __launch_bounds__(kRowThreads, 2) search_kernel(SampleArgs a, in
       search_row(w, a, r, st, key_low, left.about);
       __syncthreads();
     }
-    seen = (seen + (int)n) % all;
   }
   // no CTA leaves while another of its cluster may read its memory
   if (!first && ctas > 1) row_sync(ctas);
@@ -1548,14 +1561,17 @@ template <class E>
 int launch_draws(const SampleArgs& a, cudaStream_t st) {
   const int rows = a.x.rows, sms = num_sms(), ctas = row_ctas(rows, a.x.V, 2 * sms), most = row_ctas(1, a.x.V, 2 * sms);
   // Few rows have all the CTAs that a search wants from the start; among many, rows to be searched
-  // get them from a second launch.
-  if (ctas == most) return launch_rows<SampleArgs, sample_kernel<E, true>>(a, rows, ctas, "sample", st);
+  // get them from a second launch (also of small rows: with the search in it a kernel has two CTAs an
+  // SM, without four; 4096 rows of 1000, 193 us against 117).
+  if (ctas == most && (long long)rows * ctas <= 2 * sms)
+    return launch_rows<SampleArgs, sample_kernel<E, true>>(a, rows, ctas, "sample", st);
   const int rc = launch_rows<SampleArgs, sample_kernel<E, false>>(a, rows, ctas, "sample", st);
   if (rc != DF_OK) return rc;
   // Clusters of 4, as many as are resident at two CTAs to an SM (of 8 and at four CTAs, the last
-  // clusters began when others were through: 73 rows of 151936, 190 us against 173; 114 of 2064,
-  // 222 against 187).
-  const int search = std::min(most, 4);
+  // clusters began when others were through: 73 rows of 151936, 190 us against 173); of 2 where so
+  // many rows may be left that clusters of 4 would take them in turns (by mass alone, 1024 rows of
+  // 100000: 335 us against 496, 2064 mixed rows of 151936: 354 against 385; but 256 rows: 299 against 224).
+  const int search = std::max(ctas, std::min(most, rows > 4 * sms ? 2 : 4));
   return launch_rows<SampleArgs, search_kernel<E>>(a, std::min(rows, 2 * sms / search), search, "sample_search", st);
 }
 

@@ -544,6 +544,19 @@ def test_largest_vocabulary(dtype):
                   1.0, 1.0, (1.0,), dtype)
 
 
+@pytest.mark.parametrize("rows,V", [(1500, 9001), (700, 40000), (80000, 300)])
+def test_many_rows_whose_borders_lie_far_behind(rows, V):
+    """Flat rows cut by mass: more of them to search than there are places at once, in all three more than a list holds."""
+    base, u = logits(29, 16, V, spread=0.5, heads=0), np.random.default_rng(7).random(16).astype(np.float32)
+    settings = [(1.0, 0, 0.9, 0.0), (1.0, 0, 1.0, 0.0), (0.8, 0, 0.99, 0.0), (1.0, 2000, 0.95, 0.0)] * 4
+    small, n = held(base, "bf16"), rows // 16 + 1
+    one = check_sample(small, u, settings, 1)
+    got = run_sample(small.repeat(n, 1)[:rows], np.tile(u, n)[:rows], (settings * n)[:rows], 1)
+    assert got[3] == 0
+    for i in (0, 2):
+        assert got[i] == (one[i] * n)[:rows]
+
+
 def test_rows_farther_apart_than_32_bits():
     """Element offsets beyond 2^31 and byte offsets beyond 2^32, of the rows and of the gradient."""
     V, ld = 5001, (1 << 30) + 13
