@@ -52,6 +52,7 @@ constexpr int kSub = 8;            // groups of a thread
 constexpr uint32_t kNone = 1u << 20, kAbove = 1u << 21;   // no bin of a level: below it, above it
 constexpr uint32_t kAround = 512;  // tokens listed on either side of the bin where a border should be
 
+constexpr uint32_t kMaskedKey = 0x0EB60D35u;   // of -1e30: masks by a type's lowest number lie below it
 __device__ const Pow2Table kPow2;
 
 struct Bins {          // running sums over bins: tokens, and about their mass
@@ -331,7 +332,7 @@ struct RowWork {
     for (int j = 0; j < kSub; ++j) {
       key[j] = s.group_key[j * kRowThreads + tid];
       big = max(big, key[j]);
-      if (key[j] > kNegInfKey) small = min(small, key[j]);
+      if (key[j] > kMaskedKey) small = min(small, key[j]);
     }
     __syncthreads();
     big = __reduce_max_sync(0xffffffffu, big);
