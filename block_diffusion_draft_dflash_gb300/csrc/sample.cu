@@ -157,29 +157,33 @@ struct RowWork {
   }
 
   // -------------------------------------------------------------------------- the first tokens
-  float top[kSub];     // largest logits of this thread's groups (the first kSub / ctas)
-  float sum[kSub];     // with SUMS: their sums of 2^(l c - ref)
-  float ref;           // an exponent at most 8 below that of the thread's largest logit; inf: that of `far`
-  float far;
+  // What a thread keeps of its groups (kSub of them, an eighth of its pieces each).  In registers: not
+  // part of RowWork, whose address functions that are not inlined take.
+  struct Tops {
+    float top[kSub];     // their largest logits
+    float sum[kSub];     // with SUMS: their sums of 2^(l c - ref)
+    float ref;           // an exponent at most 8 below that of the thread's largest logit; inf: that of `far`
+    float far;
+  };
 
   // Reads the row.  SUMS: also the groups' sums, and with `count` the number of logits above -inf.
   template <bool SUMS>
-  DF_DEV void read_tops(float c, bool count, uint32_t* live) {
+  DF_DEV void read_tops(Tops& my, float c, bool count, uint32_t* live) {
     float m[kSub];
     uint32_t n_live = 0;
-    ref = -INFINITY;
+    my.ref = -INFINITY, my.far = 0.f;
 #pragma unroll
-    for (int j = 0; j < kSub; ++j) m[j] = -INFINITY, sum[j] = 0.f;
+    for (int j = 0; j < kSub; ++j) m[j] = -INFINITY, my.sum[j] = 0.f;
     // four groups' pieces, largest logit `big`
     auto add = [&](const uint4* v, int n, float big, float* to) {
       const float y = big * c;
-      if (y > ref + 8.f) {              // also the first time
-        const float f = ref > -INFINITY ? ex2_approx(ref - y) : 0.f;
+      if (y > my.ref + 8.f) {              // also the first time
+        const float f = my.ref > -INFINITY ? ex2_approx(my.ref - y) : 0.f;
 #pragma unroll
-        for (int j = 0; j < kSub; ++j) sum[j] = f > 0.f ? sum[j] * f : 0.f;     // a sum may be infinite, see sum_far
-        ref = y;
+        for (int j = 0; j < kSub; ++j) my.sum[j] = f > 0.f ? my.sum[j] * f : 0.f;     // a sum may be infinite, see sum_far
+        my.ref = y;
       }
-      if (!(ref > -INFINITY)) {         // nothing, or l c overflows
+      if (!(my.ref > -INFINITY)) {         // nothing, or l c overflows
         if (count && big > -INFINITY)
 #pragma unroll
           for (int j = 0; j < n; ++j) {
@@ -198,7 +202,7 @@ struct RowWork {
 #pragma unroll
           for (int e = 0; e < VE; ++e) n_live += x[e] > -INFINITY;
 #pragma unroll
-        for (int e = 0; e < VE; ++e) x[e] = ex2_approx(fmaf(x[e], c, -ref));
+        for (int e = 0; e < VE; ++e) x[e] = ex2_approx(fmaf(x[e], c, -my.ref));
 #pragma unroll
         for (int w = VE / 2; w > 0; w >>= 1)
 #pragma unroll
@@ -220,7 +224,7 @@ struct RowWork {
           m[h + j] = max_nan(m[h + j], l);
           if (SUMS) big = fmaxf(big, l);
         }
-        if (SUMS) add(v, U, big, sum + h);
+        if (SUMS) add(v, U, big, my.sum + h);
       }
     }
     const int edge = part.my_edge();       // goes with the thread's first group
@@ -228,22 +232,32 @@ struct RowWork {
       const uint4 v = part.edge(edge);
       const float l = RowOf<E>::largest(v);
       m[0] = max_nan(m[0], l);
-      if (SUMS) add(&v, 1, l, sum);
+      if (SUMS) add(&v, 1, l, my.sum);
     }
 #pragma unroll
-    for (int j = 0; j < kSub; ++j) top[j] = m[j];
+    for (int j = 0; j < kSub; ++j) my.top[j] = m[j];
     if (SUMS) *live = n_live;
-    if (SUMS && !(fabsf(ref) < 0x1p24f)) sum_far(c);     // also a thread without logits
+    if (SUMS && !(fabsf(my.ref) < 0x1p24f)) {     // also a thread without logits
+      float big = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < kSub; ++j) big = fmaxf(big, m[j]);
+      my.ref = -INFINITY;
+      if (big > -INFINITY) {
+        my.ref = INFINITY;
+        my.far = big;
+        const Sums far = sum_far(c, big);
+#pragma unroll
+        for (int j = 0; j < kSub; ++j) my.sum[j] = far.of[j];
+      }
+    }
   }
   // The sums of a thread for which l c is too large a number: as a float it is off by so much that
-  // 2^(l c - ref) may overflow, or it overflows itself.  Relative to the thread's largest logit.
-  __device__ __noinline__ void sum_far(float c) {
-    float m = -INFINITY;
-    for (int g = 0; g < kSub; ++g) m = fmaxf(m, top[g]);
-    ref = -INFINITY;
-    if (!(m > -INFINITY)) return;
-    ref = INFINITY;
-    far = m;
+  // 2^(l c - ref) may overflow, or it overflows itself.  Relative to the thread's largest logit m.
+  struct Sums {
+    float of[kSub];
+  };
+  __device__ __noinline__ Sums sum_far(float c, float m) const {
+    Sums sum;
     auto add = [&](const uint4& v, float* to) {
       float x[VE];
       RowOf<E>::unpack(v, x);
@@ -252,20 +266,21 @@ struct RowWork {
     };
 #pragma unroll 1
     for (int g = 0; g < kSub; ++g) {
-      sum[g] = 0.f;
+      sum.of[g] = 0.f;
 #pragma unroll 1
-      for (int i = part.lo + tid + g * kRowThreads; i < part.hi; i += kSub * kRowThreads) add(part.pieces[i], &sum[g]);
+      for (int i = part.lo + tid + g * kRowThreads; i < part.hi; i += kSub * kRowThreads) add(part.pieces[i], &sum.of[g]);
     }
     const int edge = part.my_edge();
-    if (edge >= 0) add(part.edge(edge), &sum[0]);
+    if (edge >= 0) add(part.edge(edge), &sum.of[0]);
+    return sum;
   }
   static DF_DEV uint32_t top_key(float l) { return l == l ? logit_key(l) : 0xFFFFFFFFu; }
 
   // The groups' keys to the first CTA, those of several CTAs as the largest of `ctas` groups each.
-  DF_DEV void post_groups() {
+  DF_DEV void post_groups(const Tops& my) {
     float m[kSub];
 #pragma unroll
-    for (int j = 0; j < kSub; ++j) m[j] = top[j];
+    for (int j = 0; j < kSub; ++j) m[j] = my.top[j];
     const int sub = kSub / ctas;
 #pragma unroll
     for (int n = kSub / 2; n > 0; n >>= 1)
@@ -279,10 +294,10 @@ struct RowWork {
 
   // This CTA's largest key (*largest), and a key that at least k of its threads reach, or all that
   // have a token: the upper 16 bits of the k-th largest of the threads' keys.  Every warp finds it.
-  DF_DEV uint32_t part_threshold(int k, uint32_t* largest) {
-    float m = top[0];
+  DF_DEV uint32_t part_threshold(const Tops& my, int k, uint32_t* largest) {
+    float m = my.top[0];
 #pragma unroll
-    for (int j = 1; j < kSub; ++j) m = max_nan(m, top[j]);
+    for (int j = 1; j < kSub; ++j) m = max_nan(m, my.top[j]);
     s.hist[tid] = top_key(m);
     __syncthreads();
     uint32_t key[kRowWarps], big = 0, n = 0;
@@ -308,14 +323,14 @@ struct RowWork {
   // key.  In the first CTA:
   // part_max and part_least; with SUMS tail, relative to the part's largest logit.
   template <bool SUMS>
-  DF_DEV uint32_t list_part(int k, float c) {
+  DF_DEV uint32_t list_part(const Tops& my, int k, float c) {
     uint32_t big;
-    const uint32_t least = part_threshold(k, &big);
+    const uint32_t least = part_threshold(my, k, &big);
     if (tid == 0) {
       st_remote(at_rank(&s.part_max[rank], 0), big);
       st_remote(at_rank(&s.part_least[rank], 0), least);
     }
-    list_tops<SUMS>(least, key_float(big), c);
+    list_tops<SUMS>(my, least, key_float(big), c);
     return big;
   }
 
@@ -381,20 +396,20 @@ struct RowWork {
   // on the list has left its rounding there.  (A group's pieces are lo + who, lo + who + kSub *
   // kRowThreads, ..., who = the thread + its group * kRowThreads.)
   template <bool SUMS>
-  DF_DEV void list_tops(uint32_t least, float largest, float c) {
+  DF_DEV void list_tops(const Tops& my, uint32_t least, float largest, float c) {
     const int lane = tid & 31, warp = tid / 32;
     float tail = 0.f;
     uint32_t who[kSub], at = 0;
 #pragma unroll
     for (int g = 0; g < kSub; ++g) {
-      const bool yes = logit_key(top[g]) >= least;
-      if (SUMS && !yes) tail += sum[g];
+      const bool yes = logit_key(my.top[g]) >= least;
+      if (SUMS && !yes) tail += my.sum[g];
       who[g] = __ballot_sync(0xffffffffu, yes);
       at += __popc(who[g]);
     }
     // in a fixed order, on which the rounding of the threads' sums depends
     if (lane == 0) s.n_chosen[warp] = at;
-    if (SUMS) tail *= over_largest(largest, c);
+    if (SUMS) tail *= over_largest(my, largest, c);
     __syncthreads();
     uint32_t n_chosen = 0;
 #pragma unroll
@@ -445,24 +460,24 @@ struct RowWork {
       for (int j = 0; j < 4; ++j) look(v[j], piece[j]);
     }
     const int edge = part.my_edge();
-    if (edge >= 0 && logit_key(top[0]) >= least) look(part.edge(edge), edge);
+    if (edge >= 0 && logit_key(my.top[0]) >= least) look(part.edge(edge), edge);
     if (SUMS) {
       tail = block_add(tail, s.tmpf);
       if (tid == 0) st_remote(at_rank(&s.tail[rank], 0), tail);
     }
     hand_over(&s.n_list, s.list, kListCap);
   }
-  // 2^(ref - largest c): ref is a float, l c - ref in the sums is rounded once, and so is this.
-  DF_DEV float over_largest(float largest, float c) const {
-    if (ref == INFINITY) return ex2_approx((far - largest) * c);
-    return ref > -INFINITY ? ex2_approx(fmaf(-largest, c, ref)) : 0.f;
+  // 2^(my.ref - largest c): ref is a float, l c - ref in the sums is rounded once, and so is this.
+  static DF_DEV float over_largest(const Tops& my, float largest, float c) {
+    if (my.ref == INFINITY) return ex2_approx((my.far - largest) * c);
+    return my.ref > -INFINITY ? ex2_approx(fmaf(-largest, c, my.ref)) : 0.f;
   }
   // The part's sum relative to its largest logit, in the first CTA: sums.
-  DF_DEV void give_sum(float largest, float c) {
+  DF_DEV void give_sum(const Tops& my, float largest, float c) {
     float all = 0.f;
 #pragma unroll
-    for (int g = 0; g < kSub; ++g) all += sum[g];
-    all = block_add(all * over_largest(largest, c), s.tmpf);
+    for (int g = 0; g < kSub; ++g) all += my.sum[g];
+    all = block_add(all * over_largest(my, largest, c), s.tmpf);
     if (tid == 0) st_remote(at_rank(&s.sums[rank], 0), all);
   }
   // What this CTA has put on its own list goes to the first CTA's (which has put its own there).
@@ -1278,6 +1293,7 @@ __global__ void __launch_bounds__(kRowThreads, SEARCH ? 2 : 4) sample_kernel(Sam
   }
   const RowPart<E> part(static_cast<const E*>(a.x.data), a.x.ld, r, a.x.V, rank, ctas);
   RowWork<E> w(s, part, rank, ctas);
+  typename RowWork<E>::Tops my;
   const bool count = st.by_mass && st.p >= 1.f && a.n_kept;
   // Every CTA finds the first tokens of its own part, if they are few; else the row's are found together.
   const bool parts = st.by_mass || (st.by_k && st.k <= kFewTop);
@@ -1287,20 +1303,20 @@ __global__ void __launch_bounds__(kRowThreads, SEARCH ? 2 : 4) sample_kernel(Sam
   uint32_t big = 0, key_low = 0;
   if (st.by_mass) {
     uint32_t live;
-    w.template read_tops<true>(c, count, &live);
+    w.template read_tops<true>(my, c, count, &live);
     if (ctas > 1) cluster_wait();   // every CTA of the cluster runs before its memory is written
-    w.template list_part<true>(kLikely / ctas + 8, c);
+    w.template list_part<true>(my, kLikely / ctas + 8, c);
     if (count) {
       live = block_add(live, s.tmp32);
       if (tid == 0) add_remote(at_rank(&s.live, 0), live);
     }
   } else {
-    w.template read_tops<false>(0.f, false, nullptr);
+    w.template read_tops<false>(my, 0.f, false, nullptr);
     if (ctas > 1) cluster_wait();
     if (parts) {
-      w.template list_part<false>(st.k, 0.f);
+      w.template list_part<false>(my, st.k, 0.f);
     } else {
-      w.post_groups();
+      w.post_groups(my);
       row_sync(ctas);
       if (rank == 0) {
         const uint32_t least = w.threshold(st.by_k ? st.k : 1, &big);
@@ -1313,7 +1329,7 @@ __global__ void __launch_bounds__(kRowThreads, SEARCH ? 2 : 4) sample_kernel(Sam
       if (big > kNegInfKey && big < kPosInfKey && st.k <= kMaxTop) {
         if (st.low > 0.f) key_low = logit_key(least_logit(key_float(big), st.T, st.low, s.tmpf));
         if (st.p >= 1.f) least = st.by_min ? key_low : max(least, key_low);
-        w.template list_tops<false>(least, 0.f, 0.f);
+        w.template list_tops<false>(my, least, 0.f, 0.f);
       }
     }
   }
@@ -1443,6 +1459,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a, i
   const int r = blockIdx.x / ctas, K = a.K;
   const RowPart<E> part(static_cast<const E*>(a.x.data), a.x.ld, r, a.x.V, rank, ctas);
   RowWork<E> w(s, part, rank, ctas);
+  typename RowWork<E>::Tops my;
   int32_t* id = a.id + (size_t)r * K;
   float* val = a.val + (size_t)r * K;
   auto fill = [&](int from) {
@@ -1456,12 +1473,12 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a, i
   uint32_t live, big = 0;
   const float c = 1.44269504f / a.temperature;
   const bool parts = K <= kFewTop;
-  w.template read_tops<true>(c, false, &live);
+  w.template read_tops<true>(my, c, false, &live);
   if (ctas > 1) cluster_wait();     // every CTA of the cluster runs before its memory is written
   if (parts) {
-    w.give_sum(key_float(w.template list_part<false>(K, 0.f)), c);
+    w.give_sum(my, key_float(w.template list_part<false>(my, K, 0.f)), c);
   } else {
-    w.post_groups();
+    w.post_groups(my);
     row_sync(ctas);
     if (rank == 0) {
       const uint32_t least = w.threshold(K, &big);
@@ -1472,8 +1489,8 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a, i
     row_sync(ctas);
     big = s.word[0];
     if (big > kNegInfKey && big < kPosInfKey) {
-      w.template list_tops<false>(s.word[1], 0.f, 0.f);
-      w.give_sum(key_float(big), c);
+      w.template list_tops<false>(my, s.word[1], 0.f, 0.f);
+      w.give_sum(my, key_float(big), c);
     }
   }
   row_sync(ctas);
