@@ -42,7 +42,7 @@ struct Temper {
     lo = fmaf(-hi, T, 1.f) / T;
     c = 1.44269504f * hi;
   }
-  DF_DEV float over(float x) const { return fmaf(x, hi, x * lo); }              // x / T
+  DF_DEV float over(float x) const { return fabsf(x) < INFINITY ? fmaf(x, hi, x * lo) : x; }   // x / T
   DF_DEV float over(float x, float minus) const { return fmaf(x, hi, -minus) + x * lo; }   // x / T - minus
 };
 
@@ -317,7 +317,8 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a, int
       const float f = ex2_approx((mi - m) * T.c);
       R += s.post[i][1] * f;
       S += s.post[i][2] * f;
-      cross += s.post[i][3] + T.over(m - mi) * s.post[i][4];
+      cross += s.post[i][3];
+      if (s.post[i][4] > 0.f) cross += T.over(m - mi) * s.post[i][4];     // (m - mi) / T may be infinite
     } else {
       cross += s.post[i][3];
     }

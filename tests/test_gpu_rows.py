@@ -531,6 +531,22 @@ def test_rows_masked_by_the_lowest_number(dtype, V):
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_distill_a_part_of_the_row_masked_by_the_lowest_number(dtype):
+    """What one CTA of a row reads is masked as a whole, and its largest logit over T is out of range."""
+    V, T = 40000, 0.5
+    x, y = logits(30, 15, V), logits(31, 15, V).astype(np.float32)
+    x[:, V // 2:], y[:, V // 2:] = LOWEST[dtype], -20.0
+    ids, vals, lse = lists(y, 20, T, V)
+    z = held(x, dtype)
+    loss, stats, grad, status = run_distill(z, ids, vals, lse, T)
+    back, status2 = run_backward(z, ids, vals, lse, T, stats)
+    assert status == status2 == 0 and torch.isfinite(loss).all()
+    for r in range(15):
+        check_row(f64(loss)[r], f64(stats)[r], (f64(grad)[r], f64(back)[r]), f64(z)[r], ids[r].cpu().numpy(), f64(vals)[r],
+                  float(lse[r]), T, 1.0, (1.0, 1.0), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_largest_vocabulary(dtype):
     V = 1 << 20
     x = held(logits(23, 15, V), dtype)
