@@ -23,11 +23,11 @@
 //
 // Bounds.  The least that a row can do is to be read once.  What is measured (rows of 151936, one
 // GB300, whole calls):
-//   1 row, fp32                   11 us: the host's call (7 us), a barrier of the cluster and one warp's end of the row
+//   1 row, fp32                   11 us: the cluster's start and barriers, and one warp's end of the row
 //   16 rows, 20 largest, fp32     12 us: the same
 //   257 rows, top-k 20, fp32      46 us for 156 MB; a kernel that only reads them takes 26, a row's end 8
 //   256 rows, top-p 0.9, bf16     197 to 222 us: 73 of the rows are searched, which reads each twice more
-//                                 with 13 instructions for a token's exact mass
+//                                 with some 25 instructions for a token's exact mass
 //   2064 rows, mixed, bf16        339 us for 627 MB: first pass 191 (3.9 TB/s: four CTAs an SM, and each
 //                                 ends its row without reading), 114 rows searched 149
 //   2048 rows, 256 largest, bf16  243 us for 622 MB, and 288 MB of groups read again
