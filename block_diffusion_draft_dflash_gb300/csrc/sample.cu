@@ -14,7 +14,7 @@
 // Mass alone (top-p, or nothing cut).  The first pass also sums exp((l - max) / T) in fp32, which
 // gives the mass of the tokens that are not listed within 2^-15 of it.  If both ends of that
 // interval put the borders on the same tokens of the list, they are right; a sure row's are.
-// Otherwise a pass counts tokens in 2048 bins of 1/32 of a power of two of probability, from which
+// Otherwise a pass counts tokens in 2048 bins of 1/64 of a power of two of probability, from which
 // follows where a border should lie; one more pass sums all masses, and those before the bins of
 // the two borders, exactly, and lists these bins' tokens (up to 1024 for each border).  A border
 // that is not among them is looked for bin by bin between exact masses.  Where a bin has too many
@@ -26,10 +26,10 @@
 //   1 row, fp32                   11 us: the cluster's start and barriers, and one warp's end of the row
 //   16 rows, 20 largest, fp32     12 us: the same
 //   257 rows, top-k 20, fp32      46 us for 156 MB; a kernel that only reads them takes 26, a row's end 8
-//   256 rows, top-p 0.9, bf16     197 to 222 us: 73 of the rows are searched, which reads each twice more
+//   256 rows, top-p 0.9, bf16     165 to 198 us: 73 of the rows are searched, which reads each twice more
 //                                 with some 25 instructions for a token's exact mass
-//   2064 rows, mixed, bf16        339 us for 627 MB: first pass 191 (3.9 TB/s: four CTAs an SM, and each
-//                                 ends its row without reading), 114 rows searched 149
+//   2064 rows, mixed, bf16        350 us for 627 MB: first pass 191 (3.9 TB/s: four CTAs an SM, and each
+//                                 ends its row without reading), 114 rows searched 160
 //   2048 rows, 256 largest, bf16  243 us for 622 MB, and 288 MB of groups read again
 #include <algorithm>
 
@@ -668,13 +668,14 @@ struct RowWork {
     }
     __syncthreads();
   }
-  // Tokens' bins by probability: 1/32 of a power of two; what is added for one (its place in the
-  // bin in eighths goes above the count).
-  static DF_DEV uint32_t bin_of(uint32_t below_top) { return below_top >> 5; }
-  static DF_DEV uint32_t entry_of(uint32_t below_top) { return 1u + ((below_top & 28u) << 17); }
+  // Tokens' bins by probability: 1/64 of a power of two, the last one all below 2^-32; what is added
+  // for one (its place in the bin in eighths goes above the count).  Of 1/32 (no last one) flat rows
+  // have more tokens in a bin than a list takes: 2064 mixed rows 338 to 438 us against 346 to 356.
+  static DF_DEV uint32_t bin_of(uint32_t below_top) { return min(below_top >> 4, kBins - 1u); }
+  static DF_DEV uint32_t entry_of(uint32_t below_top) { return 1u + ((below_top & 14u) << 18); }
   static DF_DEV float bin_mass(int b, uint32_t n, uint32_t places) {
     const float at = places < 1u << 30 ? ((float)places / (float)n + 0.5f) * 0.125f : 0.5f;
-    return (float)n * exp2f(-((float)b + at) * (1.f / 32.f));
+    return (float)n * exp2f(b < kBins - 1 ? -((float)b + at) * (1.f / 64.f) : -40.f);
   }
   bool by_probability;     // the bins are these (else of a range of keys)
 
@@ -911,7 +912,9 @@ struct RowWork {
   __device__ __noinline__ void sum_and_list() {
     const MassScale c = scale;
     const RowPart<E> p = part;
-    const uint32_t a1 = s.word[0], a2 = s.word[1], d1 = s.word[3], d2 = s.word[4], last = max(a2, d2);
+    // bins are not cut off at the last one here; a window that ends there has no end
+    auto end = [](uint32_t b) { return b < kBins - 1 ? b : ~0u; };
+    const uint32_t a1 = s.word[0], a2 = end(s.word[1]), d1 = s.word[3], d2 = end(s.word[4]), last = max(a2, d2);
     const float2* const table = s.table;
     MassSum m, ma, md;
     for_pieces<2>(p, [&](const float* x, int piece, bool) {
@@ -920,7 +923,7 @@ struct RowWork {
       for (int e = 1; e < VE; ++e) big = fmaxf(big, x[e]);
       m.room(VE);
       m.n += VE;
-      if (bin_of(c.top - c.bits(big)) > last) {      // the piece lies behind both windows
+      if ((c.top - c.bits(big)) >> 4 > last) {      // the piece lies behind both windows
 #pragma unroll
         for (int e = 0; e < VE; ++e) add_mass(m, c, table, x[e]);
         return;
@@ -931,7 +934,7 @@ struct RowWork {
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
         uint32_t ta, tb;
-        const uint32_t bin = bin_of(c.top - mass_terms(c, table, x[e], &ta, &tb));
+        const uint32_t bin = (c.top - mass_terms(c, table, x[e], &ta, &tb)) >> 4;
         m.a += ta;
         m.b += tb;
         if (bin < a1) ma.a += ta, ma.b += tb, ++ma.n;
