@@ -26,7 +26,7 @@
 //   1 row, fp32                   11 us: the cluster's start and barriers, and one warp's end of the row
 //   16 rows, 20 largest, fp32     12 us: the same
 //   257 rows, top-k 20, fp32      46 us for 156 MB; a kernel that only reads them takes 26, a row's end 8
-//   256 rows, top-p 0.9, bf16     137 to 176 us: 73 of the rows are searched, which reads each twice more
+//   256 rows, top-p 0.9, bf16     137 to 192 us: 73 of the rows are searched, which reads each twice more
 //                                 with some 25 instructions for a token's exact mass
 //   2064 rows, mixed, bf16        325 us for 627 MB: first pass 191 (3.9 TB/s: four CTAs an SM, and each
 //                                 ends its row without reading), 114 rows searched 135

@@ -494,8 +494,8 @@ typedef struct {
  *   min_p  those with w_v >= min_p (0: all);
  * each of them keeps the first tokens of the order, and the fewest count.  The token is the
  * first one in order at which the kept mass exceeds u times all of it.  temperature 0 (and any
- * below 2^-126): the first token.  Masses are sums of whole numbers of 2^-42 made with a relative
- * error near 2^-35, so the result does not depend on the order of summation.
+ * below 2^-126): the first token.  Masses are sums of whole numbers of 2^-42 of the first token's,
+ * made with a relative error near 2^-35, so the result does not depend on the order of summation.
  *   group        row r takes setting r / group; rows is a multiple of it
  *   temperature, top_k, top_p, min_p   [rows / group] each, or NULL: 1, 0, 1, 0.
  *                0 <= temperature <= 2^100, 0 < top_p <= 1, 0 <= min_p <= 1

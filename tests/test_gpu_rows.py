@@ -573,6 +573,42 @@ def test_many_rows_whose_borders_lie_far_behind(rows, V):
         assert got[i] == (one[i] * n)[:rows]
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("V", [9001, 150001])
+def test_borders_among_tokens_of_next_to_no_probability(dtype, V):
+    """All but one token lie below 2^-32 of the first; together they still hold the last numbers' draws.
+
+    A mass is a whole number of 2^-42 of the first token's: off by at most 2^-43 (its rounding) and 2^-35 of itself, so a
+    sum of up to V of them by V 2^-43 + 2^-35 M.  A border compares two such sums: it is right within twice that.
+    """
+    rng = np.random.default_rng(V)
+    x = rng.normal(-23.6, 0.3, (15, V))
+    x[np.arange(15), rng.integers(0, V, 15)] = 0.0
+    u = 1 - 2.0 ** -24 * np.arange(1, 16) ** 2
+    p = 1 - 2.0 ** -24
+    x = held(x, dtype)
+    for settings, group in (([(1.0, 0, 1.0, 0.0)], 15), ([(1.0, 0, p, 0.0)], 15),
+                            ([(1.0, V // 2, p, 0.0), (0.95, V - 5, 1.0, 0.0), (1.0, 3, 1.0, 0.0)], 5)):
+        token, _, kept, status = run_sample(x, u, settings, group)
+        assert status == 0
+        for r, row in enumerate(f64(x)):
+            T, k, top_p, _ = settings[r // group]
+            T, top_p = float(np.float32(T)), float(np.float32(top_p))
+            order = np.lexsort((np.arange(V), -row))
+            cum = np.cumsum(np.exp(row[order] / T))
+            if k:
+                cum = cum[:k]
+            tol = 2 * (V * 2.0 ** -43 + 2.0 ** -35 * cum[-1])
+            n = kept[r]
+            if top_p < 1:
+                assert cum[n - 1] >= top_p * cum[-1] - tol and (n == 1 or cum[n - 2] < top_p * cum[-1] + tol)
+            else:
+                assert n == cum.size
+            at = int(np.nonzero(order == token[r])[0][0])
+            want = float(np.float32(u[r])) * cum[n - 1]
+            assert at < n and cum[at] > want - tol and (at == 0 or cum[at - 1] <= want + tol)
+
+
 def test_rows_farther_apart_than_32_bits():
     """Element offsets beyond 2^31 and byte offsets beyond 2^32, of the rows and of the gradient."""
     V, ld = 5001, (1 << 30) + 13
