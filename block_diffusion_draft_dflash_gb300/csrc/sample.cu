@@ -711,7 +711,8 @@ struct RowWork {
     if (SUMS) give_mass(m, &s.mass);
     by_probability = true;
   }
-  // First CTA: *total, *live = tokens above -inf.
+  // First CTA: *total, *live = tokens above -inf.  Ends with a barrier, like locate(): what follows may
+  // set the sums that every thread has just read back to 0.
   __device__ __noinline__ void count_all(uint64_t* total, uint32_t* live) {
     if (tid == 0) s.mass = 0;
     row_sync(ctas);
@@ -722,6 +723,7 @@ struct RowWork {
       *total = s.mass;
       *live = s.bins.count[kBins - 1];
     }
+    row_sync(ctas);
   }
 
   // The part of a search that a level's bins are left with (first CTA): the border lies in bins
