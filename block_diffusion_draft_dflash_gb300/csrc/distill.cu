@@ -174,7 +174,9 @@ DF_DEV void write_zeros(const RowPart<E>& p, E* grad) {
 template <class E>
 DF_DEV void write_gradient(const RowPart<E>& p, E* grad, const Entries& en, const float* z, const bool* mine, float m,
                            float c, float scale, float inv_s, float rho_over_r) {
-  const float out = fminf(fmaxf(scale * (inv_s - rho_over_r), -3.4e38f), 3.4e38f);
+  // finite where the weight is (rho / R may overflow); a NaN or an infinity in it stays one
+  float out = scale * (inv_s - rho_over_r);
+  if (fabsf(scale) < INFINITY) out = fminf(fmaxf(out, -3.4e38f), 3.4e38f);
   write_pieces<4, true>(p, grad, [&](float* x) {
 #pragma unroll
     for (int e = 0; e < RowPart<E>::VE; ++e) x[e] = ex2_approx((x[e] - m) * c) * out;

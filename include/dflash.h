@@ -536,7 +536,8 @@ int dflash_top_logits(const df_rows* logits, int K, float temperature, int32_t* 
  *   lse          [n_teacher] fp32 or NULL
  *   teacher_row  [rows] int32: the list of row r, -1: the row does not learn; or NULL: list r
  *                (n_teacher >= rows)
- *   weight       [rows] fp32 or NULL: 1; with weight 0 the row does not learn
+ *   weight       [rows] fp32 or NULL: 1; with weight 0 the row does not learn; with a NaN or an infinity
+ *                its loss and all of its gradient are such (and no error is recorded)
  *   loss         [rows] fp32 out
  *   stats        [rows][4] fp32 out: the row's largest logit m, ln sum exp((z - m) / T) over all
  *                tokens, the same over those outside the list (-inf: none), 0
@@ -554,7 +555,7 @@ int dflash_distill(const df_rows* student, int K, int n_teacher, const int32_t* 
 
 /* dflash_distill_backward -- the gradient of sum_r grad_loss[r] loss[r] by the student's logits,
  * from dflash_distill's arguments and its stats.
- *   grad_loss    [rows] fp32 or NULL: 1
+ *   grad_loss    [rows] fp32 or NULL: 1; a NaN or an infinity does what one in the weight does
  *   Rows that do not learn or were left out have a gradient of zeros; the workspace of
  *   dflash_distill_workspace_size. */
 int dflash_distill_backward(const df_rows* student, int K, int n_teacher, const int32_t* id, const float* val,
