@@ -42,8 +42,15 @@ struct Temper {
     lo = fmaf(-hi, T, 1.f) / T;
     c = 1.44269504f * hi;
   }
-  DF_DEV float over(float x) const { return fabsf(x) < INFINITY ? fmaf(x, hi, x * lo) : x; }   // x / T
-  DF_DEV float over(float x, float minus) const { return fmaf(x, hi, -minus) + x * lo; }   // x / T - minus
+  // x / T, and x / T - minus (finite); infinite where x hi is, whatever x lo, which may be infinite as well, says
+  DF_DEV float over(float x) const {
+    const float p = x * hi;
+    return fabsf(p) < INFINITY ? fmaf(x, hi, x * lo) : p;
+  }
+  DF_DEV float over(float x, float minus) const {
+    const float p = x * hi;
+    return fabsf(p) < INFINITY ? fmaf(x, hi, -minus) + x * lo : p;
+  }
 };
 
 // A thread's entries of a teacher's list: entry tid + 512 j.
