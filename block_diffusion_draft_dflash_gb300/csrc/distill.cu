@@ -3,9 +3,13 @@
 // With e_j = exp((z_j - m) / T), m the row's largest logit, S = sum of e_j over all tokens and R
 // over those outside the teacher's list (t_i, rho):
 //   loss / weight = sum_i t_i (ln t_i - (z_i - m) / T) + sum t ln S + rho (ln rho - ln(R / S))
-//   gradient = weight / T (e_j / S - t_j) in the list, weight / T e_j (1 / S - rho / R) outside
+//   gradient = weight / T (e_j / S - t_j) in the list, weight / T e_j / R (R / S - rho) outside
 // R is summed over the tokens outside (a bit for each token marks the list), not taken as S minus
-// the list's part: where the student is sure of the list, that difference has no digits left.
+// the list's part: where the student is sure of the list, that difference has no digits left.  It is
+// summed relative to the largest logit outside, m', and e_j / R is made from z_j - m' or, from kept
+// statistics, from the difference of exponents: relative to m all of it falls to 0 where m' lies 87 T
+// below m.  ln R is kept in two floats where it is below -64 (in one its rounding is that of the shares
+// e_j / R), and from 2^30 on, where two have no digits for them either, the others count as masked.
 // Both passes are bound by the row's bytes: loss reads a row once; with the gradient a row is read
 // again from L2 by the CTAs that just read it, and written.  512 threads a CTA: a list's 1024 entries
 // are two a thread, and a row's CTAs are few.  Measured with rows of 151936 on one GB300, whole calls:
@@ -23,16 +27,24 @@ namespace {
 constexpr int kMaxList = 1024;
 constexpr int kPer = kMaxList / kRowThreads;   // entries of a thread
 
-struct Post {            // what a CTA tells the others of its part of a row
-  float largest, rest, listed;   // sums of e_j relative to `largest`
-  float cross, t;                // sum of t_i (ln t_i - (z_i - largest) / T), and of t_i
-  uint32_t bad;                  // 1: NaN or +inf, 2: a bad list
-};
+// What a CTA tells the others of its part of a row, as floats: the largest logit, the largest outside
+// the list, the sum of exp((z - that) / T) outside the list, that of exp((z - largest) / T) in it, the sums of
+// t_i (ln t_i - (z_i - largest) / T) and of t_i, and flags (1: NaN or +inf, 2: a bad list).
+enum { kLargest, kLargestRest, kRest, kListed, kCross, kT, kFlags, kPosts };
 struct Shared {
-  float post[8][8];      // Post of every CTA of the row
-  float tmp[kRowWarps];
+  float post[8][kPosts];   // of every CTA of the row
+  float tmp[kRowWarps], tmp2[kRowWarps];
   uint32_t flags;
 };
+constexpr float kFar = -64.f;         // below it ln R is kept in two floats
+constexpr float kMasked = -0x1p30f;   // (m' - m) / T below which the tokens outside count as masked
+
+// Largest number of the warp, in one instruction (NaN only where all are).
+DF_DEV float redux_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
 
 // 1 / T in two floats, and log2(e) / T.
 struct Temper {
@@ -176,18 +188,10 @@ DF_DEV void write_zeros(const RowPart<E>& p, E* grad) {
   });
 }
 
-// Gradient of a row's part: the formula of the tokens outside the list for every element, then
-// the list's own over it.  z: the student's logits at the thread's entries, where they lie in the part.
+// The list's own gradient, over what the formula of the tokens outside has left there.  z: the student's
+// logits at the thread's entries, where they lie in the part.
 template <class E>
-DF_DEV void write_gradient(const RowPart<E>& p, E* grad, const Entries& en, const float* z, const bool* mine, float m,
-                           float c, float scale, float inv_s, float rho_over_r) {
-  // finite where the weight is (rho / R may overflow); a NaN or an infinity in it stays one
-  float out = scale * (inv_s - rho_over_r);
-  if (fabsf(scale) < INFINITY) out = fminf(fmaxf(out, -3.4e38f), 3.4e38f);
-  write_pieces<4, true>(p, grad, [&](float* x) {
-#pragma unroll
-    for (int e = 0; e < RowPart<E>::VE; ++e) x[e] = ex2_approx((x[e] - m) * c) * out;
-  });
+DF_DEV void write_listed(E* grad, const Entries& en, const float* z, const bool* mine, float m, float c, float scale, float inv_s) {
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < kPer; ++j)
@@ -208,18 +212,18 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a, int
   const RowPart<E> part(static_cast<const E*>(a.x.data), a.x.ld, r, a.x.V, rank, ctas);
   E* grad = a.grad ? static_cast<E*>(a.grad) + r * a.ld_grad : nullptr;
   const int list = list_of(a, r);
-  auto give = [&](float loss, float s0, float s1, float s2) {
-    a.loss[r] = loss;
-    reinterpret_cast<float4*>(a.stats)[r] = make_float4(s0, s1, s2, loss == loss || s0 == s0 ? 0.f : NAN);
+  auto give = [&](float v) {
+    a.loss[r] = v;
+    reinterpret_cast<float4*>(a.stats)[r] = make_float4(v, v, v, v);
   };
   if (list < 0) {
     if (grad) write_zeros(part, grad);
     if (rank == 0 && tid == 0) {
       if (list == -1) {
-        give(0.f, 0.f, 0.f, 0.f);
+        give(0.f);
       } else {
         set_status(a.status, DF_ERR_ARG, r);
-        give(NAN, NAN, NAN, NAN);
+        give(NAN);
       }
     }
     return;
@@ -249,41 +253,51 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a, int
   }
   if (bad) atomicOr(&s.flags, bad);
   __syncthreads();
-  // largest logit and the sum outside the list, a thread's own
-  float m = -INFINITY, rest = 0.f, check = -INFINITY;
+  // largest logit and the sum outside the list, a thread's own.  With the lowest number to begin with, what is
+  // masked adds 0 without a question; the sum is 0 where nothing is left.
+  float mr = -0x1.fffffep127f, rest = 0.f, check = -INFINITY;
   const uint8_t* marks = reinterpret_cast<const uint8_t*>(bits);
-  for_pieces<4>(part, [&](const float* x, int piece, bool on) {
+  for_pieces<4>(part, [&](float* x, int piece, bool on) {
     float big = x[0];
 #pragma unroll
     for (int e = 1; e < VE; ++e) big = max_nan(big, x[e]);
     check = max_nan(check, big);
-    if (!(big > -INFINITY)) return;
-    if (big > m) {
-      rest *= ex2_approx((m - big) * T.c);
-      m = big;
-    }
     uint32_t listed = 0;
     if (on) {
       const int q = piece - part.begin;
       listed = VE == 8 ? marks[q] : (marks[q >> 1] >> ((q & 1) * 4)) & 15u;
     }
-    if (listed == 0) {
+    if (listed) {          // few pieces; one way through the sums for all (960 rows of 151936: with two 141 us, not 131)
+      big = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < VE; ++e) rest += ex2_approx((x[e] - m) * T.c);
-    } else {
-#pragma unroll
-      for (int e = 0; e < VE; ++e)
-        if (!(listed >> e & 1)) rest += ex2_approx((x[e] - m) * T.c);
+      for (int e = 0; e < VE; ++e) {
+        if (listed >> e & 1) x[e] = -INFINITY;
+        big = fmaxf(big, x[e]);
+      }
     }
+    if (big > mr) {
+      rest *= ex2_approx((mr - big) * T.c);
+      mr = big;
+    }
+#pragma unroll
+    for (int e = 0; e < VE; ++e) rest += ex2_approx((x[e] - mr) * T.c);
   });
+  if (rest == 0.f) mr = -INFINITY;
   // the CTA's part
-  float big = warp_max(m);
+  float zmax = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) zmax = fmaxf(zmax, z[j]);
+  float big = redux_max(zmax), big_rest = redux_max(mr);
   __syncthreads();
-  if ((tid & 31) == 0) s.tmp[tid >> 5] = big;
+  if ((tid & 31) == 0) {
+    s.tmp[tid >> 5] = big;
+    s.tmp2[tid >> 5] = big_rest;
+  }
   if (!(check < INFINITY)) atomicOr(&s.flags, 1u);
   __syncthreads();
-  big = warp_max(s.tmp[tid & (kRowWarps - 1)]);
-  rest = block_add(m > -INFINITY ? rest * ex2_approx((m - big) * T.c) : 0.f, s.tmp);
+  big_rest = redux_max(s.tmp2[tid & (kRowWarps - 1)]);
+  big = fmaxf(redux_max(s.tmp[tid & (kRowWarps - 1)]), big_rest);
+  rest = block_add(mr > -INFINITY ? rest * ex2_approx((mr - big_rest) * T.c) : 0.f, s.tmp);
   float in = 0.f, cross = 0.f, tsum = 0.f;
 #pragma unroll
   for (int j = 0; j < kPer; ++j)
@@ -299,49 +313,82 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a, int
   tsum = block_add(tsum, s.tmp);
   if (ctas > 1) cluster_wait();     // every CTA of the cluster runs before its memory is written
   if (tid < ctas) {
-    const float w[6] = {big, rest, in, cross, tsum, __uint_as_float(s.flags)};
-    for (int i = 0; i < 6; ++i) st_remote(at_rank(&s.post[rank][i], tid), w[i]);
+    const float w[kPosts] = {big, big_rest, rest, in, cross, tsum, __uint_as_float(s.flags)};
+    for (int i = 0; i < kPosts; ++i) st_remote(at_rank(&s.post[rank][i], tid), w[i]);
   }
   row_sync(ctas);
-  m = -INFINITY;
+  float m = -INFINITY;
+  mr = -INFINITY;
   bad = 0;
   for (int i = 0; i < ctas; ++i) {
-    m = fmaxf(m, s.post[i][0]);
-    bad |= __float_as_uint(s.post[i][5]);
+    m = fmaxf(m, s.post[i][kLargest]);
+    mr = fmaxf(mr, s.post[i][kLargestRest]);
+    bad |= __float_as_uint(s.post[i][kFlags]);
   }
   if (!(m > -INFINITY)) bad |= 1;
   if (bad) {
     if (grad) write_zeros(part, grad);
     if (rank == 0 && tid == 0) {
       set_status(a.status, bad & 2 ? DF_ERR_ARG : DF_ERR_NAN, r);
-      give(NAN, NAN, NAN, NAN);
+      give(NAN);
     }
     return;
   }
-  float R = 0.f, S = 0.f;
+  float R = 0.f, S = 0.f;              // R relative to m'
   cross = 0.f;
   for (int i = 0; i < ctas; ++i) {
-    const float mi = s.post[i][0];
+    const float mi = s.post[i][kLargest], mri = s.post[i][kLargestRest];
+    if (mri > -INFINITY) R += s.post[i][kRest] * ex2_approx((mri - mr) * T.c);
+    cross += s.post[i][kCross];
     if (mi > -INFINITY) {
-      const float f = ex2_approx((mi - m) * T.c);
-      R += s.post[i][1] * f;
-      S += s.post[i][2] * f;
-      cross += s.post[i][3];
-      if (s.post[i][4] > 0.f) cross += T.over(m - mi) * s.post[i][4];     // (m - mi) / T may be infinite
-    } else {
-      cross += s.post[i][3];
+      S += s.post[i][kListed] * ex2_approx((mi - m) * T.c);
+      if (s.post[i][kT] > 0.f) cross += T.over(m - mi) * s.post[i][kT];     // (m - mi) / T may be infinite
     }
   }
-  S += R;
+  const float below = T.over(mr - m);
+  const bool others = below >= kMasked;     // not: there are none, or they count as masked
+  if (!others) {
+    R = 0.f;
+    mr = m;
+  }
+  const float to_m = ex2_approx((mr - m) * T.c);     // e_j = exp((z_j - m') / T) times this
+  S += R * to_m;
   const float rho = a.lse ? fmaxf(1.f - en.sum, 0.f) : 0.f;
   const float weight = a.weight ? a.weight[r] : 1.f;
   if (rank == 0 && tid == 0) {
-    const float ln_s = logf(S), ln_r = logf(R);
+    const float ln_s = logf(S);
+    float ln_r = others ? below + logf(R) : -INFINITY, left = 0.f;
+    if (others && ln_r < kFar) {
+      const double exact = ((double)mr - (double)m) / (double)a.temperature + (double)logf(R);
+      ln_r = (float)exact;
+      left = (float)(exact - (double)ln_r);
+    }
     const float kl = cross + en.sum * ln_s + (rho > 0.f ? rho * (logf(rho) - (ln_r - ln_s)) : 0.f);
-    give(weight * kl, m, ln_s, ln_r);
+    a.loss[r] = weight * kl;
+    reinterpret_cast<float4*>(a.stats)[r] = make_float4(m, ln_s, ln_r, left);
   }
-  if (grad)
-    write_gradient(part, grad, en, z, mine, m, T.c, T.over(weight), 1.f / S, R > 0.f ? rho / R : 0.f);
+  if (grad) {
+    const float scale = T.over(weight), inv_s = 1.f / S;
+    const float out = scale * (to_m * inv_s - (others ? rho / R : 0.f));
+    write_pieces<4, true>(part, grad, [&](float* x) {
+#pragma unroll
+      for (int e = 0; e < VE; ++e) x[e] = ex2_approx((x[e] - mr) * T.c) * out;
+    });
+    write_listed(grad, en, z, mine, m, T.c, scale, inv_s);
+  }
+}
+
+// The gradient of the tokens outside the list where ln R, in the two floats ln_r + left, lies so far below 0
+// that exponents need more digits than a float has; few rows do.
+template <class E>
+__device__ __noinline__ void write_far(const E* row, int V, int rank, int ctas, E* grad, float T, float m, float ln_r, float left,
+                                       float out) {
+  const RowPart<E> p(row, 0, 0, V, rank, ctas);
+  const double c = 1.4426950408889634 / (double)T, to = ((double)ln_r + (double)left) * 1.4426950408889634;
+  write_pieces<1, true>(p, grad, [&](float* x) {
+#pragma unroll
+    for (int e = 0; e < RowPart<E>::VE; ++e) x[e] = ex2_approx((float)(((double)x[e] - (double)m) * c - to)) * out;
+  });
 }
 
 // grid: rows x CTAs of a row; they do not depend on each other.
@@ -376,7 +423,18 @@ __global__ void __launch_bounds__(kRowThreads) distill_backward_kernel(DistillAr
   __syncthreads();     // an entry's logit is read before it may be written over
   const float rho = a.lse ? fmaxf(1.f - en.sum, 0.f) : 0.f;
   const float scale = T.over((a.weight ? a.weight[r] : 1.f) * (a.grad_loss ? a.grad_loss[r] : 1.f));
-  write_gradient(part, grad, en, z, mine, st.x, T.c, scale, expf(-st.y), st.z > -INFINITY ? rho * expf(-st.z) : 0.f);
+  const bool others = st.z > -INFINITY;
+  // e_j / R (without others e_j), times R / S - rho (1 / S)
+  const float ln_r = others ? st.z : 0.f, out = scale * (expf(ln_r - st.y) - (others ? rho : 0.f));
+  const float m = st.x, to = ln_r * 1.44269504f;
+  if (ln_r < kFar)
+    write_far(part.row, a.x.V, rank, ctas, grad, a.temperature, m, ln_r, st.w, out);
+  else
+    write_pieces<4, true>(part, grad, [&](float* x) {
+#pragma unroll
+      for (int e = 0; e < VE; ++e) x[e] = ex2_approx(fmaf(x[e] - m, T.c, -to)) * out;
+    });
+  write_listed(grad, en, z, mine, m, T.c, scale, expf(-st.y));
 }
 
 __global__ void __launch_bounds__(256) path_rows_kernel(int b, int D, int n_tree, const int32_t* __restrict__ n_new,

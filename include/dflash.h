@@ -530,7 +530,8 @@ int dflash_top_logits(const df_rows* logits, int K, float temperature, int32_t* 
  *   dloss / dz_j = weight / T (q_j - t_j)              j in the list
  *                  weight / T q_j (1 - rho / sigma)    others (lse NULL: weight / T q_j)
  * Terms with t_i = 0 or rho = 0 are 0.  A student's -inf where the teacher has mass gives an
- * infinite loss (its gradient stays finite; with sigma = 0 < rho there are no others).
+ * infinite loss (its gradient stays finite; with sigma = 0 < rho there are no others).  Where all of
+ * the student's logits outside the list lie more than 2^30 T below its largest one, sigma counts as 0.
  *   student      the rows; T = temperature, 2^-100 .. 2^100
  *   id, val      [n_teacher][K] int32, fp32; entries with id -1 are not there; 1 <= K <= 1024
  *   lse          [n_teacher] fp32 or NULL
@@ -540,7 +541,8 @@ int dflash_top_logits(const df_rows* logits, int K, float temperature, int32_t* 
  *                its loss and all of its gradient are such (and no error is recorded)
  *   loss         [rows] fp32 out
  *   stats        [rows][4] fp32 out: the row's largest logit m, ln sum exp((z - m) / T) over all
- *                tokens, the same over those outside the list (-inf: none), 0
+ *                tokens, the same over those outside the list (-inf: sigma is 0), 0; where the third
+ *                one is below -64, the fourth is what its rounding to fp32 left
  *   grad         [rows][ld_grad] out in the student's type, or NULL; may be the student's own
  *                array (with its ld); behind V it is left as it was
  * A row that does not learn has loss 0, stats 0 and a gradient of zeros.  A row left out has loss

@@ -77,7 +77,8 @@ def check(z, ids, vals, list_lse, T, loss, stats, grads, dtype, w=1.0):
     grad = q * total
     kept = np.zeros(z.size)
     if lnr > -INF:
-        share = np.exp(y - lnr)
+        share = np.zeros(z.size)
+        share[other] = np.exp(y[other] - lnr)
         grad[other] -= (rho * share)[other]
         far = np.where(share > 0, np.abs(y - lnr), 0.0)
         rel = 2.0 ** -21 + 2.0 ** -22 * (far + min(abs(lnr), 64)) + 2 * s
@@ -103,6 +104,65 @@ def teach(z, ids, vals, lses, T, dtype, status=0):
     for r in range(x.shape[0]):
         check(hz[r], hi[r], hv[r], None if lses is None else float(lses[r]), T, hl[r], hs[r], ((hg[r], False), (hb[r], True)), dtype)
     return hl, hs, hg, hb
+
+
+# ------------------------------------------------------------------------------ what a list leaves, far below it
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("V,K", [(300, 4), (3000, 33), (40000, 4), (40000, 1000)])
+@pytest.mark.parametrize("margin,T", [(60.0, 1.0), (90.0, 1.0), (100.0, 1.0), (200.0, 1.0), (1000.0, 1.0), (65536.0, 1.0),
+                                      (float(1 << 29), 1.0), (20.0, 0.1), (48.0, 0.3), (2.0 ** 20, 2.0 ** -8), (3.0, 0.001)])
+def test_a_margin_between_the_list_and_the_others(dtype, V, K, margin, T):
+    """The teacher leaves mass to the others, of which the student has next to none."""
+    rng = np.random.default_rng(V + K)
+    n = 6
+    y = np.zeros((n, V), np.float32)
+    at = np.stack([rng.permutation(V)[:K] for _ in range(n)])
+    np.put_along_axis(y, at, T * rng.uniform(3.0, 6.0, (n, K)).astype(np.float32), 1)
+    z = T * rng.normal(0, 2, (n, V))
+    np.put_along_axis(z, at, margin * (1 + 0.01 * rng.random((n, K))), 1)
+    for r, upto in ((1, V // 2), (2, 7)):  # the others masked from there on: whole parts of the row have none
+        z[r, upto:] = np.where(np.isin(np.arange(upto, V), at[r]), z[r, upto:], -INF)
+    ids, vals, lses = lists(y, K, float(np.float32(T)), V)
+    teach(z, ids, vals, lses, T, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("T", [0.1, 0.05, 0.01])
+def test_a_student_like_its_teacher_at_a_small_temperature(dtype, T):
+    V, K, n = 20000, 20, 200
+    y = logits(40, n, V)
+    x = held(y, dtype)
+    ids, vals, lses = lists(f64(x).astype(np.float32), K, float(np.float32(T)), V)
+    hl, _, _, _ = teach(f64(x), ids, vals, lses, T, dtype)
+    assert np.isfinite(hl).all()
+
+
+def test_what_lies_beyond_all_statistics_counts_as_masked():
+    V, K = 5000, 3
+    y = np.zeros((2, V), np.float32)
+    y[:, :K] = [6.0, 5.0, 4.0]
+    z = np.zeros((2, V))
+    z[:, :K] = float(1 << 32)
+    z[1, 100:] = -INF
+    ids, vals, lses = lists(y, K, 1.0, V)
+    hl, hs, hg, hb = teach(z, ids, vals, lses, 1.0, "fp32")
+    assert (hl == INF).all() and (hg[:, K:] == 0).all() and (hb[:, K:] == 0).all()
+
+
+@pytest.mark.parametrize("margin", [30.0, 90.0, 200.0])
+def test_gradient_by_differences_far_out(margin):
+    V, K, h = 64, 4, 0.0625
+    rng = np.random.default_rng(3)
+    y, z = (rng.normal(0, 2, (1, V)).astype(np.float32) for _ in range(2))
+    ids, vals, lses = lists(y, K, 1.0, V)
+    z[0, ids[0].long().cpu().numpy()] = margin + rng.normal(0, 1, K).astype(np.float32)
+    grad = f64(run_distill(f32(z), ids, vals, lses, 1.0)[2])[0]
+    for j in (0, 5, V - 1, int(ids[0, 0])):
+        d = np.zeros((1, V), np.float32)
+        d[0, j] = h
+        up, down = (f64(run_distill(f32(z + k * d), ids, vals, lses, 1.0, grad=False)[0])[0] for k in (1, -1))
+        # the third derivative of a log-sum is at most 1/4: h^2 / 24; losses below 2^8 and their terms are off by 2^-15
+        assert abs((up - down) / (2 * h) - grad[j]) <= h * h / 24 + 2.0 ** -15 / h
 
 
 # ------------------------------------------------------------------------------ weights that are no numbers
