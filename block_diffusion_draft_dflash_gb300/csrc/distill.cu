@@ -3,7 +3,8 @@
 // With e_j = exp((z_j - m) / T), m the row's largest logit, S = sum of e_j over all tokens and R
 // over those outside the teacher's list (t_i, rho):
 //   loss / weight = sum_i t_i (ln t_i - (z_i - m) / T) + sum t ln S + rho (ln rho - ln(R / S))
-//   gradient = weight / T (e_j / S - t_j) in the list, weight / T e_j / R (R / S - rho) outside
+//   gradient = weight / T (e_j / S - t_j) in the list, weight / T e_j / R (R / S - rho) outside,
+//   where sum t + rho = 1 (else e_j / S and R / S are times that)
 // R is summed over the tokens outside (a bit for each token marks the list), not taken as S minus
 // the list's part: where the student is sure of the list, that difference has no digits left.  It is
 // summed relative to the largest logit outside, m', and e_j / R is made from z_j - m' or, from kept
@@ -70,6 +71,7 @@ struct Entries {
   int id[kPer];
   float ln_t[kPer], t[kPer];
   float sum;             // of all t of the list
+  float rho, all;        // what is left for the others, and sum + rho: 1 where lse is the list's
   uint32_t bad;          // of this thread's entries
 
   DF_DEV void load(const DistillArgs& a, const Temper& T, int list, float* tmp) {
@@ -130,6 +132,9 @@ struct Entries {
       s += t[j];
     }
     sum = block_add(s, tmp);
+    if (!(sum < INFINITY)) bad |= 1;
+    rho = a.lse ? fmaxf(1.f - sum, 0.f) : 0.f;
+    all = a.lse && sum > 1.f + 0x1p-20f + 0x1p-23f * fabsf(lse) ? sum : 1.f;    // not what the rounding of lse makes
   }
 };
 
@@ -195,7 +200,7 @@ DF_DEV void write_listed(E* grad, const Entries& en, const float* z, const bool*
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < kPer; ++j)
-    if (mine[j]) RowOf<E>::set(grad, en.id[j], scale * (ex2_approx((z[j] - m) * c) * inv_s - en.t[j]));
+    if (mine[j]) RowOf<E>::set(grad, en.id[j], scale * (ex2_approx((z[j] - m) * c) * inv_s * en.all - en.t[j]));
 }
 
 // grid: rows x CTAs of a row.
@@ -353,7 +358,7 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a, int
   }
   const float to_m = ex2_approx((mr - m) * T.c);     // e_j = exp((z_j - m') / T) times this
   S += R * to_m;
-  const float rho = a.lse ? fmaxf(1.f - en.sum, 0.f) : 0.f;
+  const float rho = en.rho;
   const float weight = a.weight ? a.weight[r] : 1.f;
   if (rank == 0 && tid == 0) {
     const float ln_s = logf(S);
@@ -369,7 +374,7 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillArgs a, int
   }
   if (grad) {
     const float scale = T.over(weight), inv_s = 1.f / S;
-    const float out = scale * (to_m * inv_s - (others ? rho / R : 0.f));
+    const float out = scale * (to_m * inv_s * en.all - (others ? rho / R : 0.f));
     write_pieces<4, true>(part, grad, [&](float* x) {
 #pragma unroll
       for (int e = 0; e < VE; ++e) x[e] = ex2_approx((x[e] - mr) * T.c) * out;
@@ -421,11 +426,11 @@ __global__ void __launch_bounds__(kRowThreads) distill_backward_kernel(DistillAr
     z[j] = mine[j] ? RowOf<E>::value(part.row, en.id[j]) : 0.f;
   }
   __syncthreads();     // an entry's logit is read before it may be written over
-  const float rho = a.lse ? fmaxf(1.f - en.sum, 0.f) : 0.f;
+  const float rho = en.rho;
   const float scale = T.over((a.weight ? a.weight[r] : 1.f) * (a.grad_loss ? a.grad_loss[r] : 1.f));
   const bool others = st.z > -INFINITY;
   // e_j / R (without others e_j), times R / S - rho (1 / S)
-  const float ln_r = others ? st.z : 0.f, out = scale * (expf(ln_r - st.y) - (others ? rho : 0.f));
+  const float ln_r = others ? st.z : 0.f, out = scale * (expf(ln_r - st.y) * en.all - (others ? rho : 0.f));
   const float m = st.x, to = ln_r * 1.44269504f;
   if (ln_r < kFar)
     write_far(part.row, a.x.V, rank, ctas, grad, a.temperature, m, ln_r, st.w, out);

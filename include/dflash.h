@@ -529,6 +529,8 @@ int dflash_top_logits(const df_rows* logits, int K, float temperature, int32_t* 
  *   loss = weight (sum_i t_i (ln t_i - ln q_i) + rho (ln rho - ln sigma))
  *   dloss / dz_j = weight / T (q_j - t_j)              j in the list
  *                  weight / T q_j (1 - rho / sigma)    others (lse NULL: weight / T q_j)
+ * With an lse that is not the list's sum t may be above 1; the loss is what stands here, and its gradient
+ * has q_j sum t in place of q_j where sum t > 1 + 2^-20 + 2^-23 |lse| (what lse's rounding does not explain).
  * Terms with t_i = 0 or rho = 0 are 0.  A student's -inf where the teacher has mass gives an
  * infinite loss (its gradient stays finite; with sigma = 0 < rho there are no others).  Where all of
  * the student's logits outside the list lie more than 2^30 T below its largest one, sigma counts as 0.
@@ -547,7 +549,7 @@ int dflash_top_logits(const df_rows* logits, int K, float temperature, int32_t* 
  *                array (with its ld); behind V it is left as it was
  * A row that does not learn has loss 0, stats 0 and a gradient of zeros.  A row left out has loss
  * and stats NaN and a gradient of zeros: one with a NaN or +inf in it or in its list, with nothing
- * but -inf in it, or without lse in its list (DF_ERR_NAN); with a list outside 0 .. n_teacher - 1,
+ * but -inf in it, or with no finite lse or sum t in its list (DF_ERR_NAN); with a list outside 0 .. n_teacher - 1,
  * an id outside -1 .. V - 1 or one that stands twice in its list (DF_ERR_ARG). */
 size_t dflash_distill_workspace_size(int rows, int V);
 int dflash_distill(const df_rows* student, int K, int n_teacher, const int32_t* id, const float* val,

@@ -209,3 +209,43 @@ def test_the_lowest_number_over_a_small_temperature(dtype, full, V, T):
     ids, vals, lses = lists(y, K, T, V)
     # (fp32 subnormals count as 0 or not: none is among them)
     teach(z, ids, vals, lses if full else None, T, dtype)
+
+
+# ------------------------------------------------------------------------------ a log-sum that is not the list's
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("V", [200, 40000])
+@pytest.mark.parametrize("shift", [-0.5, -3.0, 0.25])
+def test_a_log_sum_of_another_list(dtype, V, shift):
+    """Listed probabilities that sum to more than 1 leave nothing to the others, and the gradient is still the loss's own."""
+    K, n = 9, 4
+    ids, vals, lses = lists(logits(43, n, V).astype(np.float32), K, 1.0, V)
+    teach(logits(44, n, V), ids, vals, lses + shift, 1.0, dtype)
+
+
+def test_gradient_by_differences_of_a_log_sum_of_another_list():
+    V, K, h = 50, 6, 0.0625
+    ids, vals, lses = lists(logits(45, 1, V).astype(np.float32), K, 1.0, V)
+    lses = lses - 1.0
+    z = logits(46, 1, V).astype(np.float32)
+    loss, stats, grad, _ = run_distill(f32(z), ids, vals, lses, 1.0)
+    back, _ = run_backward(f32(z), ids, vals, lses, 1.0, stats)
+    for j in (0, V - 1, int(ids[0, 0]), int(ids[0, 5])):
+        d = np.zeros((1, V), np.float32)
+        d[0, j] = h
+        up, down = (f64(run_distill(f32(z + k * d), ids, vals, lses, 1.0, grad=False)[0])[0] for k in (1, -1))
+        for g in (f64(grad)[0], f64(back)[0]):
+            # up to e in all: e h^2 / 24; losses below 2^5 are off by 2^-18
+            assert abs((up - down) / (2 * h) - g[j]) <= 3 * h * h / 24 + 2.0 ** -18 / h
+
+
+def test_a_log_sum_that_no_list_has():
+    """Probabilities out of fp32's range: the row is left out, with an error."""
+    V, K = 300, 5
+    ids, vals, lses = lists(logits(47, 2, V).astype(np.float32), K, 1.0, V)
+    lses[1] -= 200.0
+    z = held(logits(48, 2, V), "fp32")
+    loss, stats, grad, status = run_distill(z, ids, vals, lses, 1.0)
+    back, _ = run_backward(z, ids, vals, lses, 1.0, stats)
+    assert status == -6 and np.isnan(f64(loss)[1]) and np.isnan(f64(stats)[1]).all() and not grad[1].any() and not back[1].any()
+    check(f64(z)[0], ids[0].cpu().numpy(), f64(vals)[0], float(lses[0]), 1.0, f64(loss)[0], f64(stats)[0],
+          ((f64(grad)[0], False), (f64(back)[0], True)), "fp32")
