@@ -12,7 +12,8 @@
 // for min-p alone (whose bound is known).  For up to 64 tokens and for mass, every CTA of a row
 // bounds and lists its own part, which saves two of the cluster's barriers.
 // Mass alone (top-p, or nothing cut).  The first pass also sums exp((l - max) / T) in fp32, which
-// gives the mass of the tokens that are not listed within 2^-15 of it.  If both ends of that
+// gives the mass of the tokens that are not listed within 2^-15 of it, and half a unit of masses for
+// each of them (a mass is a whole number of units).  If both ends of that
 // interval put the borders on the same tokens of the list, they are right; a sure row's are.
 // Otherwise a pass counts tokens in 2048 bins of 1/64 of a power of two of probability, from which
 // follows where a border should lie; one more pass sums all masses, and those before the bins of
@@ -1096,9 +1097,13 @@ DF_DEV float log_share(const MassScale& c, float l, uint64_t w, uint64_t m) {
   return 0.693147180559945f * (y - log2f((float)m * kMassUnit));
 }
 
+// How far the mass of tokens that are not listed may be from the sum of their probabilities, in units:
+// that sum's own error, and each token's rounding to a whole number.
+DF_DEV uint64_t tail_error(uint64_t tail, int V) { return (tail >> 15) + (uint64_t)V / 2 + 1; }
+
 // The first CTA's end of a row whose first n tokens are on the list, in order.  whole: the kept
 // tokens are among them, all that top-k or min-p left; else the others have about the mass `tail`
-// (within 2^-15 of it) and the row has `live` tokens.  True: done; *about: about the row's mass.
+// (within tail_error) and the row has `live` tokens.  True: done; *about: about the row's mass.
 template <class E, class Give>
 DF_DEV bool finish(RowWork<E>& w, int n, bool whole, uint64_t tail, uint32_t live, float p, uint32_t key_low, float u,
                    bool log, uint64_t* about, Give&& give) {
@@ -1108,11 +1113,12 @@ DF_DEV bool finish(RowWork<E>& w, int n, bool whole, uint64_t tail, uint32_t liv
 #pragma unroll 1
   for (int i = from; i < upto; ++i) mine += s.each_mass[i] = mass_of(w.scale, key_float(key_of(s.list[i])));
   const uint64_t start = block_scan(mine, s.tmp64, &total);
-  uint64_t m_lo = total, m_hi = total;
+  uint64_t m_lo = total, m_hi = total, m_mid = total;
   if (!whole) {
-    m_lo += tail - (tail >> 15);
-    m_hi += tail + (tail >> 15);
-    *about = total + tail;
+    const uint64_t e = tail_error(tail, w.part.V);
+    m_lo += tail - min(tail, e);
+    m_hi += tail + e;
+    *about = m_mid = total + tail;
   }
   uint32_t n_kept = whole ? n : live;
   int room = n;                      // listed tokens that may be drawn
@@ -1132,7 +1138,7 @@ DF_DEV bool finish(RowWork<E>& w, int n, bool whole, uint64_t tail, uint32_t liv
     c = block_add(c, s.tmp32);
     n_kept = room = c & 0xFFFF;
     if (!whole && (room != (int)(c >> 16) || room == n)) return false;
-    m_lo = m_hi = block_add(mine, s.tmp64);
+    m_lo = m_hi = m_mid = block_add(mine, s.tmp64);
   }
   const uint64_t want_lo = mass_above(u, m_lo), want_hi = mass_above(u, m_hi);
   if (w.tid == 0) s.found = 0;
@@ -1144,7 +1150,7 @@ DF_DEV bool finish(RowWork<E>& w, int n, bool whole, uint64_t tail, uint32_t liv
     at += m;
     if (before < want_lo && at >= want_hi) {
       const uint64_t comp = s.list[i];
-      give(id_of(comp), log ? log_share(w.scale, key_float(key_of(comp)), m, (m_lo >> 1) + (m_hi >> 1)) : 0.f, (int32_t)n_kept);
+      give(id_of(comp), log ? log_share(w.scale, key_float(key_of(comp)), m, m_mid) : 0.f, (int32_t)n_kept);
       s.found = 1;
     }
   }
@@ -1168,11 +1174,12 @@ DF_DEV bool finish_few(RowWork<E>& w, int n, bool whole, uint64_t tail, uint32_t
     if (lane >= o) incl += x;
   }
   const uint64_t start = incl - m0 - m1, total = __shfl_sync(0xffffffffu, incl, 31);
-  uint64_t m_lo = total, m_hi = total;
+  uint64_t m_lo = total, m_hi = total, m_mid = total;
   if (!whole) {
-    m_lo += tail - (tail >> 15);
-    m_hi += tail + (tail >> 15);
-    *about = total + tail;
+    const uint64_t e = tail_error(tail, w.part.V);
+    m_lo += tail - min(tail, e);
+    m_hi += tail + e;
+    *about = m_mid = total + tail;
   }
   uint32_t n_kept = whole ? n : live;
   int room = n;
@@ -1184,14 +1191,14 @@ DF_DEV bool finish_few(RowWork<E>& w, int n, bool whole, uint64_t tail, uint32_t
     const uint32_t both = __reduce_add_sync(0xffffffffu, c);
     n_kept = room = both & 0xFFFF;
     if (!whole && (room != (int)(both >> 16) || room == n)) return false;
-    m_lo = m_hi = warp_add((y0 ? m0 : 0) + (y1 ? m1 : 0));
+    m_lo = m_hi = m_mid = warp_add((y0 ? m0 : 0) + (y1 ? m1 : 0));
   }
   const uint64_t want_lo = mass_above(u, m_lo), want_hi = mass_above(u, m_hi);
   const bool at0 = 2 * lane < room && start < want_lo && start + m0 >= want_hi;
   const bool at1 = 2 * lane + 1 < room && start + m0 < want_lo && incl >= want_hi;
   if (at0 || at1) {
     const uint64_t comp = at0 ? e0 : e1;
-    give(id_of(comp), log ? log_share(w.scale, key_float(key_of(comp)), at0 ? m0 : m1, (m_lo >> 1) + (m_hi >> 1)) : 0.f,
+    give(id_of(comp), log ? log_share(w.scale, key_float(key_of(comp)), at0 ? m0 : m1, m_mid) : 0.f,
          (int32_t)n_kept);
   }
   return __any_sync(0xffffffffu, at0 || at1);
