@@ -287,8 +287,10 @@ class SpecDecoder:
 
     def status(self):
         """First device-side error of any call (0 if none); synchronises the stream."""
-        for ws in (self.ws_draft, self.ws_tree, self.ws_verify, self.ws_accept) + ((self.ws_distill,) if self.teach else ()):
-            s = ws.status()
+        # in the calls' order; the prompt pass and the first draft have workspaces of their own
+        for name in ("prefill", "draft0", "draft", "tree", "verify", "accept", "distill"):
+            ws = getattr(self, "ws_" + name, None)
+            s = ws.status() if ws is not None else 0
             if s:
                 return s
         return 0
