@@ -17,7 +17,7 @@ struct SampleArgs {
   const float *temperature, *top_p, *min_p;   // [rows / group], each may be null
   const int32_t* top_k;
   const float* u;                 // [rows], or null:
-  const uint32_t* draw_key;       // [rows] keys of the draws
+  const uint32_t* draw_key;       // [rows] keys of the draws (without logprob and n_kept; see as_unset in sample.cu)
   int32_t* token;                 // [rows]
   float* logprob;                 // [rows], may be null
   int32_t* n_kept;                // [rows], may be null

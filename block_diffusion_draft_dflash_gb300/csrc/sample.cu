@@ -1209,6 +1209,7 @@ struct Settings {
   float T, p, low, u;
   int k;
   bool ok, by_k, by_min, by_mass;
+  bool as_unset;       // nothing is cut, and the draw is keyed: the token of a draw without settings
 
   DF_DEV Settings(const SampleArgs& a, int r) {
     const int g = (a.row0 + r) / a.group;
@@ -1226,6 +1227,7 @@ struct Settings {
     by_k = k > 0 && k <= kMaxTop;
     by_min = k <= 0 && p >= 1.f && low > 0.f;
     by_mass = k <= 0 && !by_min;
+    as_unset = !a.u && by_mass && p >= 1.f && low == 0.f;
   }
 };
 
@@ -1291,6 +1293,42 @@ __device__ __noinline__ void search_row(RowWork<E>& w, const SampleArgs& a, int 
   }
 }
 
+// A keyed draw that no setting cuts: the token that the LM head's own temperature draw gives (the argmax over
+// logit / T + draw_noise(), in the same operations), so that settings which cut nothing change no text.
+template <class E>
+__device__ __noinline__ void draw_uncut(Shared& s, const E* row, int V, uint32_t draw, float T, int32_t* token, int* status, int r,
+                                        int rank, int ctas) {     // values: the kernel's arguments stay where they are
+  if (ctas > 1) cluster_arrive();
+  const RowPart<E> part(row, 0, 0, V, rank, ctas);
+  const float inv_temp = 1.f / T;
+  const int tid = threadIdx.x;
+  uint64_t best = 0;       // 0: no token; all bits: a NaN or +inf
+  for_pieces<2>(part, [&](const float* x, int piece, bool) {
+#pragma unroll
+    for (int e = 0; e < RowPart<E>::VE; ++e) {
+      if (x[e] == -INFINITY) continue;
+      const int id = part.id(piece, e);
+      const float v = __fadd_rn(__fmul_rn(x[e], inv_temp), draw_noise(draw, id));
+      best = max(best, x[e] < INFINITY ? comp_of(float_key(v), id) : ~(uint64_t)0);
+    }
+  });
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+  if ((tid & 31) == 0) s.tmp64[tid >> 5] = best;
+  __syncthreads();
+  if (ctas > 1) cluster_wait();     // every CTA of the cluster runs before its memory is written
+  if (tid == 0) {
+    for (int w = 1; w < kRowWarps; ++w) best = max(best, s.tmp64[w]);
+    st_remote(at_rank(&s.list[rank], 0), best);
+  }
+  row_sync(ctas);
+  if (rank == 0 && tid == 0) {
+    for (int i = 0; i < ctas; ++i) best = max(best, s.list[i]);
+    if (best == ~(uint64_t)0) set_status(status, DF_ERR_NAN, r);
+    *token = best == 0 || best == ~(uint64_t)0 ? -1 : id_of(best);
+  }
+}
+
 // grid: rows x CTAs of a row.  SEARCH: rows that need it are searched here, else left to
 // search_kernel (a.left).
 template <class E, bool SEARCH>
@@ -1311,6 +1349,11 @@ __global__ void __launch_bounds__(kRowThreads, SEARCH ? 2 : 4) sample_kernel(Sam
       give_row(a, r, -1, -INFINITY, 0);
       leave(0, 0, 0);
     }
+    return;
+  }
+  if (st.as_unset) {
+    draw_uncut(s, static_cast<const E*>(a.x.data) + r * a.x.ld, a.x.V, a.draw_key[r], st.T, a.token + r, a.status, r, rank, ctas);
+    if (rank == 0 && tid == 0) leave(0, 0, 0);
     return;
   }
   const RowPart<E> part(static_cast<const E*>(a.x.data), a.x.ld, r, a.x.V, rank, ctas);

@@ -132,6 +132,7 @@ class SpecDecoder:
     replayed ones too.
     teach K: every verification also gives its nodes' first K tokens, and distill() the loss of
     the step's draft against them, at the accepted path's nodes, with its gradient by `logprobs`.
+    Lists alone, and settings that cut nothing, leave the emitted tokens as they are without them.
     """
 
     def __init__(self, target: DeviceModel, drafter: DeviceModel, b: int, B: int, cap: int, prompt_len: int = 0,

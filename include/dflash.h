@@ -574,7 +574,9 @@ int dflash_distill_backward(const df_rows* student, int K, int n_teacher, const 
  *
  * Sequence s draws at position n with u = (23 bits + 1/2) / 2^23, the number that the sampled
  * forward gives token 0 there, so speculative decoding emits the tokens plain decoding emits under
- * the same seed and settings.  Logits (fp32) are made and used in blocks of at most 1024 nodes.
+ * the same seed and settings.  A sequence whose settings cut nothing (top_k <= 0, top_p 1, min_p 0) chooses
+ * as dflash_target_tree_forward_sampled does at its temperature, and at temperature 0 as
+ * dflash_target_tree_forward, so lists alone (K > 0) change no choice.  Logits (fp32) are made and used in blocks of at most 1024 nodes.
  *   temperature, top_k, top_p, min_p   [b] (device) or NULL, as in dflash_sample; a setting outside
  *             its range is recorded and its sequence's choices are -1
  *   K         0: no lists; else 1 .. 1024 with top_temperature (2^-100 .. 2^100),
