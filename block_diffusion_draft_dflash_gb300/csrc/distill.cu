@@ -14,7 +14,7 @@
 // Both passes are bound by the row's bytes: loss reads a row once; with the gradient a row is read
 // again from L2 by the CTAs that just read it, and written.  512 threads a CTA: a list's 1024 entries
 // are two a thread, and a row's CTAs are few.  Measured with rows of 151936 on one GB300, whole calls:
-// 240 rows fp32, loss alone 36 us (4.1 TB/s); 960 rows bf16 with the gradient 132 us (4.4 TB/s of what
+// 240 rows fp32, loss alone 35 us (4.2 TB/s); 960 rows bf16 with the gradient 131 us (4.5 TB/s of what
 // has to move); 960 rows fp32, gradient from kept statistics, 174 us (6.7 TB/s, the copy rate);
 // 15 rows fp32 with the gradient 13 us, of which 11 in a graph.
 #define DF_ROW_THREADS 512

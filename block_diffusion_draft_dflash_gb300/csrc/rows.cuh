@@ -28,11 +28,6 @@ DF_DEV uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-DF_DEV uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
 DF_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 DF_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 // Barrier over the CTAs of a row, with their shared memory.
@@ -302,7 +297,7 @@ struct MassScale {
       ref = rintf(a * 1024.f) * (1.f / 1024.f);
     }
     shift = 12288.f - ref;
-    floor = (ref - 63.75f) / c_hi;     // 2^-63.75 counts as 0 (and is the last of 2048 bins of 1/32)
+    floor = (ref - 63.75f) / c_hi;     // 2^-63.75 counts as 0; bins of 1/64, where they are not cut off, end at 4080
     top = bits(largest);
   }
   DF_DEV float arg(float l) const { return fmaxf(l - base, floor); }

@@ -27,8 +27,8 @@
 //   1 row, fp32                   11 us: the cluster's start and barriers, and one warp's end of the row
 //   16 rows, 20 largest, fp32     12 us: the same
 //   257 rows, top-k 20, fp32      46 us for 156 MB; a kernel that only reads them takes 26, a row's end 8
-//   256 rows, top-p 0.9, bf16     137 to 192 us: 73 of the rows are searched, which reads each twice more
-//                                 with some 25 instructions for a token's exact mass
+//   256 rows, top-p 0.9, bf16     137 to 210 us, by the inputs: 73 of the rows are searched, which reads each
+//                                 twice more with some 25 instructions for a token's exact mass
 //   2064 rows, mixed, bf16        325 us for 627 MB: first pass 191 (3.9 TB/s: four CTAs an SM, and each
 //                                 ends its row without reading), 114 rows searched 135
 //   2048 rows, 256 largest, bf16  243 us for 622 MB, and 288 MB of groups read again
@@ -540,8 +540,8 @@ struct RowWork {
     __syncthreads();
     const float bigf = key_float(s.key_max), to = (float)kBuckets / (bigf - key_float(s.key_min));
     // A list of bf16 logits may have few different ones: these share the buckets, and the tokens of
-    // one are dealt by their ids (2064 mixed rows 325 us, by the logit alone 346; 256 nucleus rows
-    // 154 against 173).
+    // one are dealt by their ids (2064 mixed rows 325 us, by the logit alone 346; 256 nucleus rows of four
+    // inputs 165, 176, 143, 137 against 182, 198, 157, 163).
     const uint32_t levels = ((s.key_max - s.key_min) >> 16) + 1, each = VE == 8 ? kBuckets / levels : 0;
     const float by_id = (float)each / (float)part.V;
     uint64_t e[OWN];
