@@ -72,7 +72,8 @@ def teacher(ids, vals, lse, temperature):
 
 
 def distill(z, ids, vals, lse, temperature, weight=1.0):
-    """(loss, gradient by z, stats) of one student row; `lse` None: the list is all there is."""
+    """(loss, gradient by z, stats) of one student row; `lse` that of the list's own row, None: the list is all there is.
+    Sums are relative to the row's largest logit: what lies 745 temperatures below it is 0 here."""
     z = np.asarray(z, np.float64)
     ids, t, rho = teacher(ids, vals, lse, temperature)
     m = z.max()
